@@ -288,6 +288,103 @@ DA_API int decode_attn_multi_reserve(size_t bytes);
 DA_API int decode_attn_multi_launches(da_shape s, int q_tokens, int ring_window, int max_seq_len);
 
 /*
+ * decode_attn_paged_weights / decode_attn_paged_fp8_weights -- decode_attn_paged and
+ * decode_attn_paged_fp8 that also accumulate how much each cached token is attended, for
+ * kv_evict. (The pages describe nothing like it; a bounded cache is this library's choice.)
+ *   weights  [num_pages, Hkv, page_size] fp32, laid out as the cache's cells. With P the
+ *            step's probabilities (sink in the denominator),
+ *                weights[cell(j), g] += sum over the G query heads h of g of P[h][j]
+ *            for every attended position j; the cell of a token appended by this call is set
+ *            to its sum instead (it held another token's). Other cells are not touched.
+ * Probabilities are formed in fp32 from the fp32 scores (the output's rounding of P to bf16 or
+ * fp16 does not enter). A cell receives one addition per sequence that attends it, so the
+ * result does not depend on any order unless sequences share a page; shared pages are added up
+ * correctly, in no fixed order. Cells of a page outside the pool are skipped
+ * (DA_STATUS_BAD_PAGE). Cells appended by other calls hold whatever they held before: set a
+ * page's weights to zero when it is handed out.
+ * scale must be positive and finite. Workspace: the one-token workspace, and the weights
+ * workspace (decode_attn_weights_workspace_bytes); both grow on first use outside graph
+ * capture, else DA_ERR_WORKSPACE. Results (out, caches), status and errors otherwise as in
+ * decode_attn_paged / decode_attn_paged_fp8; after DA_STATUS_TIMEOUT the weights are garbage
+ * too.
+ */
+DA_API int decode_attn_paged_weights(const void *q, const void *k_new, const void *v_new, void *k_cache,
+                                     void *v_cache, float *weights, const int32_t *block_table,
+                                     const int32_t *seq_lens, const float *sinks, int window, float scale,
+                                     void *out, da_shape s, int page_size, int max_pages_per_seq,
+                                     int num_pages, int max_seq_len, void *stream);
+DA_API int decode_attn_paged_fp8_weights(const void *q, const void *k_new, const void *v_new, void *kv_cache,
+                                         float *weights, const int32_t *block_table,
+                                         const int32_t *seq_lens, const float *sinks, int window,
+                                         float scale, void *out, da_shape s, int page_size,
+                                         int max_pages_per_seq, int num_pages, int max_seq_len,
+                                         void *stream);
+
+/*
+ * decode_attn_paged_multi_weights -- decode_attn_paged_multi that also accumulates the weights,
+ * summed over the new tokens' query rows too: weights[cell(j), g] += sum over t < n and the
+ * query heads of g of P[t][h][j]. The cells of the n new tokens are set to their sums. A prompt
+ * of which only the last tokens' attention is to count goes through decode_attn_paged_multi up
+ * to them and through this call from there. Workspaces: the multi-token one and the weights
+ * one. scale must be positive and finite; everything else as in decode_attn_paged_multi.
+ */
+DA_API int decode_attn_paged_multi_weights(const void *q, const void *k_new, const void *v_new, void *k_cache,
+                                           void *v_cache, float *weights, const int32_t *block_table,
+                                           const int32_t *seq_lens, const int32_t *q_lens,
+                                           const float *sinks, int window, float scale, void *out,
+                                           da_shape s, int q_tokens, int page_size, int max_pages_per_seq,
+                                           int num_pages, int max_seq_len, void *stream);
+
+/*
+ * kv_evict / kv_evict_fp8 -- shrink every sequence of more than `keep` cells to `keep` cells
+ * per KV head, in place. For L = seq_lens[b] > keep and each KV head:
+ *   - the first keep_first and the last keep_last cells stay;
+ *   - of the cells between them the keep - keep_first - keep_last of largest accumulated weight
+ *     stay (equal weights: the lower cell; -0 equals +0; a NaN and a cell of a page outside the
+ *     pool rank below everything);
+ *   - a kept cell below keep - keep_last stays where it is; the other kept cells between the
+ *     first and the last, in order, go into the freed cells, in order; the last keep_last cells
+ *     go to [keep - keep_last, keep), in order.
+ * K, V and weight move together (fp8: the codes and scales as they are). The cells from keep on
+ * hold what they held; the pages past ceil(keep / page_size) are free for reuse. Attention does
+ * not depend on the order of cells without a window; with one it counts cells, and the first
+ * and last cells keep their order among themselves. KV heads keep different tokens. Positions
+ * are the caller's to track (kept says what went where): after an eviction the next token's
+ * position is not new_lens[b], so rotate q and k_new before the call instead of using the
+ * _rope forms.
+ *   seq_lens  [B] int32, lengths before the eviction; 0 = inactive slot
+ *   new_lens  [B] int32, written: min(seq_lens[b], keep); must not overlap seq_lens
+ *   kept      [B, Hkv, keep] int32, written: kept[b][g][i] = the old cell of the token now in
+ *             cell i; a sequence of L <= keep cells has kept[b][g][i] = i for i < L, then -1
+ *   keep >= 1; keep_first, keep_last >= 0; keep_first + keep_last <= keep
+ *   s         batch, num_q_heads = num_kv_heads = Hkv, head_dim
+ * Evicted sequences must not share pages with each other or with sequences that still need
+ * them. A page outside the pool sets DA_STATUS_BAD_PAGE and the moves into or out of it are
+ * skipped; a bad length sets DA_STATUS_BAD_SEQ_LEN and the slot is treated as inactive. One
+ * launch, and the weights workspace (kv_evict_workspace_bytes). Other arguments and errors as
+ * in decode_attn_paged.
+ */
+DA_API int kv_evict(void *k_cache, void *v_cache, float *weights, const int32_t *block_table,
+                    const int32_t *seq_lens, int32_t *new_lens, int32_t *kept, int keep, int keep_first,
+                    int keep_last, da_shape s, int page_size, int max_pages_per_seq, int num_pages,
+                    int max_seq_len, void *stream);
+DA_API int kv_evict_fp8(void *kv_cache, float *weights, const int32_t *block_table, const int32_t *seq_lens,
+                        int32_t *new_lens, int32_t *kept, int keep, int keep_first, int keep_last,
+                        da_shape s, int page_size, int max_pages_per_seq, int num_pages, int max_seq_len,
+                        void *stream);
+
+/* Bytes of the weights workspace: for a call that accumulates weights (q_tokens = 1 for the
+ * one-token calls), and for an eviction to `keep` cells. Zero for invalid arguments. */
+DA_API size_t decode_attn_weights_workspace_bytes(da_shape s, int q_tokens, int max_seq_len);
+DA_API size_t kv_evict_workspace_bytes(da_shape s, int keep);
+/* Grow the weights workspace that calls on `stream` use (the stream's own after
+ * decode_attn_stream_reserve, else the device's) to at least `bytes`; call before capturing.
+ * DA_ERR_WORKSPACE if that would allocate while `stream` is capturing. A buffer that a captured
+ * graph uses is kept when the workspace grows past it (until the process ends, or
+ * decode_attn_stream_release for a stream's own). */
+DA_API int decode_attn_weights_reserve(void *stream, size_t bytes);
+
+/*
  * kv_append -- the append alone: bit-copies k_new/v_new [B, Hkv, D] of every
  * active sequence into the cell of position p = seq_lens[b] - 1.
  * block_table != NULL: paged cache (page_size, max_pages_per_seq, num_pages as

@@ -16,6 +16,7 @@ Tensor layouts (all contiguous, bf16 unless noted):
   block_table       [B, max_pages_per_seq] int32
   seq_lens          [B] int32, length after this step's append (0 = inactive)
   sinks             [Hq] float32, or None
+  weights           [num_pages, Hkv, page_size] float32, accumulated attention weights
 """
 import ctypes
 import os
@@ -34,6 +35,9 @@ __all__ = [
     "decode_attn_paged_fp8_rope", "decode_attn_ring_fp8_rope", "decode_attn_set_early_inputs",
     "decode_attn_stream_reserve", "decode_attn_stream_release",
     "decode_attn_paged_multi_rope", "decode_attn_ring_multi_rope",
+    "decode_attn_paged_weights", "decode_attn_paged_fp8_weights", "decode_attn_paged_multi_weights",
+    "kv_evict", "kv_evict_fp8", "decode_attn_weights_workspace_bytes", "kv_evict_workspace_bytes",
+    "decode_attn_weights_reserve",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -124,7 +128,24 @@ def load_library():
     lib.decode_attn_set_early_inputs.argtypes = [c_int]
     lib.decode_attn_error_string.argtypes = [c_int]
     lib.decode_attn_error_string.restype = ctypes.c_char_p
-    for fn in (lib.decode_attn_paged, lib.decode_attn_ring, lib.kv_append, lib.decode_attn_reserve,
+    lib.decode_attn_paged_weights.argtypes = [vp, vp, vp, vp, vp, f32p, i32p, i32p, f32p, c_int, c_float, vp,
+                                              da_shape, c_int, c_int, c_int, c_int, vp]
+    lib.decode_attn_paged_fp8_weights.argtypes = [vp, vp, vp, vp, f32p, i32p, i32p, f32p, c_int, c_float, vp,
+                                                  da_shape, c_int, c_int, c_int, c_int, vp]
+    lib.decode_attn_paged_multi_weights.argtypes = [vp, vp, vp, vp, vp, f32p, i32p, i32p, i32p, f32p, c_int,
+                                                    c_float, vp, da_shape, c_int, c_int, c_int, c_int, c_int, vp]
+    lib.kv_evict.argtypes = [vp, vp, f32p, i32p, i32p, i32p, i32p, c_int, c_int, c_int, da_shape, c_int, c_int,
+                             c_int, c_int, vp]
+    lib.kv_evict_fp8.argtypes = [vp, f32p, i32p, i32p, i32p, i32p, c_int, c_int, c_int, da_shape, c_int, c_int,
+                                 c_int, c_int, vp]
+    lib.decode_attn_weights_workspace_bytes.argtypes = [da_shape, c_int, c_int]
+    lib.decode_attn_weights_workspace_bytes.restype = ctypes.c_size_t
+    lib.kv_evict_workspace_bytes.argtypes = [da_shape, c_int]
+    lib.kv_evict_workspace_bytes.restype = ctypes.c_size_t
+    lib.decode_attn_weights_reserve.argtypes = [vp, ctypes.c_size_t]
+    for fn in (lib.decode_attn_paged_weights, lib.decode_attn_paged_fp8_weights,
+               lib.decode_attn_paged_multi_weights, lib.kv_evict, lib.kv_evict_fp8,
+               lib.decode_attn_weights_reserve, lib.decode_attn_paged, lib.decode_attn_ring, lib.kv_append, lib.decode_attn_reserve,
                lib.decode_attn_device_status, lib.decode_attn_paged_rope, lib.decode_attn_ring_rope,
                lib.decode_attn_paged_fp8, lib.decode_attn_ring_fp8, lib.decode_attn_paged_multi,
                lib.decode_attn_ring_multi, lib.decode_attn_multi_reserve,
@@ -428,3 +449,135 @@ def decode_attn_test_expire_wait(tile: int):
     """Testing aid: the next one-token attention call gives up at its first worker's tile
     wait number `tile` (after the tile landed) as if the wait had expired; < 0 disarms."""
     _check(load_library().decode_attn_test_expire_wait(int(tile)))
+
+
+def _tensor(name, t, dtype, *shape):
+    """t as the library reads it: of this type and shape, contiguous, on the current device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}, got {t.dtype} "
+                         f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _paged_tensors(bf16_pool, k, v, weights, block_table, seq_lens):
+    """Checked pointers of a paged cache (v None: fp8 blocks), and its sizes."""
+    if k.dim() != (4 if bf16_pool else 3) or block_table.dim() != 2:
+        raise ValueError(f"the cache is {tuple(k.shape)}, the block table {tuple(block_table.shape)}")
+    num_pages, Hkv = k.shape[0], k.shape[1]
+    B, max_pages = block_table.shape
+    if bf16_pool:
+        kp = _tensor("k_cache", k, torch.bfloat16, num_pages, Hkv, 16, 64)
+        vp = _tensor("v_cache", v, torch.bfloat16, num_pages, Hkv, 16, 64)
+    else:
+        kp, vp = _tensor("kv_cache", k, torch.uint8, num_pages, Hkv, FP8_BLOCK_BYTES), None
+    return (kp, vp, _tensor("weights", weights, torch.float32, num_pages, Hkv, 16),
+            _tensor("block_table", block_table, torch.int32, B, max_pages),
+            _tensor("seq_lens", seq_lens, torch.int32, B), B, Hkv, max_pages, num_pages)
+
+
+def _new_tensors(q, k_new, v_new, sinks, out, lead, Hkv):
+    Hq = q.shape[-2]
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new are given together")
+    return (_tensor("q", q, torch.bfloat16, *lead, Hq, 64),
+            None if k_new is None else _tensor("k_new", k_new, torch.bfloat16, *lead, Hkv, 64),
+            None if v_new is None else _tensor("v_new", v_new, torch.bfloat16, *lead, Hkv, 64),
+            None if sinks is None else _tensor("sinks", sinks, torch.float32, Hq),
+            _tensor("out", out, torch.bfloat16, *lead, Hq, 64), Hq)
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream
+
+
+def decode_attn_paged_weights(q, k_new, v_new, k_cache, v_cache, weights, block_table, seq_lens, sinks,
+                              window, scale, out, max_seq_len=None, stream=None):
+    """decode_attn_paged that also adds every attended token's attention weight (its probabilities
+    summed over the query heads of its KV head) to its cell of weights, fp32
+    [num_pages, Hkv, 16]; the appended token's cell is set to its weight."""
+    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(True, k_cache, v_cache, weights, block_table,
+                                                                       seq_lens)
+    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv)
+    _check(load_library().decode_attn_paged_weights(
+        qp, knp, vnp, kp, vp, wp, bp, lp, sp, window, scale, op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
+        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+    return out
+
+
+def decode_attn_paged_fp8_weights(q, k_new, v_new, kv_cache, weights, block_table, seq_lens, sinks, window,
+                                  scale, out, max_seq_len=None, stream=None):
+    """decode_attn_paged_weights over an fp8 cache (kv_cache as in decode_attn_paged_fp8)."""
+    kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(False, kv_cache, None, weights, block_table,
+                                                                      seq_lens)
+    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv)
+    _check(load_library().decode_attn_paged_fp8_weights(
+        qp, knp, vnp, kp, wp, bp, lp, sp, window, scale, op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
+        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+    return out
+
+
+def decode_attn_paged_multi_weights(q, k_new, v_new, k_cache, v_cache, weights, block_table, seq_lens, sinks,
+                                    window, scale, out, q_lens=None, max_seq_len=None, stream=None):
+    """decode_attn_paged_multi that also adds every attended token's attention weight, summed over
+    the new tokens and the query heads of its KV head, to its cell of weights; the new tokens'
+    cells are set to theirs."""
+    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(True, k_cache, v_cache, weights, block_table,
+                                                                       seq_lens)
+    if q.dim() != 4 or k_new is None:
+        raise ValueError("q is [B, T, Hq, 64] and k_new, v_new are required")
+    T = q.shape[1]
+    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B, T), Hkv)
+    _check(load_library().decode_attn_paged_multi_weights(
+        qp, knp, vnp, kp, vp, wp, bp, lp, None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, B), sp,
+        window, scale, op, da_shape(B, Hq, Hkv, 64), T, 16, max_pages, num_pages,
+        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+    return out
+
+
+def kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_lens, kept, keep_first=0, keep_last=0,
+             max_seq_len=None, stream=None):
+    """Shrink every sequence longer than keep = kept.shape[2] cells to keep cells per KV head, in
+    place: the first keep_first and the last keep_last cells stay, and of those between them the
+    ones of the largest accumulated weight. new_lens [B] int32 receives the lengths, kept
+    [B, Hkv, keep] int32 the old cell of each kept cell (-1 beyond a shorter sequence's end)."""
+    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(True, k_cache, v_cache, weights, block_table,
+                                                                       seq_lens)
+    keep = kept.shape[-1]
+    _check(load_library().kv_evict(
+        kp, vp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, B),
+        _tensor("kept", kept, torch.int32, B, Hkv, keep), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
+        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+    return new_lens
+
+
+def kv_evict_fp8(kv_cache, weights, block_table, seq_lens, new_lens, kept, keep_first=0, keep_last=0,
+                 max_seq_len=None, stream=None):
+    """kv_evict over an fp8 cache: codes and scales move as they are."""
+    kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(False, kv_cache, None, weights, block_table,
+                                                                      seq_lens)
+    keep = kept.shape[-1]
+    _check(load_library().kv_evict_fp8(
+        kp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, B),
+        _tensor("kept", kept, torch.int32, B, Hkv, keep), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
+        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+    return new_lens
+
+
+def decode_attn_weights_workspace_bytes(batch, num_q_heads, num_kv_heads, q_tokens=1, max_seq_len=0, head_dim=64):
+    """Bytes of the weights workspace for a call of q_tokens new tokens (1: the one-token calls)."""
+    return int(load_library().decode_attn_weights_workspace_bytes(
+        da_shape(batch, num_q_heads, num_kv_heads, head_dim), int(q_tokens), int(max_seq_len)))
+
+
+def kv_evict_workspace_bytes(batch, num_kv_heads, keep):
+    return int(load_library().kv_evict_workspace_bytes(da_shape(batch, num_kv_heads, num_kv_heads, 64), int(keep)))
+
+
+def decode_attn_weights_reserve(nbytes: int, stream=None):
+    """Grow the weights workspace that calls on `stream` use (the stream's own after
+    decode_attn_stream_reserve, else the device's) to at least nbytes; call before a capture."""
+    _check(load_library().decode_attn_weights_reserve(_raw_stream(stream), int(nbytes)))

@@ -43,6 +43,7 @@
 #include <unordered_map>
 #include <stdint.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 #include <type_traits>
 
@@ -215,6 +216,10 @@ struct Params {
     // shared memory after it, with its query rows and new tokens); 0: every input is read
     // after the wait
     int early;
+    // the calls that also accumulate attention weights (WTS): log2 of every query row's softmax
+    // denominator (sink included) goes to lse[(b Hkv + g) lse_ld + row]
+    float *lse;
+    int lse_ld;
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -572,6 +577,25 @@ __device__ __forceinline__ void state_write_out_mt(SegState<NT> &s, const float 
     }
 }
 
+// log2 of the softmax denominators (sink included, log2 units) of a segment finished by one
+// warp: column c is query row r0 + c, lse_bg its group's rows. A column with no key and no sink
+// (not a query row) gets +inf, so that every weight 2^(s - lse) of it is 0.
+template <int NT>
+__device__ __forceinline__ void state_write_lse(const SegState<NT> &s, const float (&sig)[NT][2], float *lse_bg,
+                                                int rows, int r0, int lane) {
+    if (lane >= 4) return;  // (after state_reduce_l every lane of a column holds the same m and l)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = r0 + n * 8 + 2 * lane + j;
+            if (r >= rows) continue;
+            const float M = fmaxf(s.m[n][j], sig[n][j]);
+            lse_bg[r] = M == -INFINITY ? INFINITY
+                                       : M + log2f(s.l[n][j] * fast_exp2(s.m[n][j] - M) + fast_exp2(sig[n][j] - M));
+        }
+}
+
 // ---- fp8 (e4m3) helpers
 // Four e4m3 codes (bytes 0..3 of w) to two fp16 pairs: bytes 0,1 -> lo, bytes 2,3 -> hi
 // (lower byte to the lower half). Exact: every e4m3 value is an fp16 value.
@@ -650,7 +674,9 @@ struct SmemLayout {
 // sees the positions lo_t .. base + t (base = L - n, lo_t its window start), the n new tokens
 // are appended in the same pass, rows t >= n are zero. With more than 16 rows per KV head the
 // rows are cut into groups of 16 (p.ngrp), one per CTA of a pair that covers the same units.
-template <int NT, bool RING, bool ROPE, bool KV8, int CPS, bool MT = false>
+// WTS: the denominators of the softmax are written too (p.lse), for the kernel that adds up the
+// attention weights after this one.
+template <int NT, bool RING, bool ROPE, bool KV8, int CPS, bool MT = false, bool WTS = false>
 __global__ void __launch_bounds__(kThreads, CPS)
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const Params p) {
@@ -727,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
     if (!early) wait_previous();
 
     const int B = p.B, Hkv = p.Hkv;
+    auto lse_of = [&](int b, int g) { return p.lse + (static_cast<size_t>(b) * Hkv + g) * p.lse_ld; };  // (WTS)
 
     // ---- 1. lengths, validation, prefix of units over sequences
     {
@@ -1551,11 +1578,13 @@ __global__ void __launch_bounds__(kThreads, CPS)
                         float sig[NT][2];
                         sinks_of(sig);
                         state_write_out_mt(st, sig, p.out, sb, sgk, p.T, p.G, p.Hq, nq_seg, r0g, lane);
+                        if constexpr (WTS) state_write_lse(st, sig, lse_of(sb, sgk), p.T * p.G, r0g, lane);
                     } else {
                         float sig[NT][2];
                         sinks_of(sig);
                         state_write_out(st, sig, p.out + (static_cast<size_t>(sb) * p.Hq + sgk * p.G) * kD,
                                         p.G, lane);
+                        if constexpr (WTS) state_write_lse(st, sig, lse_of(sb, sgk), p.G, 0, lane);
                     }
                 }
                 sb = tb; sgk = tg;
@@ -1746,10 +1775,12 @@ __global__ void __launch_bounds__(kThreads, CPS)
             float sig[NT][2];
             sinks_of(sig);
             state_write_out_mt(st, sig, p.out, sb, sgk, p.T, p.G, p.Hq, nq_seg, r0g, lane);
+            if constexpr (WTS) state_write_lse(st, sig, lse_of(sb, sgk), p.T * p.G, r0g, lane);
         } else {
             float sig[NT][2];
             sinks_of(sig);
             state_write_out(st, sig, p.out + (static_cast<size_t>(sb) * p.Hq + sgk * p.G) * kD, p.G, lane);
+            if constexpr (WTS) state_write_lse(st, sig, lse_of(sb, sgk), p.G, 0, lane);
         }
         // partial states -> this warp's (drained) buffer area
         Slot<NT> *slot0 = reinterpret_cast<Slot<NT> *>(wbase);
@@ -1857,6 +1888,8 @@ __global__ void __launch_bounds__(kThreads, CPS)
                         const float Mf = fmaxf(M, sg);
                         const float r = M == -INFINITY ? 0.f : fast_exp2(M - Mf);
                         den = den * r + (sg == -INFINITY ? 0.f : fast_exp2(sg - Mf));
+                        if (WTS && d0 == 0 && rn < qrows)
+                            lse_of(b, g)[rn] = Mf == -INFINITY ? INFINITY : Mf + log2f(den);
                         if (rn < qrows) {
                             const int t = MT ? rn / p.G : 0, h = MT ? rn - t * p.G : rn;
                             const float inv = (MT && t >= s_n[b]) ? 0.f : r / den;  // no query token: zeros
@@ -1976,6 +2009,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
         const float Mf = fmaxf(M, sg);
         const float a = M == -INFINITY ? 0.f : fast_exp2(M - Mf);
         den = den * a + (sg == -INFINITY ? 0.f : fast_exp2(sg - Mf));
+        if (WTS && cd0 == 0 && rc < qrows) lse_of(b, g)[rc] = Mf == -INFINITY ? INFINITY : Mf + log2f(den);
         const int ct = MT ? rc / p.G : 0, ch = MT ? rc - ct * p.G : rc;
         const float f = (den > 0.f && !(MT && ct >= s_n[b])) ? a / den : 0.f;  // no query token: zeros
         if (rc < qrows) {
@@ -2032,6 +2066,10 @@ __global__ void kv_append_kernel(const __nv_bfloat16 *__restrict__ k_new,
 // ------------------------------------------------------------------ several query tokens
 #include "multi_attn.cuh"
 #include "multi_tc.cuh"
+
+// ------------------------------------------------------------------ accumulated weights, eviction
+#include "weights.cuh"
+#include "evict.cuh"
 
 // ------------------------------------------------------------------ host side
 thread_local char t_err[256];
@@ -2115,21 +2153,36 @@ bool make_kv_map(CUtensorMap *map, void *base, uint64_t rows, uint64_t slices, i
 
 constexpr int kMaxDevices = 64;
 
-// A zeroed device buffer that only grows (its arrival counters are zero at rest).
+// A zeroed device buffer that only grows (its arrival counters are zero at rest). A buffer that
+// a captured graph holds (in_graph) is kept when it is outgrown, so that the graph can still
+// be launched.
 struct Workspace {
     void *p = nullptr;
     size_t bytes = 0;
+    bool in_graph = false;
+    struct Kept {
+        void *p;
+        Kept *next;
+    } *kept = nullptr;  // outgrown buffers that captured graphs hold
+};
+
+// The workspaces of a device or of a stream.
+enum WorkspaceKind {
+    kWsDecode,   // one-token calls: counters + CTA partials
+    kWsMulti,    // multi-token calls: counters + split partials
+    kWsWeights,  // calls that accumulate weights (denominators, scores), evictions (move lists)
+    kWsKinds
 };
 
 // Per-device state. The workspace pointers change only under g_mu; the SM count and the
 // "kernel attribute set" flags are caches that several host threads may fill at once (with
 // the same values), so they are atomics.
 struct DeviceState {
-    Workspace ws;        // one-token calls: counters + CTA partials
-    Workspace ws_multi;  // multi-token calls: counters + split partials
+    Workspace ws[kWsKinds];
     std::atomic<int> sm_count{0};
-    std::atomic<bool> attr_set[64] = {};
+    std::atomic<bool> attr_set[128] = {};
     std::atomic<bool> multi_attr_set[8] = {};
+    std::atomic<bool> evict_attr_set[2] = {};
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -2139,7 +2192,7 @@ std::mutex g_mu;
 // there are none.
 struct StreamWorkspaces {
     int dev;
-    Workspace ws, ws_multi;
+    Workspace ws[kWsKinds];
 };
 std::unordered_map<cudaStream_t, StreamWorkspaces> g_stream_ws;
 std::atomic<int> g_n_stream_ws{0};
@@ -2175,7 +2228,16 @@ size_t workspace_for(int G, int sms) {
 // Grow w to at least `bytes` (synchronous: the old buffer is freed, the new one zeroed).
 int grow_locked(Workspace &w, size_t bytes) {
     if (w.bytes >= bytes) return DA_OK;
-    if (w.p) {
+    if (w.p && w.in_graph) {
+        Workspace::Kept *k = static_cast<Workspace::Kept *>(malloc(sizeof(Workspace::Kept)));
+        if (k == nullptr) return DA_ERR_WORKSPACE;
+        k->p = w.p;
+        k->next = w.kept;
+        w.kept = k;
+        w.p = nullptr;
+        w.bytes = 0;
+        w.in_graph = false;
+    } else if (w.p) {
         cudaError_t e = cudaFree(w.p);
         w.p = nullptr;
         w.bytes = 0;
@@ -2195,14 +2257,15 @@ int grow_locked(Workspace &w, size_t bytes) {
 }
 
 // The workspace a call on `stream` uses (the stream's own if it has one, else the
-// device's), grown to `need` unless the stream is capturing. Under g_mu.
-int workspace_locked(int dev, cudaStream_t stream, bool multi, size_t need, void **ptr) {
-    Workspace *w = multi ? &g_dev[dev].ws_multi : &g_dev[dev].ws;
+// device's), grown to `need` unless the stream is capturing. Under g_mu. captured: the stream
+// is known to be capturing, the buffer goes into a graph.
+int workspace_locked(int dev, cudaStream_t stream, WorkspaceKind kind, size_t need, void **ptr, bool captured = false) {
+    Workspace *w = &g_dev[dev].ws[kind];
     if (g_n_stream_ws.load(std::memory_order_relaxed) > 0) {
         auto it = g_stream_ws.find(stream);
         if (it != g_stream_ws.end()) {
             if (it->second.dev != dev) return DA_ERR_INVALID_ARG;  // the stream is another device's
-            w = multi ? &it->second.ws_multi : &it->second.ws;
+            w = &it->second.ws[kind];
         }
     }
     if (w->bytes < need) {
@@ -2213,6 +2276,7 @@ int workspace_locked(int dev, cudaStream_t stream, bool multi, size_t need, void
         int rc = grow_locked(*w, need);
         if (rc != DA_OK) return rc;
     }
+    if (captured) w->in_graph = true;
     *ptr = w->p;
     return DA_OK;
 }
@@ -2230,14 +2294,14 @@ int check_shape(const da_shape &s) {
     return DA_OK;
 }
 
-template <int NT, bool RING, bool ROPE, bool KV8 = false, int CPS = 1, bool MT = false>
+template <int NT, bool RING, bool ROPE, bool KV8 = false, int CPS = 1, bool MT = false, bool WTS = false>
 int launch_attn(const CUtensorMap &mk, const CUtensorMap &mv, const Params &prm, int dev, cudaStream_t stream) {
     if (sm_count(dev) > kMaxSms) return DA_ERR_UNSUPPORTED;  // the kernel keeps a boundary per CTA
     static_assert(CPS == 1 || (KV8 && NT == 1), "two CTAs per SM: fp8 kernel with 8-head groups only");
     const size_t smem = SmemLayout<NT, ROPE, KV8, CPS, MT>::bytes;
     const size_t smem_max = smem;
-    auto kern = decode_attn_kernel<NT, RING, ROPE, KV8, CPS, MT>;
-    const int idx = (MT ? 32 : 0) + (CPS - 1) * 16 + (NT - 1) * 8 + (RING ? 4 : 0) + (ROPE ? 2 : 0) + (KV8 ? 1 : 0);
+    auto kern = decode_attn_kernel<NT, RING, ROPE, KV8, CPS, MT, WTS>;
+    const int idx = (WTS ? 64 : 0) + (MT ? 32 : 0) + (CPS - 1) * 16 + (NT - 1) * 8 + (RING ? 4 : 0) + (ROPE ? 2 : 0) + (KV8 ? 1 : 0);
     if (!g_dev[dev].attr_set[idx].load(std::memory_order_acquire)) {
         cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_max));
@@ -2264,12 +2328,12 @@ int launch_attn(const CUtensorMap &mk, const CUtensorMap &mv, const Params &prm,
     return DA_OK;
 }
 
-int prepare_workspace(int dev, int G, cudaStream_t stream, float **part, int **counters) {
+int prepare_workspace(int dev, int G, cudaStream_t stream, float **part, int **counters, bool captured = false) {
     const size_t need = workspace_for(G, sm_count(dev));
     void *ws = nullptr;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        int rc = workspace_locked(dev, stream, false, need, &ws);
+        int rc = workspace_locked(dev, stream, kWsDecode, need, &ws, captured);
         if (rc != DA_OK) return rc;
     }
     *counters = static_cast<int *>(ws);
@@ -2283,11 +2347,20 @@ std::atomic<int> g_expire_next{-1};
 // decode_attn_set_early_inputs: what is read before the wait for the previous kernel
 std::atomic<int> g_early_inputs{0};
 
+// What a call that accumulates attention weights adds to the attention it runs: where the
+// denominators go, and whether the stream is capturing a graph.
+struct WeightsOut {
+    float *lse;
+    int lse_ld;
+    bool captured;
+};
+
 int run_attention(bool ring, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                   const int32_t *block_table, const int32_t *seq_lens, const float *sinks, int window,
                   float scale, void *out, const da_shape &s, int page_size, int max_pages, int num_pages,
                   int max_seq_len, void *stream_v, const float *rope_cos = nullptr,
-                  const float *rope_sin = nullptr, int max_position = 0, bool kv8 = false) {
+                  const float *rope_sin = nullptr, int max_position = 0, bool kv8 = false,
+                  const WeightsOut *wts = nullptr) {
     int rc = check_shape(s);
     if (rc != DA_OK) return rc;
     if (!q || !k_cache || (!kv8 && !v_cache) || !seq_lens || !out) return DA_ERR_INVALID_ARG;
@@ -2343,7 +2416,9 @@ int run_attention(bool ring, const void *q, const void *k_new, const void *v_new
     prm.expire_at = g_expire_next.exchange(-1);
     prm.head_scratch = nullptr;
     prm.early = g_early_inputs.load();
-    rc = prepare_workspace(dev, G, stream, &prm.part, &prm.counters);
+    prm.lse = wts ? wts->lse : nullptr;
+    prm.lse_ld = wts ? wts->lse_ld : 0;
+    rc = prepare_workspace(dev, G, stream, &prm.part, &prm.counters, wts != nullptr && wts->captured);
     if (rc != DA_OK) return rc;
 
     CUtensorMap mk, mv;
@@ -2370,6 +2445,9 @@ int run_attention(bool ring, const void *q, const void *k_new, const void *v_new
                 per_seq = (span + kPage - 1) / kPage + 1;
             }
             const bool two = static_cast<long long>(s.batch) * s.num_kv_heads * per_seq >= DA_FP8_2CTA_MIN_TILES;
+            if (wts)
+                return two ? launch_attn<1, false, false, true, 2, false, true>(mk, mv, prm, dev, stream)
+                           : launch_attn<1, false, false, true, 1, false, true>(mk, mv, prm, dev, stream);
             if (rope_cos != nullptr) {
                 if (two)
                     return ring ? launch_attn<1, true, true, true, 2>(mk, mv, prm, dev, stream)
@@ -2383,12 +2461,16 @@ int run_attention(bool ring, const void *q, const void *k_new, const void *v_new
             return ring ? launch_attn<1, true, false, true>(mk, mv, prm, dev, stream)
                         : launch_attn<1, false, false, true>(mk, mv, prm, dev, stream);
         }
+        if (wts) return launch_attn<2, false, false, true, 1, false, true>(mk, mv, prm, dev, stream);
         if (rope_cos != nullptr)
             return ring ? launch_attn<2, true, true, true>(mk, mv, prm, dev, stream)
                         : launch_attn<2, false, true, true>(mk, mv, prm, dev, stream);
         return ring ? launch_attn<2, true, false, true>(mk, mv, prm, dev, stream)
                     : launch_attn<2, false, false, true>(mk, mv, prm, dev, stream);
     }
+    if (wts)
+        return G <= 8 ? launch_attn<1, false, false, false, 1, false, true>(mk, mv, prm, dev, stream)
+                      : launch_attn<2, false, false, false, 1, false, true>(mk, mv, prm, dev, stream);
     if (rope_cos != nullptr) {
         if (G <= 8)
             return ring ? launch_attn<1, true, true>(mk, mv, prm, dev, stream)
@@ -2562,7 +2644,7 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
               const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens, const float *sinks,
               int window, float scale, void *out, const da_shape &s, int T, int page_size, int max_pages,
               int num_pages, int max_seq_len, void *stream_v, const float *rope_cos = nullptr,
-              const float *rope_sin = nullptr, int max_position = 0) {
+              const float *rope_sin = nullptr, int max_position = 0, const WeightsOut *wts = nullptr) {
     int rc = check_shape(s);
     if (rc != DA_OK) return rc;
     if (!q || !k_new || !v_new || !k_cache || !v_cache || !seq_lens || !out) return DA_ERR_INVALID_ARG;
@@ -2595,8 +2677,9 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
     const size_t rope_off = (m.counter_bytes + m.part_bytes + 255) & ~static_cast<size_t>(255);
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        rc = workspace_locked(dev, stream, true, rope ? rope_off + rope_scratch_bytes(s, T) : m.counter_bytes + m.part_bytes,
-                              &ws);
+        rc = workspace_locked(dev, stream, kWsMulti,
+                              rope ? rope_off + rope_scratch_bytes(s, T) : m.counter_bytes + m.part_bytes, &ws,
+                              wts != nullptr && wts->captured);
         if (rc != DA_OK) return rc;
     }
     if (rope) {  // rotate q and k_new into the workspace; the attention reads them from there
@@ -2641,12 +2724,18 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         dp.expire_at = -1;
         dp.head_scratch = m.rows == 32 ? dp.part + static_cast<size_t>(sm_count(dev)) * 2 * slot_floats(m.rows) : nullptr;
         dp.early = g_early_inputs.load();
+        dp.lse = wts ? wts->lse : nullptr;
+        dp.lse_ld = wts ? wts->lse_ld : 0;
         CUtensorMap mk, mv;
         const uint64_t slices = static_cast<uint64_t>(num_pages) * s.num_kv_heads;
         if (!make_kv_map(&mk, k_cache, kPage, slices) || !make_kv_map(&mv, v_cache, kPage, slices)) {
             snprintf(t_err, sizeof t_err, "CUDA error: tensor map encoding failed");
             return DA_ERR_CUDA;
         }
+        if (wts)
+            return m.rows == 8    ? launch_attn<1, false, false, false, 1, true, true>(mk, mv, dp, dev, stream)
+                   : m.rows == 16 ? launch_attn<2, false, false, false, 1, true, true>(mk, mv, dp, dev, stream)
+                                  : launch_attn<4, false, false, false, 1, true, true>(mk, mv, dp, dev, stream);
         return m.rows == 8    ? launch_attn<1, false, false, false, 1, true>(mk, mv, dp, dev, stream)
                : m.rows == 16 ? launch_attn<2, false, false, false, 1, true>(mk, mv, dp, dev, stream)
                               : launch_attn<4, false, false, false, 1, true>(mk, mv, dp, dev, stream);
@@ -2676,6 +2765,8 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
     prm.counters = static_cast<int *>(ws);
     prm.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
     prm.defer = m.defer ? 1 : 0;
+    prm.lse = wts ? wts->lse : nullptr;
+    prm.lse_ld = wts ? wts->lse_ld : 0;
 
     CUtensorMap mk, mv, nk, nv;
     const uint64_t rows = ring ? static_cast<uint64_t>(window) : static_cast<uint64_t>(kPage);
@@ -2734,6 +2825,175 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         ring ? nullptr : block_table, seq_lens, q_lens, T, s.num_kv_heads, ring ? window : 0, prm.max_pages,
         prm.num_pages, prm.max_seq_len);
     e = cudaGetLastError();
+    return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+}
+
+// ------------------------------------------------------------------ accumulated weights: host side
+// Rows of a (sequence, KV head)'s denominators in the workspace, a multiple of 4 (16 bytes).
+int lse_rows(const da_shape &s, int T) { return (T * (s.num_q_heads / s.num_kv_heads) + 3) & ~3; }
+
+size_t weights_bytes(const da_shape &s, int T) {
+    return static_cast<size_t>(s.batch) * s.num_kv_heads * lse_rows(s, T) * sizeof(float);
+}
+
+// The weights workspace of a call on `stream`; *captured: the stream is capturing a graph.
+int prepare_weights(int dev, cudaStream_t stream, size_t need, void **ws, bool *captured) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &cs);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    *captured = cs != cudaStreamCaptureStatusNone;
+    std::lock_guard<std::mutex> lk(g_mu);
+    return workspace_locked(dev, stream, kWsWeights, need, ws, *captured);
+}
+
+// One step of attention (T = 0: one token per sequence; else T, with q_lens) over a paged cache
+// that also adds every attended cell's attention weight to `weights`.
+int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                float *weights, const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                const float *sinks, int window, float scale, void *out, const da_shape &s, int T, int page_size,
+                int max_pages, int num_pages, int max_seq_len, void *stream_v) {
+    int rc = check_shape(s);
+    if (rc != DA_OK) return rc;
+    if (!weights || !aligned16(weights) || T < 0 || !(scale > 0.f) || !(scale < INFINITY)) return DA_ERR_INVALID_ARG;
+    if (T > kMMaxTokens) return DA_ERR_UNSUPPORTED;
+    const int rows_t = T > 0 ? T : 1;
+    WeightsOut wo{nullptr, lse_rows(s, rows_t), false};
+    int dev = 0;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    // Everything else is checked by the attention call itself, which comes first: with no
+    // workspace yet it is asked for an empty batch, which launches nothing.
+    auto attention = [&](const da_shape &sh, const WeightsOut *w) {
+        return T > 0 ? run_multi(false, q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, q_lens, sinks, window,
+                                 scale, out, sh, T, page_size, max_pages, num_pages, max_seq_len, stream_v, nullptr,
+                                 nullptr, 0, w)
+                     : run_attention(false, q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, sinks, window, scale,
+                                     out, sh, page_size, max_pages, num_pages, max_seq_len, stream_v, nullptr, nullptr, 0,
+                                     kv8, w);
+    };
+    rc = attention(da_shape{0, s.num_q_heads, s.num_kv_heads, s.head_dim}, nullptr);
+    if (rc != DA_OK || s.batch == 0) return rc;
+    rc = current_device(&dev);
+    if (rc != DA_OK) return rc;
+    void *ws = nullptr;
+    rc = prepare_weights(dev, stream, weights_bytes(s, rows_t), &ws, &wo.captured);
+    if (rc != DA_OK) return rc;
+    wo.lse = static_cast<float *>(ws);
+    rc = attention(s, &wo);
+    if (rc != DA_OK) return rc;
+
+    WeightParams p;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.weights = weights;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.q_lens = q_lens;
+    p.lse = wo.lse;
+    p.lse_ld = wo.lse_ld;
+    p.scale_log2 = scale * kLog2e;
+    p.B = s.batch;
+    p.Hq = s.num_q_heads;
+    p.Hkv = s.num_kv_heads;
+    p.G = s.num_q_heads / s.num_kv_heads;
+    p.T = rows_t;
+    p.window = window;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.max_seq_len = max_seq_len;
+    p.assign_new = k_new != nullptr ? 1 : 0;
+    if (max_seq_len == 0) return DA_OK;
+    const int span = window > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(window) + rows_t - 1 + kPage) : max_seq_len;
+    const int tiles = (span + kPage - 1) / kPage + 1;
+    const dim3 grid((tiles + 7) / 8, s.num_kv_heads, s.batch);
+    if (kv8)
+        weights_plain_kernel<true><<<grid, 256, 0, stream>>>(p);
+    else
+        weights_plain_kernel<false><<<grid, 256, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+}
+
+// ------------------------------------------------------------------ eviction: host side
+size_t evict_bytes(const da_shape &s, int keep) {
+    return static_cast<size_t>(s.batch) * s.num_kv_heads * keep * 2 * sizeof(int2);
+}
+
+bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return x < y + nb && y < x + na;
+}
+
+int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int32_t *block_table,
+              const int32_t *seq_lens, int32_t *new_lens, int32_t *kept, int keep, int keep_first, int keep_last,
+              const da_shape &s, int page_size, int max_pages, int num_pages, int max_seq_len, void *stream_v) {
+    int rc = check_shape(s);
+    if (rc != DA_OK) return rc;
+    if (!k_cache || (!kv8 && !v_cache) || !weights || !block_table || !seq_lens || !new_lens || !kept)
+        return DA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || (!kv8 && !aligned16(v_cache)) || !aligned16(weights)) return DA_ERR_INVALID_ARG;
+    if (keep <= 0 || keep_first < 0 || keep_last < 0 || keep_first > keep || keep_last > keep - keep_first)
+        return DA_ERR_INVALID_ARG;
+    if (max_pages <= 0 || num_pages <= 0 || max_seq_len < 0) return DA_ERR_INVALID_ARG;
+    if (page_size != kPage) return DA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(max_pages) * kPage < max_seq_len) return DA_ERR_INVALID_ARG;
+    if (static_cast<long long>(num_pages) * s.num_kv_heads > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+    if (s.batch == 0) return DA_OK;
+    // the lengths are read by every KV head's CTAs while one of them writes the new ones
+    if (overlaps(seq_lens, s.batch * sizeof(int32_t), new_lens, s.batch * sizeof(int32_t))) return DA_ERR_INVALID_ARG;
+    int dev;
+    rc = current_device(&dev);
+    if (rc != DA_OK) return rc;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    void *ws = nullptr;
+    bool captured;
+    rc = prepare_weights(dev, stream, evict_bytes(s, keep), &ws, &captured);
+    if (rc != DA_OK) return rc;
+
+    EvictParams p;
+    p.k_cache = static_cast<uint8_t *>(k_cache);
+    p.v_cache = static_cast<uint8_t *>(v_cache);
+    p.weights = weights;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.new_lens = new_lens;
+    p.kept = kept;
+    p.lists = static_cast<int2 *>(ws);
+    p.Hkv = s.num_kv_heads;
+    p.keep = keep;
+    p.first = keep_first;
+    p.last = keep_last;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.max_seq_len = max_seq_len;
+    // CTAs per (sequence, KV head): as many as fill the GPU's SMs twice, each with at least a
+    // chunk of cells per warp
+    const int pairs = s.batch * s.num_kv_heads;
+    int C = 1;
+    while (C < kEvMaxCluster && 2 * C * pairs <= 2 * sm_count(dev) && 2 * C * kEvThreads <= max_seq_len) C *= 2;
+    const int chunks = (max_seq_len + 31) / 32, cpw = (chunks + C * kEvWarps - 1) / (C * kEvWarps);
+    p.key_cap = std::min<long long>(static_cast<long long>(kEvThreads) * std::max(cpw, 1), kEvMaxKeys);
+    auto kern = kv8 ? kv_evict_kernel<true> : kv_evict_kernel<false>;
+    if (!g_dev[dev].evict_attr_set[kv8].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvMaxKeys * 4);
+        if (e != cudaSuccess) return set_cuda_error(e);
+        g_dev[dev].evict_attr_set[kv8].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C, s.num_kv_heads, s.batch);
+    cfg.blockDim = dim3(kEvThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.key_cap) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? DA_OK : set_cuda_error(e);
 }
 
@@ -2831,6 +3091,8 @@ int run_paged_noalloc(const void *q, const void *k_new, const void *v_new, void 
     prm.expire_at = -1;
     prm.head_scratch = nullptr;
     prm.early = g_early_inputs.load();
+    prm.lse = nullptr;
+    prm.lse_ld = 0;
     prm.counters = static_cast<int *>(scratch);
     prm.part = reinterpret_cast<float *>(static_cast<char *>(scratch) + kNoAllocCounterBytes);
     // The array keeps whatever the previous call left: the arrival counters this call
@@ -2926,6 +3188,65 @@ int decode_attn_ring_fp8_rope(const void *q, const void *k_new, const void *v_ne
                          s, kPage, 0, 0, 0, stream, rope_cos, rope_sin, max_position, true);
 }
 
+int decode_attn_paged_weights(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                              float *weights, const int32_t *block_table, const int32_t *seq_lens, const float *sinks,
+                              int window, float scale, void *out, da_shape s, int page_size, int max_pages_per_seq,
+                              int num_pages, int max_seq_len, void *stream) {
+    return run_weights(false, q, k_new, v_new, k_cache, v_cache, weights, block_table, seq_lens, nullptr, sinks, window,
+                       scale, out, s, 0, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+int decode_attn_paged_fp8_weights(const void *q, const void *k_new, const void *v_new, void *kv_cache, float *weights,
+                                  const int32_t *block_table, const int32_t *seq_lens, const float *sinks, int window,
+                                  float scale, void *out, da_shape s, int page_size, int max_pages_per_seq,
+                                  int num_pages, int max_seq_len, void *stream) {
+    return run_weights(true, q, k_new, v_new, kv_cache, nullptr, weights, block_table, seq_lens, nullptr, sinks, window,
+                       scale, out, s, 0, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+int decode_attn_paged_multi_weights(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                                    float *weights, const int32_t *block_table, const int32_t *seq_lens,
+                                    const int32_t *q_lens, const float *sinks, int window, float scale, void *out,
+                                    da_shape s, int q_tokens, int page_size, int max_pages_per_seq, int num_pages,
+                                    int max_seq_len, void *stream) {
+    if (q_tokens <= 0) return DA_ERR_INVALID_ARG;
+    return run_weights(false, q, k_new, v_new, k_cache, v_cache, weights, block_table, seq_lens, q_lens, sinks, window,
+                       scale, out, s, q_tokens, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+int kv_evict(void *k_cache, void *v_cache, float *weights, const int32_t *block_table, const int32_t *seq_lens,
+             int32_t *new_lens, int32_t *kept, int keep, int keep_first, int keep_last, da_shape s, int page_size,
+             int max_pages_per_seq, int num_pages, int max_seq_len, void *stream) {
+    return run_evict(false, k_cache, v_cache, weights, block_table, seq_lens, new_lens, kept, keep, keep_first, keep_last,
+                     s, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+int kv_evict_fp8(void *kv_cache, float *weights, const int32_t *block_table, const int32_t *seq_lens,
+                 int32_t *new_lens, int32_t *kept, int keep, int keep_first, int keep_last, da_shape s, int page_size,
+                 int max_pages_per_seq, int num_pages, int max_seq_len, void *stream) {
+    return run_evict(true, kv_cache, nullptr, weights, block_table, seq_lens, new_lens, kept, keep, keep_first, keep_last,
+                     s, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+size_t decode_attn_weights_workspace_bytes(da_shape s, int q_tokens, int max_seq_len) {
+    if (check_shape(s) != DA_OK || q_tokens <= 0 || q_tokens > kMMaxTokens || max_seq_len < 0) return 0;
+    return weights_bytes(s, q_tokens);
+}
+
+size_t kv_evict_workspace_bytes(da_shape s, int keep) {
+    if (check_shape(s) != DA_OK || keep <= 0) return 0;
+    return evict_bytes(s, keep);
+}
+
+int decode_attn_weights_reserve(void *stream_v, size_t bytes) {
+    int dev;
+    int rc = current_device(&dev);
+    if (rc != DA_OK) return rc;
+    void *ws;
+    std::lock_guard<std::mutex> lk(g_mu);
+    return workspace_locked(dev, static_cast<cudaStream_t>(stream_v), kWsWeights, bytes, &ws);
+}
+
 int kv_append(const void *k_new, const void *v_new, void *k_cache, void *v_cache, const int32_t *block_table,
               const int32_t *seq_lens, int window, da_shape s, int page_size, int max_pages_per_seq, int num_pages,
               void *stream) {
@@ -3017,7 +3338,7 @@ int decode_attn_multi_reserve(size_t bytes) {
     int rc = current_device(&dev);
     if (rc != DA_OK) return rc;
     std::lock_guard<std::mutex> lk(g_mu);
-    return grow_locked(g_dev[dev].ws_multi, bytes);
+    return grow_locked(g_dev[dev].ws[kWsMulti], bytes);
 }
 
 size_t decode_attn_workspace_bytes(da_shape s, int max_seq_len) {
@@ -3033,7 +3354,7 @@ int decode_attn_reserve(size_t bytes) {
     int rc = current_device(&dev);
     if (rc != DA_OK) return rc;
     std::lock_guard<std::mutex> lk(g_mu);
-    return grow_locked(g_dev[dev].ws, bytes);
+    return grow_locked(g_dev[dev].ws[kWsDecode], bytes);
 }
 
 int decode_attn_stream_reserve(void *stream_v, size_t bytes, size_t multi_bytes) {
@@ -3048,13 +3369,13 @@ int decode_attn_stream_reserve(void *stream_v, size_t bytes, size_t multi_bytes)
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_stream_ws.find(stream);
     if (it == g_stream_ws.end()) {
-        it = g_stream_ws.emplace(stream, StreamWorkspaces{dev, {}, {}}).first;
+        it = g_stream_ws.emplace(stream, StreamWorkspaces{dev, {}}).first;
         g_n_stream_ws.fetch_add(1, std::memory_order_relaxed);
     } else if (it->second.dev != dev) {
         return DA_ERR_INVALID_ARG;
     }
-    rc = grow_locked(it->second.ws, bytes);
-    if (rc == DA_OK) rc = grow_locked(it->second.ws_multi, multi_bytes);
+    rc = grow_locked(it->second.ws[kWsDecode], bytes);
+    if (rc == DA_OK) rc = grow_locked(it->second.ws[kWsMulti], multi_bytes);
     return rc;
 }
 
@@ -3071,11 +3392,17 @@ int decode_attn_stream_release(void *stream_v) {
     e = cudaGetDevice(&prev);
     if (e == cudaSuccess && prev != it->second.dev) e = cudaSetDevice(it->second.dev);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);  // its calls are done with them
-    for (Workspace *w : {&it->second.ws, &it->second.ws_multi}) {
-        if (e == cudaSuccess && w->p) {
-            e = cudaFree(w->p);
-            w->p = nullptr;
-            w->bytes = 0;
+    for (Workspace &w : it->second.ws) {
+        if (e == cudaSuccess && w.p) {
+            e = cudaFree(w.p);
+            w.p = nullptr;
+            w.bytes = 0;
+        }
+        while (e == cudaSuccess && w.kept) {
+            Workspace::Kept *k = w.kept;
+            e = cudaFree(k->p);
+            w.kept = k->next;
+            free(k);
         }
     }
     if (prev >= 0 && prev != it->second.dev) cudaSetDevice(prev);

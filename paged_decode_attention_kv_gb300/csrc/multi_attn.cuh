@@ -76,7 +76,14 @@ struct MultiParams {
     float *part;                    // [B * Hkv * row_blocks][splits][rows per CTA][kMSlotFloats]
     int *counters;                  // [B * Hkv * row_blocks], zero at rest
     int defer;                      // 1: the split partials are left for multi_combine_kernel
+    float *lse;                     // null, or log2 of every query row's softmax denominator (sink
+    int lse_ld;                     // included): [B * Hkv][lse_ld], row r = t G + h at lse_ld bg + r
 };
+
+// log2 of a row's denominator: running maximum M (sink included, log2 units) and the sum under
+// it; +inf for a row that saw no key and has no sink
+__device__ __forceinline__ float log2_den(float M, float den) { return M == -INFINITY ? INFINITY : M + log2f(den); }
+
 
 // The key tiles of the block of query rows r0 .. r_end - 1 of sequence b: the cached tiles
 // (pages pt_lo .. pt_lo + ncache - 1, or the ring's 16-cell groups) come first, then tiles of
@@ -190,6 +197,8 @@ __device__ __noinline__ void multi_combine_rows(const MultiParams &p, const floa
             if (Mf[i] != -INFINITY) {
                 const float d = den[i] * exp2f(M[i] - Mf[i]) + (sg[i] == -INFINITY ? 0.f : exp2f(sg[i] - Mf[i]));
                 inv[i] = d > 0.f ? 1.f / d : 0.f;
+                if (p.lse != nullptr && lane == 0)
+                    p.lse[(static_cast<size_t>(b) * p.Hkv + g) * p.lse_ld + r0 + rl[i]] = log2_den(Mf[i], d);
             }
         }
         float o[kCombRows][8];
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(NW * 32, MultiShape<NW>::kMinBlocks)
     state_reduce_l(st);
 
     // ---- finish: one split writes the rows, several leave partials for the last to combine
-    auto finish_row = [&](float m, float l, float sg, float &f) {  // f: factor on acc; false: zero row
+    auto finish_row = [&](float m, float l, float sg, float &f, int r) {  // f: factor on acc; false: zero row
         const float M = fmaxf(m, sg);
         if (M == -INFINITY) {
             f = 0.f;
@@ -523,6 +532,7 @@ __global__ void __launch_bounds__(NW * 32, MultiShape<NW>::kMinBlocks)
         }
         const float den = l * exp2f(m - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
         f = den > 0.f ? exp2f(m - M) / den : 0.f;
+        if (p.lse != nullptr && lane < 4) p.lse[bg * p.lse_ld + r] = log2_den(M, den);
     };
     if (nsplit == 1) {
 #pragma unroll
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(NW * 32, MultiShape<NW>::kMinBlocks)
                 const int r = r0 + kMRowsPerWarp * warp + 8 * j + 2 * (lane & 3) + c;
                 if (r >= r_end) continue;
                 float f = 0.f;
-                if (rp[j][c] >= 0) finish_row(st.m[j][c], st.l[j][c], sig[j][c], f);
+                if (rp[j][c] >= 0) finish_row(st.m[j][c], st.l[j][c], sig[j][c], f, r);
                 __nv_bfloat16 *o = out_row(r);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
@@ -628,6 +638,7 @@ __global__ void __launch_bounds__(kCombWarps * 32) multi_combine_kernel(const Mu
     if (Mf != -INFINITY) {
         const float d = den * exp2f(M - Mf) + (sg == -INFINITY ? 0.f : exp2f(sg - Mf));
         inv = d > 0.f ? 1.f / d : 0.f;
+        if (p.lse != nullptr && lane == 0) p.lse[bg * p.lse_ld + r] = log2_den(Mf, d);
     }
     // this lane's splits' weighted accumulators
     float o[kD];
