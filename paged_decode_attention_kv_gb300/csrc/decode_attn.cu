@@ -216,10 +216,12 @@ struct Params {
     // shared memory after it, with its query rows and new tokens); 0: every input is read
     // after the wait
     int early;
-    // the calls that also accumulate attention weights (WTS): log2 of every query row's softmax
-    // denominator (sink included) goes to lse[(b Hkv + g) lse_ld + row]
-    float *lse;
+    // the calls that also accumulate attention weights (WTS): minus log2 of every query row's
+    // softmax denominator (sink included) goes to nlse[(b Hkv + g) lse_ld + row], and in the
+    // one-token form every score (log2 units, masked: -inf) to scores[unit][16 tokens][G]
+    float *nlse;
     int lse_ld;
+    float *scores;
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -577,11 +579,15 @@ __device__ __forceinline__ void state_write_out_mt(SegState<NT> &s, const float 
     }
 }
 
-// log2 of the softmax denominators (sink included, log2 units) of a segment finished by one
-// warp: column c is query row r0 + c, lse_bg its group's rows. A column with no key and no sink
-// (not a query row) gets +inf, so that every weight 2^(s - lse) of it is 0.
+// Minus log2 of a row's softmax denominator: running maximum M (sink included, log2 units) and
+// the sum under it; -inf for a row that saw no key and has no sink (not a query row), so that
+// every weight 2^(s + nlse) of it is 0.
+__device__ __forceinline__ float neg_log2_den(float M, float den) { return M == -INFINITY ? -INFINITY : -(M + log2f(den)); }
+
+// The same for a segment finished by one warp: column c is query row r0 + c, nlse_bg its
+// group's rows.
 template <int NT>
-__device__ __forceinline__ void state_write_lse(const SegState<NT> &s, const float (&sig)[NT][2], float *lse_bg,
+__device__ __forceinline__ void state_write_lse(const SegState<NT> &s, const float (&sig)[NT][2], float *nlse_bg,
                                                 int rows, int r0, int lane) {
     if (lane >= 4) return;  // (after state_reduce_l every lane of a column holds the same m and l)
 #pragma unroll
@@ -591,8 +597,7 @@ __device__ __forceinline__ void state_write_lse(const SegState<NT> &s, const flo
             const int r = r0 + n * 8 + 2 * lane + j;
             if (r >= rows) continue;
             const float M = fmaxf(s.m[n][j], sig[n][j]);
-            lse_bg[r] = M == -INFINITY ? INFINITY
-                                       : M + log2f(s.l[n][j] * fast_exp2(s.m[n][j] - M) + fast_exp2(sig[n][j] - M));
+            nlse_bg[r] = neg_log2_den(M, s.l[n][j] * fast_exp2(s.m[n][j] - M) + fast_exp2(sig[n][j] - M));
         }
 }
 
@@ -674,8 +679,8 @@ struct SmemLayout {
 // sees the positions lo_t .. base + t (base = L - n, lo_t its window start), the n new tokens
 // are appended in the same pass, rows t >= n are zero. With more than 16 rows per KV head the
 // rows are cut into groups of 16 (p.ngrp), one per CTA of a pair that covers the same units.
-// WTS: the denominators of the softmax are written too (p.lse), for the kernel that adds up the
-// attention weights after this one.
+// WTS: the denominators of the softmax are written too (p.nlse), and with one token the scores,
+// for the kernel that adds up the attention weights after this one.
 template <int NT, bool RING, bool ROPE, bool KV8, int CPS, bool MT = false, bool WTS = false>
 __global__ void __launch_bounds__(kThreads, CPS)
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -753,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
     if (!early) wait_previous();
 
     const int B = p.B, Hkv = p.Hkv;
-    auto lse_of = [&](int b, int g) { return p.lse + (static_cast<size_t>(b) * Hkv + g) * p.lse_ld; };  // (WTS)
+    auto lse_of = [&](int b, int g) { return p.nlse + (static_cast<size_t>(b) * Hkv + g) * p.lse_ld; };  // (WTS)
 
     // ---- 1. lengths, validation, prefix of units over sequences
     {
@@ -1408,6 +1413,21 @@ __global__ void __launch_bounds__(kThreads, CPS)
                         }
                     }
                 }
+                if constexpr (WTS && !MT) {  // this lane's two tokens, two heads each
+                    const int h = n * 8 + (lane & 3) * 2;
+#pragma unroll
+                    for (int u = 0; u < UT; ++u) {
+                        float *dst = p.scores + (static_cast<size_t>(ua + i + u) * kPage + row_tok) * p.G + h;
+                        float *dst2 = dst + (KV8 ? 2 : 8) * p.G;
+                        if (h + 1 < p.G) {
+                            *reinterpret_cast<float2 *>(dst) = make_float2(sv[u][0], sv[u][1]);
+                            *reinterpret_cast<float2 *>(dst2) = make_float2(sv[u][2], sv[u][3]);
+                        } else if (h < p.G) {  // (G = 1)
+                            *dst = sv[u][0];
+                            *dst2 = sv[u][2];
+                        }
+                    }
+                }
                 float mx0 = fmaxf(sv[0][0], sv[0][2]), mx1 = fmaxf(sv[0][1], sv[0][3]);
 #pragma unroll
                 for (int u = 1; u < UT; ++u) {
@@ -1889,7 +1909,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
                         const float r = M == -INFINITY ? 0.f : fast_exp2(M - Mf);
                         den = den * r + (sg == -INFINITY ? 0.f : fast_exp2(sg - Mf));
                         if (WTS && d0 == 0 && rn < qrows)
-                            lse_of(b, g)[rn] = Mf == -INFINITY ? INFINITY : Mf + log2f(den);
+                            lse_of(b, g)[rn] = neg_log2_den(Mf, den);
                         if (rn < qrows) {
                             const int t = MT ? rn / p.G : 0, h = MT ? rn - t * p.G : rn;
                             const float inv = (MT && t >= s_n[b]) ? 0.f : r / den;  // no query token: zeros
@@ -2009,7 +2029,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
         const float Mf = fmaxf(M, sg);
         const float a = M == -INFINITY ? 0.f : fast_exp2(M - Mf);
         den = den * a + (sg == -INFINITY ? 0.f : fast_exp2(sg - Mf));
-        if (WTS && cd0 == 0 && rc < qrows) lse_of(b, g)[rc] = Mf == -INFINITY ? INFINITY : Mf + log2f(den);
+        if (WTS && cd0 == 0 && rc < qrows) lse_of(b, g)[rc] = neg_log2_den(Mf, den);
         const int ct = MT ? rc / p.G : 0, ch = MT ? rc - ct * p.G : rc;
         const float f = (den > 0.f && !(MT && ct >= s_n[b])) ? a / den : 0.f;  // no query token: zeros
         if (rc < qrows) {
@@ -2183,6 +2203,7 @@ struct DeviceState {
     std::atomic<bool> attr_set[128] = {};
     std::atomic<bool> multi_attr_set[8] = {};
     std::atomic<bool> evict_attr_set[2] = {};
+    std::atomic<bool> mw_attr_set[4] = {};
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -2348,10 +2369,11 @@ std::atomic<int> g_expire_next{-1};
 std::atomic<int> g_early_inputs{0};
 
 // What a call that accumulates attention weights adds to the attention it runs: where the
-// denominators go, and whether the stream is capturing a graph.
+// denominators and (one token) the scores go, and whether the stream is capturing a graph.
 struct WeightsOut {
-    float *lse;
+    float *nlse;
     int lse_ld;
+    float *scores;
     bool captured;
 };
 
@@ -2416,8 +2438,9 @@ int run_attention(bool ring, const void *q, const void *k_new, const void *v_new
     prm.expire_at = g_expire_next.exchange(-1);
     prm.head_scratch = nullptr;
     prm.early = g_early_inputs.load();
-    prm.lse = wts ? wts->lse : nullptr;
+    prm.nlse = wts ? wts->nlse : nullptr;
     prm.lse_ld = wts ? wts->lse_ld : 0;
+    prm.scores = wts ? wts->scores : nullptr;
     rc = prepare_workspace(dev, G, stream, &prm.part, &prm.counters, wts != nullptr && wts->captured);
     if (rc != DA_OK) return rc;
 
@@ -2724,8 +2747,9 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         dp.expire_at = -1;
         dp.head_scratch = m.rows == 32 ? dp.part + static_cast<size_t>(sm_count(dev)) * 2 * slot_floats(m.rows) : nullptr;
         dp.early = g_early_inputs.load();
-        dp.lse = wts ? wts->lse : nullptr;
+        dp.nlse = wts ? wts->nlse : nullptr;
         dp.lse_ld = wts ? wts->lse_ld : 0;
+        dp.scores = nullptr;
         CUtensorMap mk, mv;
         const uint64_t slices = static_cast<uint64_t>(num_pages) * s.num_kv_heads;
         if (!make_kv_map(&mk, k_cache, kPage, slices) || !make_kv_map(&mv, v_cache, kPage, slices)) {
@@ -2765,7 +2789,7 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
     prm.counters = static_cast<int *>(ws);
     prm.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
     prm.defer = m.defer ? 1 : 0;
-    prm.lse = wts ? wts->lse : nullptr;
+    prm.nlse = wts ? wts->nlse : nullptr;
     prm.lse_ld = wts ? wts->lse_ld : 0;
 
     CUtensorMap mk, mv, nk, nv;
@@ -2829,11 +2853,23 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
 }
 
 // ------------------------------------------------------------------ accumulated weights: host side
-// Rows of a (sequence, KV head)'s denominators in the workspace, a multiple of 4 (16 bytes).
-int lse_rows(const da_shape &s, int T) { return (T * (s.num_q_heads / s.num_kv_heads) + 3) & ~3; }
+// Rows of a (sequence, KV head)'s denominators in the workspace: a one-token call's query heads,
+// a multi-token call's query rows in blocks of kMwMaxRows (whole blocks are copied).
+int lse_rows(const da_shape &s, int T) {
+    const int G = s.num_q_heads / s.num_kv_heads;
+    return T == 0 ? G : (T * G + kMwMaxRows - 1) / kMwMaxRows * kMwMaxRows;
+}
 
-size_t weights_bytes(const da_shape &s, int T) {
-    return static_cast<size_t>(s.batch) * s.num_kv_heads * lse_rows(s, T) * sizeof(float);
+size_t lse_bytes(const da_shape &s, int T) {
+    const size_t n = static_cast<size_t>(s.batch) * s.num_kv_heads * lse_rows(s, T) * sizeof(float);
+    return (n + 255) & ~static_cast<size_t>(255);
+}
+
+// The weights workspace: the denominators, and for a one-token call (T = 0) its scores, 16 tokens
+// and G heads per tile of the longest sequences.
+size_t weights_bytes(const da_shape &s, int T, int max_seq_len) {
+    const size_t tiles = T == 0 ? (static_cast<size_t>(max_seq_len) + kPage - 1) / kPage : 0;
+    return lse_bytes(s, T) + static_cast<size_t>(s.batch) * s.num_q_heads * tiles * kPage * sizeof(float);
 }
 
 // The weights workspace of a call on `stream`; *captured: the stream is capturing a graph.
@@ -2846,6 +2882,85 @@ int prepare_weights(int dev, cudaStream_t stream, size_t need, void **ws, bool *
     return workspace_locked(dev, stream, kWsWeights, need, ws, *captured);
 }
 
+// q [B][T][Hq][64] as blocks of `rows` query rows (t, h) of one KV head: dims {64, Hq, B T}, box
+// {64, G, rows / G}, 128-byte swizzle.
+bool make_q_map(CUtensorMap *map, const void *base, int Hq, int G, int rows, uint64_t tokens) {
+    const int kind = (1 << 28) | (Hq << 12) | (G << 7) | (rows / 32);  // cache key: no other view's kind
+    std::lock_guard<std::mutex> lk(g_map_mu);
+    for (int i = 0; i < kMapCache; ++i) {
+        const MapCacheEntry &e = g_maps[i];
+        if (e.base == base && e.kind == kind && e.rows == tokens) {
+            *map = e.map;
+            return true;
+        }
+    }
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(Hq), tokens};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(Hq) * kD * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kD), static_cast<cuuint32_t>(G),
+                               static_cast<cuuint32_t>(rows / G)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    MapCacheEntry &e = g_maps[g_map_next];
+    g_map_next = (g_map_next + 1) % kMapCache;
+    e.base = const_cast<void *>(base);
+    e.kind = kind;
+    e.rows = tokens;
+    e.slices = 0;
+    e.map = *map;
+    return true;
+}
+
+cudaLaunchAttribute pdl_attribute() {
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
+template <int G>
+int launch_score_weights(const WeightParams &p, int dev, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sm_count(dev) * kSwCtasPerSm);
+    cfg.blockDim = dim3(kSwThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, score_weights_kernel<G>, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+}
+
+template <int N>
+int launch_multi_weights(const CUtensorMap &mk, const CUtensorMap &mq, const WeightParams &p, int runs, int dev,
+                         cudaStream_t stream) {
+    auto kern = multi_weights_kernel<N>;
+    const int idx = N == 32 ? 0 : N == 64 ? 1 : N == 128 ? 2 : 3;
+    if (!g_dev[dev].mw_attr_set[idx].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MwLayout<N>::bytes);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return set_cuda_error(e);
+        g_dev[dev].mw_attr_set[idx].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(runs, p.Hkv, p.B);
+    cfg.blockDim = dim3(kMwThreads);
+    cfg.dynamicSmemBytes = MwLayout<N>::bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mk, mq, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+}
+
 // One step of attention (T = 0: one token per sequence; else T, with q_lens) over a paged cache
 // that also adds every attended cell's attention weight to `weights`.
 int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
@@ -2854,12 +2969,8 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
                 int max_pages, int num_pages, int max_seq_len, void *stream_v) {
     int rc = check_shape(s);
     if (rc != DA_OK) return rc;
-    if (!weights || !aligned16(weights) || T < 0 || !(scale > 0.f) || !(scale < INFINITY)) return DA_ERR_INVALID_ARG;
+    if (!weights || !aligned16(weights) || !(scale > 0.f) || !(scale < INFINITY)) return DA_ERR_INVALID_ARG;
     if (T > kMMaxTokens) return DA_ERR_UNSUPPORTED;
-    const int rows_t = T > 0 ? T : 1;
-    WeightsOut wo{nullptr, lse_rows(s, rows_t), false};
-    int dev = 0;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     // Everything else is checked by the attention call itself, which comes first: with no
     // workspace yet it is asked for an empty batch, which launches nothing.
     auto attention = [&](const da_shape &sh, const WeightsOut *w) {
@@ -2872,45 +2983,66 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     };
     rc = attention(da_shape{0, s.num_q_heads, s.num_kv_heads, s.head_dim}, nullptr);
     if (rc != DA_OK || s.batch == 0) return rc;
+    int dev = 0;
     rc = current_device(&dev);
     if (rc != DA_OK) return rc;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     void *ws = nullptr;
-    rc = prepare_weights(dev, stream, weights_bytes(s, rows_t), &ws, &wo.captured);
+    WeightsOut wo{nullptr, lse_rows(s, T), nullptr, false};
+    rc = prepare_weights(dev, stream, weights_bytes(s, T, max_seq_len), &ws, &wo.captured);
     if (rc != DA_OK) return rc;
-    wo.lse = static_cast<float *>(ws);
+    wo.nlse = static_cast<float *>(ws);
+    wo.scores = reinterpret_cast<float *>(static_cast<char *>(ws) + lse_bytes(s, T));
     rc = attention(s, &wo);
-    if (rc != DA_OK) return rc;
+    if (rc != DA_OK || max_seq_len == 0) return rc;
 
+    const int G = s.num_q_heads / s.num_kv_heads;
     WeightParams p;
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k_cache = static_cast<const uint8_t *>(k_cache);
     p.weights = weights;
     p.block_table = block_table;
     p.seq_lens = seq_lens;
     p.q_lens = q_lens;
-    p.lse = wo.lse;
+    p.nlse = wo.nlse;
     p.lse_ld = wo.lse_ld;
+    p.scores = wo.scores;
     p.scale_log2 = scale * kLog2e;
     p.B = s.batch;
-    p.Hq = s.num_q_heads;
     p.Hkv = s.num_kv_heads;
-    p.G = s.num_q_heads / s.num_kv_heads;
-    p.T = rows_t;
+    p.G = G;
+    p.T = T;
     p.window = window;
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.max_seq_len = max_seq_len;
     p.assign_new = k_new != nullptr ? 1 : 0;
-    if (max_seq_len == 0) return DA_OK;
-    const int span = window > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(window) + rows_t - 1 + kPage) : max_seq_len;
-    const int tiles = (span + kPage - 1) / kPage + 1;
-    const dim3 grid((tiles + 7) / 8, s.num_kv_heads, s.batch);
-    if (kv8)
-        weights_plain_kernel<true><<<grid, 256, 0, stream>>>(p);
-    else
-        weights_plain_kernel<false><<<grid, 256, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+    p.run = 0;
+    if (T == 0)
+        return G == 1   ? launch_score_weights<1>(p, dev, stream)
+               : G == 2 ? launch_score_weights<2>(p, dev, stream)
+               : G == 4 ? launch_score_weights<4>(p, dev, stream)
+               : G == 8 ? launch_score_weights<8>(p, dev, stream)
+                        : launch_score_weights<16>(p, dev, stream);
+    // key runs: the 128-key stages of the longest range any sequence's rows can see, cut so that
+    // the GPU has several CTAs per slot, within what a CTA can hold
+    const int rows = T * G;
+    const int N = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : kMwMaxRows;
+    const long long span = window > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(window) + T + kMwKeys) : max_seq_len;
+    const long long stages = (span + kMwKeys - 1) / kMwKeys;
+    const long long pairs = static_cast<long long>(s.batch) * s.num_kv_heads;
+    const int want = sm_count(dev) * (N < kMwMaxRows ? 8 : 4);
+    const int most = rows > kMwMaxRows ? kMwResident : kMwMaxRun;
+    p.run = static_cast<int>(std::max<long long>(1, std::min<long long>(most, stages * pairs / want)));
+    const int runs = static_cast<int>((stages + p.run - 1) / p.run);
+    CUtensorMap mk, mq;
+    if (!make_kv_map(&mk, k_cache, kPage, static_cast<uint64_t>(num_pages) * s.num_kv_heads) ||
+        !make_q_map(&mq, q, s.num_q_heads, G, N, static_cast<uint64_t>(s.batch) * T)) {
+        snprintf(t_err, sizeof t_err, "CUDA error: tensor map encoding failed");
+        return DA_ERR_CUDA;
+    }
+    return N == 32    ? launch_multi_weights<32>(mk, mq, p, runs, dev, stream)
+           : N == 64  ? launch_multi_weights<64>(mk, mq, p, runs, dev, stream)
+           : N == 128 ? launch_multi_weights<128>(mk, mq, p, runs, dev, stream)
+                      : launch_multi_weights<kMwMaxRows>(mk, mq, p, runs, dev, stream);
 }
 
 // ------------------------------------------------------------------ eviction: host side
@@ -3091,8 +3223,9 @@ int run_paged_noalloc(const void *q, const void *k_new, const void *v_new, void 
     prm.expire_at = -1;
     prm.head_scratch = nullptr;
     prm.early = g_early_inputs.load();
-    prm.lse = nullptr;
+    prm.nlse = nullptr;
     prm.lse_ld = 0;
+    prm.scores = nullptr;
     prm.counters = static_cast<int *>(scratch);
     prm.part = reinterpret_cast<float *>(static_cast<char *>(scratch) + kNoAllocCounterBytes);
     // The array keeps whatever the previous call left: the arrival counters this call
@@ -3230,7 +3363,8 @@ int kv_evict_fp8(void *kv_cache, float *weights, const int32_t *block_table, con
 
 size_t decode_attn_weights_workspace_bytes(da_shape s, int q_tokens, int max_seq_len) {
     if (check_shape(s) != DA_OK || q_tokens <= 0 || q_tokens > kMMaxTokens || max_seq_len < 0) return 0;
-    return weights_bytes(s, q_tokens);
+    const size_t many = weights_bytes(s, q_tokens, max_seq_len);  // (a multi-token call of one token, too)
+    return q_tokens == 1 ? std::max(many, weights_bytes(s, 0, max_seq_len)) : many;
 }
 
 size_t kv_evict_workspace_bytes(da_shape s, int keep) {

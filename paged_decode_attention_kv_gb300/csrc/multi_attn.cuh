@@ -76,14 +76,9 @@ struct MultiParams {
     float *part;                    // [B * Hkv * row_blocks][splits][rows per CTA][kMSlotFloats]
     int *counters;                  // [B * Hkv * row_blocks], zero at rest
     int defer;                      // 1: the split partials are left for multi_combine_kernel
-    float *lse;                     // null, or log2 of every query row's softmax denominator (sink
+    float *nlse;                    // null, or minus log2 of every query row's softmax denominator (sink
     int lse_ld;                     // included): [B * Hkv][lse_ld], row r = t G + h at lse_ld bg + r
 };
-
-// log2 of a row's denominator: running maximum M (sink included, log2 units) and the sum under
-// it; +inf for a row that saw no key and has no sink
-__device__ __forceinline__ float log2_den(float M, float den) { return M == -INFINITY ? INFINITY : M + log2f(den); }
-
 
 // The key tiles of the block of query rows r0 .. r_end - 1 of sequence b: the cached tiles
 // (pages pt_lo .. pt_lo + ncache - 1, or the ring's 16-cell groups) come first, then tiles of
@@ -197,8 +192,8 @@ __device__ __noinline__ void multi_combine_rows(const MultiParams &p, const floa
             if (Mf[i] != -INFINITY) {
                 const float d = den[i] * exp2f(M[i] - Mf[i]) + (sg[i] == -INFINITY ? 0.f : exp2f(sg[i] - Mf[i]));
                 inv[i] = d > 0.f ? 1.f / d : 0.f;
-                if (p.lse != nullptr && lane == 0)
-                    p.lse[(static_cast<size_t>(b) * p.Hkv + g) * p.lse_ld + r0 + rl[i]] = log2_den(Mf[i], d);
+                if (p.nlse != nullptr && lane == 0)
+                    p.nlse[(static_cast<size_t>(b) * p.Hkv + g) * p.lse_ld + r0 + rl[i]] = neg_log2_den(Mf[i], d);
             }
         }
         float o[kCombRows][8];
@@ -532,7 +527,7 @@ __global__ void __launch_bounds__(NW * 32, MultiShape<NW>::kMinBlocks)
         }
         const float den = l * exp2f(m - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
         f = den > 0.f ? exp2f(m - M) / den : 0.f;
-        if (p.lse != nullptr && lane < 4) p.lse[bg * p.lse_ld + r] = log2_den(M, den);
+        if (p.nlse != nullptr && lane < 4) p.nlse[bg * p.lse_ld + r] = neg_log2_den(M, den);
     };
     if (nsplit == 1) {
 #pragma unroll
@@ -638,7 +633,7 @@ __global__ void __launch_bounds__(kCombWarps * 32) multi_combine_kernel(const Mu
     if (Mf != -INFINITY) {
         const float d = den * exp2f(M - Mf) + (sg == -INFINITY ? 0.f : exp2f(sg - Mf));
         inv = d > 0.f ? 1.f / d : 0.f;
-        if (p.lse != nullptr && lane == 0) p.lse[bg * p.lse_ld + r] = log2_den(Mf, d);
+        if (p.nlse != nullptr && lane == 0) p.nlse[bg * p.lse_ld + r] = neg_log2_den(Mf, d);
     }
     // this lane's splits' weighted accumulators
     float o[kD];
