@@ -2203,7 +2203,7 @@ struct DeviceState {
     std::atomic<bool> attr_set[128] = {};
     std::atomic<bool> multi_attr_set[8] = {};
     std::atomic<bool> evict_attr_set[2] = {};
-    std::atomic<bool> mw_attr_set[4] = {};
+    std::atomic<bool> mw_attr_set[6] = {};
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -2843,12 +2843,18 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return set_cuda_error(e);
     }
-    // the append, after every read of the cache (an ordinary launch: it waits for the kernel)
-    kv_append_multi_kernel<<<s.batch, 256, 0, stream>>>(
-        prm.k_new, prm.v_new, static_cast<__nv_bfloat16 *>(k_cache), static_cast<__nv_bfloat16 *>(v_cache),
-        ring ? nullptr : block_table, seq_lens, q_lens, T, s.num_kv_heads, ring ? window : 0, prm.max_pages,
-        prm.num_pages, prm.max_seq_len);
-    e = cudaGetLastError();
+    // the append, after every read of the cache (it waits for the kernel before it reads anything)
+    cudaLaunchConfig_t ca = {};
+    ca.gridDim = dim3(s.batch, append_blocks(T, s.num_kv_heads));
+    ca.blockDim = dim3(kAppendThreads);
+    ca.stream = stream;
+    ca.attrs = attr;
+    ca.numAttrs = 1;
+    e = cudaLaunchKernelEx(&ca, kv_append_multi_kernel, prm.k_new, prm.v_new, static_cast<__nv_bfloat16 *>(k_cache),
+                           static_cast<__nv_bfloat16 *>(v_cache), ring ? static_cast<const int *>(nullptr) : block_table,
+                           seq_lens, q_lens, T, s.num_kv_heads, ring ? window : 0, prm.max_pages, prm.num_pages,
+                           prm.max_seq_len);
+    if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? DA_OK : set_cuda_error(e);
 }
 
@@ -2936,22 +2942,21 @@ int launch_score_weights(const WeightParams &p, int dev, cudaStream_t stream) {
     return e == cudaSuccess ? DA_OK : set_cuda_error(e);
 }
 
-template <int N>
-int launch_multi_weights(const CUtensorMap &mk, const CUtensorMap &mq, const WeightParams &p, int runs, int dev,
-                         cudaStream_t stream) {
-    auto kern = multi_weights_kernel<N>;
-    const int idx = N == 32 ? 0 : N == 64 ? 1 : N == 128 ? 2 : 3;
+// One of the several-token weight kernels, `idx` its attribute flag.
+template <typename Kernel>
+int launch_row_weights(Kernel kern, int idx, int threads, size_t smem, const CUtensorMap &mk, const CUtensorMap &mq,
+                       const WeightParams &p, long long blocks, int dev, cudaStream_t stream) {
     if (!g_dev[dev].mw_attr_set[idx].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MwLayout<N>::bytes);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return set_cuda_error(e);
         g_dev[dev].mw_attr_set[idx].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(runs, p.Hkv, p.B);
-    cfg.blockDim = dim3(kMwThreads);
-    cfg.dynamicSmemBytes = MwLayout<N>::bytes;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), p.Hkv, p.B);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
@@ -2959,6 +2964,20 @@ int launch_multi_weights(const CUtensorMap &mk, const CUtensorMap &mq, const Wei
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mk, mq, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+}
+
+template <int N>
+int launch_stream_keys(int idx, const CUtensorMap &mk, const CUtensorMap &mq, const WeightParams &p, long long runs,
+                       int dev, cudaStream_t stream) {
+    return launch_row_weights(stream_keys_weights_kernel<N>, idx, SkLayout<N>::kThreads, SkLayout<N>::bytes, mk, mq, p, runs,
+                              dev, stream);
+}
+
+template <int TILES>
+int launch_stream_rows(int idx, const CUtensorMap &mk, const CUtensorMap &mq, const WeightParams &p, long long blocks,
+                       int dev, cudaStream_t stream) {
+    return launch_row_weights(stream_rows_weights_kernel<TILES>, idx, SrLayout<TILES>::kThreads, SrLayout<TILES>::bytes, mk,
+                              mq, p, blocks, dev, stream);
 }
 
 // One step of attention (T = 0: one token per sequence; else T, with q_lens) over a paged cache
@@ -3022,27 +3041,32 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
                : G == 4 ? launch_score_weights<4>(p, dev, stream)
                : G == 8 ? launch_score_weights<8>(p, dev, stream)
                         : launch_score_weights<16>(p, dev, stream);
-    // key runs: the 128-key stages of the longest range any sequence's rows can see, cut so that
-    // the GPU has several CTAs per slot, within what a CTA can hold
+    // the 128-key stages of the longest range that any sequence's rows can see
     const int rows = T * G;
-    const int N = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : kMwMaxRows;
     const long long span = window > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(window) + T + kMwKeys) : max_seq_len;
     const long long stages = (span + kMwKeys - 1) / kMwKeys;
     const long long pairs = static_cast<long long>(s.batch) * s.num_kv_heads;
-    const int want = sm_count(dev) * (N < kMwMaxRows ? 8 : 4);
-    const int most = rows > kMwMaxRows ? kMwResident : kMwMaxRun;
-    p.run = static_cast<int>(std::max<long long>(1, std::min<long long>(most, stages * pairs / want)));
-    const int runs = static_cast<int>((stages + p.run - 1) / p.run);
+    const int N = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : kMwMaxRows;  // (rows that stay)
     CUtensorMap mk, mq;
     if (!make_kv_map(&mk, k_cache, kPage, static_cast<uint64_t>(num_pages) * s.num_kv_heads) ||
-        !make_q_map(&mq, q, s.num_q_heads, G, N, static_cast<uint64_t>(s.batch) * T)) {
+        !make_q_map(&mq, q, s.num_q_heads, G, rows <= kMwMaxRows ? N : kMwRowBlock, static_cast<uint64_t>(s.batch) * T)) {
         snprintf(t_err, sizeof t_err, "CUDA error: tensor map encoding failed");
         return DA_ERR_CUDA;
     }
-    return N == 32    ? launch_multi_weights<32>(mk, mq, p, runs, dev, stream)
-           : N == 64  ? launch_multi_weights<64>(mk, mq, p, runs, dev, stream)
-           : N == 128 ? launch_multi_weights<128>(mk, mq, p, runs, dev, stream)
-                      : launch_multi_weights<kMwMaxRows>(mk, mq, p, runs, dev, stream);
+    if (rows > kMwMaxRows) {
+        const bool two = stages / 2 * pairs >= 3 * sm_count(dev);
+        const long long blocks = two ? (stages + 1) / 2 : stages;
+        return two ? launch_stream_rows<2>(5, mk, mq, p, blocks, dev, stream)
+                   : launch_stream_rows<1>(4, mk, mq, p, blocks, dev, stream);
+    }
+    // runs of stages, so that the GPU has several CTAs per slot, within what a CTA can hold
+    const int want = sm_count(dev) * (N < kMwMaxRows ? 8 : 4);
+    p.run = static_cast<int>(std::max<long long>(1, std::min<long long>(kMwMaxRun, stages * pairs / want)));
+    const long long runs = (stages + p.run - 1) / p.run;
+    return N == 32    ? launch_stream_keys<32>(0, mk, mq, p, runs, dev, stream)
+           : N == 64  ? launch_stream_keys<64>(1, mk, mq, p, runs, dev, stream)
+           : N == 128 ? launch_stream_keys<128>(2, mk, mq, p, runs, dev, stream)
+                      : launch_stream_keys<kMwMaxRows>(3, mk, mq, p, runs, dev, stream);
 }
 
 // ------------------------------------------------------------------ eviction: host side

@@ -669,12 +669,20 @@ __global__ void __launch_bounds__(kCombWarps * 32) multi_combine_kernel(const Mu
 }
 
 // The append of a multi-token step: new token t < n of b goes to position L - n + t. In a
-// ring only the last W of them survive (one write per cell).
+// ring only the last W of them survive (one write per cell). A sequence's 16-byte pieces are
+// shared out over gridDim.y blocks (one block per sequence had made a 512-token append
+// 98 us long, four 2048-token ones 317 us).
+constexpr int kAppendThreads = 256, kAppendPerThread = 2;
+int append_blocks(int T, int Hkv) {
+    const long long pieces = static_cast<long long>(T) * Hkv * (kD / 8);
+    return static_cast<int>(std::min<long long>(4096, (pieces + kAppendThreads * kAppendPerThread - 1) / (kAppendThreads * kAppendPerThread)));
+}
 __global__ void kv_append_multi_kernel(const __nv_bfloat16 *__restrict__ k_new,
                                        const __nv_bfloat16 *__restrict__ v_new, __nv_bfloat16 *k_cache,
                                        __nv_bfloat16 *v_cache, const int *__restrict__ block_table,
                                        const int *__restrict__ seq_lens, const int *__restrict__ q_lens, int T,
                                        int Hkv, int window, int max_pages, int num_pages, int max_seq_len) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention has read the cache
     const int b = blockIdx.x;
     const int L = __ldg(seq_lens + b);
     const int n = q_lens != nullptr ? __ldg(q_lens + b) : T;
@@ -688,7 +696,7 @@ __global__ void kv_append_multi_kernel(const __nv_bfloat16 *__restrict__ k_new,
     const int base = L - n;
     const int first = block_table == nullptr && n > window ? n - window : 0;  // ring: last W only
     constexpr int kChunks = kD / 8;  // 16-byte pieces per row
-    for (int i = threadIdx.x; i < (n - first) * Hkv * kChunks; i += blockDim.x) {
+    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < (n - first) * Hkv * kChunks; i += gridDim.y * blockDim.x) {
         const int t = first + i / (Hkv * kChunks);
         const int g = (i / kChunks) % Hkv, c = i % kChunks;
         const int pos = base + t;

@@ -9,7 +9,7 @@
 //
 // One token per sequence: the attention kernel leaves its scores too (score_weights_kernel below
 // reads them back, mostly from L2). Several tokens: the scores are formed again on the tensor
-// cores (multi_weights_kernel), since T times as many would cost more to write and read than
+// cores (the tcgen05 kernels), since T times as many would cost more to write and read than
 // the keys cost to read.
 
 struct WeightParams {
@@ -21,7 +21,7 @@ struct WeightParams {
     float scale_log2;
     int B, Hkv, G, T, window, max_pages, num_pages, max_seq_len;
     int assign_new;                  // the call appended its new tokens
-    int run;                         // several tokens: 128-key stages per CTA
+    int run;                         // several tokens, streamed keys: 128-key stages per CTA
 };
 
 // ------------------------------------------------------------------ one token per sequence
@@ -149,43 +149,22 @@ __global__ void __launch_bounds__(kSwThreads, kSwCtasPerSm) score_weights_kernel
 }
 
 // ------------------------------------------------------------------ several tokens per sequence
-// One CTA per (sequence, KV head, run of 128-key stages). S^T = K Q^T on tcgen05 puts the keys on
-// the TMEM lanes (M = 128) and N query rows on the columns, so a key's sum over the rows is a sum
-// along a thread's own columns: no shuffles, and the denominators are the same for every lane (one
-// broadcast shared-memory read per four columns). Ten warps:
-//   warps 0-7  columns [0, N/2) (warps 0-3) and [N/2, N) (4-7) of the stage's 128 keys: exponentials
-//              and sums, into shared memory per (stage, half, key)
-//   warp 8     TMA: key stages (8 tiles), query blocks with their denominators
-//   warp 9     MMA issue, two TMEM buffers of N columns
-// Up to 256 rows (N = 32, 64, 128, 256): one query block stays, the key stages stream through a
-// ring. More: the run's stages (at most kMwResident) stay, and query blocks of 256 rows stream
-// through two slots; a key's sum then takes several blocks, added with a compensated sum (16384
-// terms one after another in 32 bits would lose the last bits).
-// Blocks of rows that see no key of a stage (causal mask, window) are skipped by every role.
+// S^T = K Q^T on tcgen05 puts 128 keys on the TMEM lanes (M) and N query rows on the columns, so a
+// key's sum over the rows is a sum along a thread's own columns: no shuffles, and the
+// denominators are the same for every lane (one broadcast shared-memory read per four columns).
+// Two kernels, for what stays in shared memory and what streams past it:
+//   stream_keys_weights_kernel<N>      up to 256 query rows per (sequence, KV head): the rows stay
+//                                      (N = 32, 64, 128 or 256), 128-key stages stream through a ring
+//   stream_rows_weights_kernel<TILES>  more: 128 or 256 keys stay, blocks of 128 query rows stream
+// Roles: groups of four warps (128 TMEM lanes each, a share of the columns) form exponentials and
+// sums from two TMEM buffers; one warp issues the TMA copies, one thread the products. Keys and
+// rows that cannot see each other (causal mask, window) are skipped by every role alike.
 constexpr int kMwKeys = 128;
 constexpr int kMwTiles = kMwKeys / kPage;
-constexpr int kMwKBytes = kMwKeys * kD * 2;  // 16 KiB per key stage
-constexpr int kMwMaxRows = 256;              // query rows per block
-constexpr int kMwResident = 4;               // key stages per CTA when query blocks stream
+constexpr int kMwKBytes = kMwKeys * kD * 2;  // 16 KiB of keys
+constexpr int kMwMaxRows = 256;              // query rows that stay, at most
+constexpr int kMwRowBlock = 128;             // query rows per streamed block
 constexpr int kMwMaxRun = 16;                // key stages per CTA at most
-constexpr int kMwThreads = 320;
-
-template <int N>
-struct MwLayout {
-    static constexpr int kQSlots = N == kMwMaxRows ? 2 : 1;
-    static constexpr int kRing = N == kMwMaxRows ? 6 : 4;
-    static constexpr int kQBytes = N * kD * 2;
-    static constexpr int k = kQSlots * kQBytes;
-    static constexpr int lse = k + kRing * kMwKBytes;
-    static constexpr int acc = lse + kQSlots * N * 4;
-    static constexpr int bars = acc + kMwMaxRun * 2 * kMwKeys * 4;
-    static constexpr int kBars = 2 * kRing + 2 * kQSlots + 5;
-    static constexpr int bytes = 1024 + bars + kBars * 8;  // with the slack to align the base
-    static constexpr int kCtas = N == kMwMaxRows ? 1 : 2;  // resident per SM
-    static_assert(kQBytes % 1024 == 0 && acc % 16 == 0 && bars % 8 == 0, "alignment");
-    static_assert(kCtas * (bytes + 1024) <= 233472, "shared memory of the CTAs on one SM");
-    static_assert(kMwResident <= kRing && kMwResident * 2 <= kMwMaxRun, "resident stages, compensated sums");
-};
 
 __device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
                                                   uint32_t bar) {
@@ -244,21 +223,114 @@ __device__ __forceinline__ float sum_columns(const uint32_t (&v)[CH], const floa
     return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
 }
 
+// What a CTA works on: sequence counts and its first key.
+struct MwKeys {
+    int L, n, base, lo0;
+    bool ok;
+};
+__device__ __forceinline__ MwKeys mw_keys(const WeightParams &p, int b) {
+    MwKeys k;
+    k.L = __ldg(p.seq_lens + b);
+    k.n = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
+    // counts out of range were flagged by the attention
+    k.ok = k.L > 0 && k.L <= p.max_seq_len && k.L <= p.max_pages * kPage && k.n > 0 && k.n <= p.T && k.n <= k.L;
+    k.base = k.L - k.n;
+    k.lo0 = p.window > 0 ? max(0, k.base - p.window + 1) : 0;
+    return k;
+}
+
+// Query rows [lo, hi) that see key j: tokens t >= j - base, t < n, t < j - base + W.
+__device__ __forceinline__ int2 rows_of_key(const WeightParams &p, const MwKeys &k, int j) {
+    const int lo = max(0, j - k.base);
+    const int hi = j < k.L ? (p.window > 0 ? max(lo, min(k.n, j - k.base + p.window)) : k.n) : lo;
+    return make_int2(lo * p.G, hi * p.G);
+}
+
+// The key tiles from position `first` on (lane u < tiles: tile u) into dst, counted on bar. Tiles past
+// the end and of pages outside the pool are left out: the sums of their keys are not used.
+__device__ __forceinline__ void mw_load_keys(const WeightParams &p, const CUtensorMap *tmk, int b, int g, int L, int first,
+                                             int tiles, uint32_t dst, uint32_t bar, uint64_t policy, int lane) {
+    const int pt = first / kPage + lane;
+    int page = -1;
+    if (lane < tiles && pt * kPage < L) page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + pt);
+    const bool ok = page >= 0 && page < p.num_pages;
+    const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
+    if (lane == 0) mbar_expect_tx(bar, cnt * kTileBytes);
+    __syncwarp();
+    if (ok) tma_load_3d(dst + lane * kTileBytes, tmk, 0, 0, page * p.Hkv + g, bar, policy);
+}
+
+// Sums of `keys` keys from position `first` on to their cells.
+template <typename Sum>
+__device__ __forceinline__ void mw_add(const WeightParams &p, const MwKeys &k, int b, int g, int first, int keys, Sum sum) {
+    for (int i = threadIdx.x; i < keys; i += blockDim.x) {
+        const int j = first + i;
+        if (j >= k.L || j < k.lo0) continue;
+        const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + j / kPage);
+        if (page < 0 || page >= p.num_pages) continue;
+        float *dst = p.weights + (static_cast<size_t>(page) * p.Hkv + g) * kPage + j % kPage;
+        if (p.assign_new && j >= k.base)
+            *dst = sum(i);
+        else
+            atomicAdd(dst, sum(i));
+    }
+}
+
+// Sum over COLS columns from TMEM column ta on, 32 (or 16) at a time, the next load under way while one
+// is summed. MASK: only the columns [lo, hi).
+template <int COLS, bool MASK>
+__device__ __forceinline__ float sum_tmem(uint32_t ta, const float *nlse, float scale, int lo, int hi) {
+    constexpr int CH = COLS < 32 ? 16 : 32;
+    uint32_t v[2][CH];
+    float sum = 0.f;
+    if constexpr (CH == 32) tmem_ld32(ta, v[0]);
+    else tmem_ld16(ta, v[0]);
+#pragma unroll
+    for (int c = 0; c < COLS / CH; ++c) {
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < CH; ++i) asm volatile("" : "+r"(v[c & 1][i]));  // (not used before the wait)
+        if constexpr (CH == 32)
+            if (c + 1 < COLS / CH) tmem_ld32(ta + 32 * (c + 1), v[(c + 1) & 1]);
+        sum += sum_columns<CH, MASK>(v[c & 1], nlse + CH * c, scale, lo - CH * c, hi - CH * c);
+    }
+    return sum;
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return !__any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity));
+}
+
 template <int N>
-__global__ void __launch_bounds__(kMwThreads, MwLayout<N>::kCtas)
-    multi_weights_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmq,
-                         const WeightParams p) {
-    using Lay = MwLayout<N>;
-    constexpr int kRing = Lay::kRing, kQSlots = Lay::kQSlots;
-    constexpr int kHalf = N / 2, CH = kHalf < 32 ? 16 : 32;  // columns per warp, and per TMEM load
+struct SkLayout {
+    static constexpr int kEpi = N == kMwMaxRows ? 16 : 8;      // warps that sum
+    static constexpr int kParts = kEpi / 4;                    // shares of the columns
+    static constexpr int kThreads = (kEpi + 2) * 32;
+    static constexpr int kCtas = N == kMwMaxRows ? 1 : 2;      // resident per SM
+    static constexpr int kRing = N == kMwMaxRows ? 8 : 4;
+    static constexpr int k = N * kD * 2;
+    static constexpr int lse = k + kRing * kMwKBytes;
+    static constexpr int acc = lse + N * 4;
+    static constexpr int bars = acc + kMwMaxRun * kParts * kMwKeys * 4;
+    static constexpr int bytes = 1024 + bars + (2 * kRing + 6) * 8;  // with the slack to align the base
+    static_assert(k % 1024 == 0 && acc % 16 == 0 && bars % 8 == 0, "alignment");
+    static_assert(kCtas * (bytes + 1024) <= 233472, "shared memory of the CTAs on one SM");
+};
+
+// One CTA per (sequence, KV head, run of p.run key stages).
+template <int N>
+__global__ void __launch_bounds__(SkLayout<N>::kThreads, SkLayout<N>::kCtas)
+    stream_keys_weights_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmq,
+                               const WeightParams p) {
+    using Lay = SkLayout<N>;
+    constexpr int kRing = Lay::kRing, kEpi = Lay::kEpi, kCols = N / Lay::kParts;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t q_s = smem_addr(smem), k_s = q_s + Lay::k;
     float *const s_lse = reinterpret_cast<float *>(smem + Lay::lse);
     float *const s_acc = reinterpret_cast<float *>(smem + Lay::acc);
     const uint32_t k_full = smem_addr(smem + Lay::bars), k_empty = k_full + 8 * kRing;
-    const uint32_t q_full = k_empty + 8 * kRing, q_empty = q_full + 8 * kQSlots;
-    const uint32_t t_full = q_empty + 8 * kQSlots, t_empty = t_full + 16, drain = t_empty + 16;
+    const uint32_t q_full = k_empty + 8 * kRing, t_full = q_full + 8, t_empty = t_full + 16, drain = t_empty + 16;
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
 
@@ -271,45 +343,22 @@ __global__ void __launch_bounds__(kMwThreads, MwLayout<N>::kCtas)
             mbar_init(k_full + 8 * s, 1);
             mbar_init(k_empty + 8 * s, 1);
         }
-        for (int s = 0; s < kQSlots; ++s) {
-            mbar_init(q_full + 8 * s, 1);
-            mbar_init(q_empty + 8 * s, 9);  // the products, and the eight warps that read the denominators
-        }
+        mbar_init(q_full, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(t_full + 8 * s, 1);
-            mbar_init(t_empty + 8 * s, 8);
+            mbar_init(t_empty + 8 * s, kEpi);
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_failed = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // ---- this CTA's rows and keys (counts out of range were flagged by the attention)
-    const int L = __ldg(p.seq_lens + b);
-    const int n = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
-    if (L <= 0 || L > p.max_seq_len || L > p.max_pages * kPage || n <= 0 || n > p.T || n > L) return;
-    const int base = L - n, W = p.window;
-    const int lo0 = W > 0 ? max(0, base - W + 1) : 0;
-    const int s0 = lo0 / kMwKeys + blockIdx.x * p.run;     // first stage: positions 128 s0 on
-    const int ns = min(p.run, (L - 1) / kMwKeys - s0 + 1);
+    const MwKeys k = mw_keys(p, b);
+    if (!k.ok) return;
+    const int s0 = k.lo0 / kMwKeys + blockIdx.x * p.run;  // first stage: positions 128 s0 on
+    const int ns = min(p.run, (k.L - 1) / kMwKeys - s0 + 1);
     if (ns <= 0) return;
-    const int nqb = (n * p.G + N - 1) / N;
-    const bool many = nqb > 1;                             // query blocks stream, the stages stay
-    // does a row of block qb see a key at a position in [first, last]?
-    auto sees = [&](int qb, int first, int last) {
-        const int t0 = qb * N / p.G, t1 = min(n - 1, (qb * N + N - 1) / p.G);
-        return base + t1 >= first && (W == 0 || base + t0 - W + 1 <= last);
-    };
-    auto sees_stage = [&](int qb, int st) {
-        const int first = (s0 + st) * kMwKeys;
-        return sees(qb, first, min(first + kMwKeys, L) - 1);
-    };
-    auto sees_run = [&](int qb) { return sees(qb, s0 * kMwKeys, min((s0 + ns) * kMwKeys, L) - 1); };
-
-    if (many)
-        for (int i = tid; i < ns * 2 * kMwKeys; i += kMwThreads) reinterpret_cast<float2 *>(s_acc)[i] = make_float2(0.f, 0.f);
-    if (warp == 9) {
+    if (warp == kEpi + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
                      "r"(static_cast<uint32_t>(2 * N)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -318,153 +367,76 @@ __global__ void __launch_bounds__(kMwThreads, MwLayout<N>::kCtas)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tmem;
-    const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
 
     bool failed = false;
-    if (warp == 8) {
-        // ---- TMA: the whole warp; lane u issues tile u of a key stage
+    if (warp == kEpi) {
+        // ---- TMA
         const uint64_t policy = evict_first_policy();
-        int ki = 0, qi = 0;  // key stages and query blocks issued
-        auto wait_all = [&](uint32_t bar, uint32_t parity) {
-            return !__any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity));
-        };
-        auto load_keys = [&](int st) {
-            const int slot = ki % kRing;
-            if (ki >= kRing && !wait_all(k_empty + 8 * slot, ((ki / kRing) - 1) & 1)) return false;
-            const int pt = (s0 + st) * kMwTiles + lane;
-            int page = -1;
-            if (lane < kMwTiles && pt * kPage < L) page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + pt);
-            const bool ok = page >= 0 && page < p.num_pages;  // (other cells are not added to)
-            const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
-            if (lane == 0) mbar_expect_tx(k_full + 8 * slot, cnt * kTileBytes);
-            __syncwarp();
-            if (ok) tma_load_3d(k_s + slot * kMwKBytes + lane * kTileBytes, &tmk, 0, 0, page * p.Hkv + g, k_full + 8 * slot, policy);
-            ++ki;
-            return true;
-        };
-        for (int st = 0; many && st < ns; ++st) load_keys(st);  // (no more than the ring holds)
-        for (int qb = 0; qb < nqb && !failed; ++qb) {
-            if (!sees_run(qb)) continue;
-            const int slot = qi % kQSlots;
-            if (qi >= kQSlots && !wait_all(q_empty + 8 * slot, ((qi / kQSlots) - 1) & 1)) {
+        if (lane == 0) {
+            mbar_expect_tx(q_full, N * kD * 2 + N * 4);
+            tma_load_3d_plain(q_s, &tmq, 0, g * p.G, b * p.T, q_full);
+            bulk_load(smem_addr(s_lse), p.nlse + (static_cast<size_t>(b) * p.Hkv + g) * p.lse_ld, N * 4, q_full);
+        }
+        __syncwarp();
+        int st = 0;
+        for (; st < ns; ++st) {
+            const int slot = st % kRing;
+            if (st >= kRing && !warp_wait(k_empty + 8 * slot, ((st / kRing) - 1) & 1)) {
                 failed = true;
                 break;
             }
-            if (lane == 0) {
-                mbar_expect_tx(q_full + 8 * slot, Lay::kQBytes + N * 4);
-                tma_load_3d_plain(q_s + slot * Lay::kQBytes, &tmq, 0, g * p.G, b * p.T + qb * N / p.G, q_full + 8 * slot);
-                bulk_load(smem_addr(s_lse + slot * N), p.nlse + bg * p.lse_ld + qb * N, N * 4, q_full + 8 * slot);
-            }
-            ++qi;
-            __syncwarp();
-            for (int st = 0; !many && st < ns; ++st)
-                if (sees_stage(qb, st) && !load_keys(st)) {
-                    failed = true;
-                    break;
-                }
+            mw_load_keys(p, &tmk, b, g, k.L, (s0 + st) * kMwKeys, kMwTiles, k_s + slot * kMwKBytes, k_full + 8 * slot, policy, lane);
         }
         // nothing may still be landing when the CTA leaves
-        for (int j = max(0, ki - kRing); j < ki; ++j) wait_all(k_full + 8 * (j % kRing), (j / kRing) & 1);
-        for (int j = max(0, qi - kQSlots); j < qi; ++j) wait_all(q_full + 8 * (j % kQSlots), (j / kQSlots) & 1);
-    } else if (warp == 9) {
-        // ---- MMA issue
+        for (int j = max(0, st - kRing); j < st; ++j) warp_wait(k_full + 8 * (j % kRing), (j / kRing) & 1);
+        warp_wait(q_full, 0);
+    } else if (warp == kEpi + 1) {
+        // ---- products
         if (lane == 0) {
             const uint32_t idesc = umma_idesc_bf16(kMwKeys, N, false);
-            int it = 0, ki = 0, qi = 0;
-            for (int qb = 0; qb < nqb && !failed; ++qb) {
-                if (!sees_run(qb)) continue;
-                const int qs = qi % kQSlots;
-                if (!mbar_wait_bounded(q_full + 8 * qs, (qi / kQSlots) & 1)) {
-                    failed = true;
-                    break;
-                }
-                for (int st = 0; st < ns; ++st) {
-                    if (!sees_stage(qb, st)) continue;
-                    const int slot = many ? st : ki % kRing, buf = it & 1;
-                    if (!mbar_wait_bounded(k_full + 8 * slot, many ? 0u : (ki / kRing) & 1) ||
-                        (it >= 2 && !mbar_wait_bounded(t_empty + 8 * buf, ((it >> 1) - 1) & 1))) {
-                        failed = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t ka = k_s + slot * kMwKBytes, qa = q_s + qs * Lay::kQBytes;
-#pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk)
-                        umma_bf16_ss(tm + buf * N, umma_sdesc(ka + 32 * kk, 16, 1024), umma_sdesc(qa + 32 * kk, 16, 1024),
-                                     idesc, kk > 0);
-                    umma_commit(t_full + 8 * buf);
-                    if (!many) umma_commit(k_empty + 8 * slot);
-                    ++it;
-                    ++ki;
-                }
-                umma_commit(q_empty + 8 * qs);
-                ++qi;
-            }
-            umma_commit(drain);  // completes when every product issued above has
-        }
-    } else {
-        // ---- exponentials and sums: key 32 (warp % 4) + lane of each stage, half warp / 4 of the columns
-        const int w = warp & 3, half = warp >> 2;
-        const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
-        int it = 0, qi = 0;
-        for (int qb = 0; qb < nqb && !failed; ++qb) {
-            if (!sees_run(qb)) continue;
-            const int qs = qi % kQSlots;
-            if (__any_sync(0xffffffffu, !mbar_wait_bounded(q_full + 8 * qs, (qi / kQSlots) & 1))) {
-                failed = true;
-                break;
-            }
-            const float *nlse = s_lse + qs * N + half * kHalf;
-            const int r0 = qb * N + half * kHalf;  // the rows of this warp's columns
-            for (int st = 0; st < ns; ++st) {
-                if (!sees_stage(qb, st)) continue;
-                const int buf = it & 1;
-                if (__any_sync(0xffffffffu, !mbar_wait_bounded(t_full + 8 * buf, (it >> 1) & 1))) {
+            if (!mbar_wait_bounded(q_full, 0)) failed = true;
+            for (int st = 0; st < ns && !failed; ++st) {
+                const int slot = st % kRing, buf = st & 1;
+                if (!mbar_wait_bounded(k_full + 8 * slot, (st / kRing) & 1) ||
+                    (st >= 2 && !mbar_wait_bounded(t_empty + 8 * buf, ((st >> 1) - 1) & 1))) {
                     failed = true;
                     break;
                 }
                 tc_fence_after();
-                ++it;
-                // rows that see key j: t >= j - base, t < n, t < j - base + W
-                const int j = (s0 + st) * kMwKeys + 32 * w + lane;
-                const int t_lo = max(0, j - base), t_hi = W > 0 ? min(n, j - base + W) : n;
-                const int lo = t_lo * p.G - r0, hi = j < L ? max(t_lo, t_hi) * p.G - r0 : lo;
-                const bool all = __all_sync(0xffffffffu, lo <= 0 && hi >= kHalf);
-                const bool any = __any_sync(0xffffffffu, lo < kHalf && hi > 0 && lo < hi);
-                const uint32_t ta = tm + lanes + buf * N + half * kHalf;
-                float sum = 0.f;
-                if (any) {
-                    uint32_t v[2][CH];
-                    if constexpr (CH == 32) tmem_ld32(ta, v[0]);
-                    else tmem_ld16(ta, v[0]);
+                const uint32_t ka = k_s + slot * kMwKBytes;
 #pragma unroll
-                    for (int c = 0; c < kHalf / CH; ++c) {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < CH; ++i) asm volatile("" : "+r"(v[c & 1][i]));  // (not used before the wait)
-                        if constexpr (CH == 32)
-                            if (c + 1 < kHalf / CH) tmem_ld32(ta + 32 * (c + 1), v[(c + 1) & 1]);
-                        sum += all ? sum_columns<CH, false>(v[c & 1], nlse + CH * c, p.scale_log2, 0, CH)
-                                   : sum_columns<CH, true>(v[c & 1], nlse + CH * c, p.scale_log2, lo - CH * c, hi - CH * c);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(t_empty + 8 * buf);
-                const int at = (st * 2 + half) * kMwKeys + 32 * w + lane;
-                if (many) {  // compensated: .x the sum, .y what its additions have lost
-                    float2 a = reinterpret_cast<float2 *>(s_acc)[at];
-                    const float y = sum - a.y, t = a.x + y;
-                    a.y = (t - a.x) - y;
-                    a.x = t;
-                    reinterpret_cast<float2 *>(s_acc)[at] = a;
-                } else {
-                    s_acc[at] = sum;
-                }
+                for (int kk = 0; kk < kD / 16; ++kk)
+                    umma_bf16_ss(tm + buf * N, umma_sdesc(ka + 32 * kk, 16, 1024), umma_sdesc(q_s + 32 * kk, 16, 1024), idesc,
+                                 kk > 0);
+                umma_commit(t_full + 8 * buf);
+                umma_commit(k_empty + 8 * slot);
             }
+            umma_commit(drain);  // completes when every product issued above has
+        }
+    } else {
+        // ---- exponentials and sums: key 32 (warp % 4) + lane of each stage, share warp / 4 of the columns
+        const int w = warp & 3, c0 = (warp >> 2) * kCols;
+        const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
+        if (!warp_wait(q_full, 0)) failed = true;
+        for (int st = 0; st < ns && !failed; ++st) {
+            const int buf = st & 1;
+            if (!warp_wait(t_full + 8 * buf, (st >> 1) & 1)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            const int2 rows = rows_of_key(p, k, (s0 + st) * kMwKeys + 32 * w + lane);
+            const int lo = rows.x - c0, hi = rows.y - c0;
+            const uint32_t ta = tm + lanes + buf * N + c0;
+            float sum = 0.f;
+            if (__all_sync(0xffffffffu, lo <= 0 && hi >= kCols))
+                sum = sum_tmem<kCols, false>(ta, s_lse + c0, p.scale_log2, 0, kCols);
+            else if (__any_sync(0xffffffffu, lo < kCols && hi > 0 && lo < hi))
+                sum = sum_tmem<kCols, true>(ta, s_lse + c0, p.scale_log2, lo, hi);
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_empty + 8 * qs);
-            ++qi;
+            if (lane == 0) mbar_arrive(t_empty + 8 * buf);
+            s_acc[(st * Lay::kParts + (warp >> 2)) * kMwKeys + 32 * w + lane] = sum;
         }
     }
     if (failed) {
@@ -472,32 +444,197 @@ __global__ void __launch_bounds__(kMwThreads, MwLayout<N>::kCtas)
         s_failed = 1;
     }
 
-    // ---- every product done before TMEM is released, every sum before it is added
-    if (tid == 9 * 32) mbar_wait_bounded(drain, 0);
+    // ---- every product done before TMEM is released, every sum made before it is added
+    if (tid == (kEpi + 1) * 32) mbar_wait_bounded(drain, 0);
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kEpi + 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(static_cast<uint32_t>(2 * N)));
     }
     if (s_failed) return;
-    for (int i = tid; i < ns * kMwKeys; i += kMwThreads) {
-        const int st = i / kMwKeys, j = s0 * kMwKeys + i;
-        if (j >= L || j < lo0) continue;
-        const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + j / kPage);
-        if (page < 0 || page >= p.num_pages) continue;
-        const int at = st * 2 * kMwKeys + i % kMwKeys;
-        float sum;
-        if (many) {
-            const float2 a = reinterpret_cast<const float2 *>(s_acc)[at], c = reinterpret_cast<const float2 *>(s_acc)[at + kMwKeys];
-            sum = (a.x + c.x) - (a.y + c.y);
-        } else {
-            sum = s_acc[at] + s_acc[at + kMwKeys];
+    mw_add(p, k, b, g, s0 * kMwKeys, ns * kMwKeys, [&](int i) {
+        const float *a = s_acc + (i / kMwKeys) * Lay::kParts * kMwKeys + i % kMwKeys;
+        float sum = a[0];
+#pragma unroll
+        for (int q = 1; q < Lay::kParts; ++q) sum += a[q * kMwKeys];
+        return sum;
+    });
+}
+
+template <int TILES>
+struct SrLayout {
+    static constexpr int kEpi = 8 * TILES;                      // two groups of four warps per 128 keys
+    static constexpr int kThreads = (kEpi + 2) * 32;
+    static constexpr int kCtas = TILES == 2 ? 1 : 2;            // resident per SM
+    static constexpr int kSlots = TILES == 2 ? 6 : 3;
+    static constexpr int kQBytes = kMwRowBlock * kD * 2;
+    static constexpr int k = kSlots * kQBytes;
+    static constexpr int lse = k + TILES * kMwKBytes;
+    static constexpr int acc = lse + kSlots * kMwRowBlock * 4;
+    static constexpr int bars = acc + TILES * 2 * kMwKeys * 8;
+    static constexpr int bytes = 1024 + bars + (2 * kSlots + 6) * 8;  // with the slack to align the base
+    static constexpr uint32_t kCols = 2 * TILES * kMwRowBlock;        // TMEM: two buffers
+    static_assert(k % 1024 == 0 && acc % 16 == 0 && bars % 8 == 0, "alignment");
+    static_assert(kCtas * (bytes + 1024) <= 233472, "shared memory of the CTAs on one SM");
+};
+
+// One CTA per (sequence, KV head, 128 TILES keys). A key's sum over thousands of rows is kept as a
+// compensated sum over the blocks (terms one after another in 32 bits would lose the last bits).
+template <int TILES>
+__global__ void __launch_bounds__(SrLayout<TILES>::kThreads, SrLayout<TILES>::kCtas)
+    stream_rows_weights_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmq,
+                               const WeightParams p) {
+    using Lay = SrLayout<TILES>;
+    constexpr int kSlots = Lay::kSlots, kEpi = Lay::kEpi, kCols = kMwRowBlock / 2, kKeys = TILES * kMwKeys;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t q_s = smem_addr(smem), k_s = q_s + Lay::k;
+    float *const s_lse = reinterpret_cast<float *>(smem + Lay::lse);
+    float2 *const s_acc = reinterpret_cast<float2 *>(smem + Lay::acc);
+    const uint32_t k_full = smem_addr(smem + Lay::bars), q_full = k_full + 8, q_empty = q_full + 8 * kSlots;
+    const uint32_t t_full = q_empty + 8 * kSlots, t_empty = t_full + 16, drain = t_empty + 16;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_failed;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = blockIdx.y, b = blockIdx.z;
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmq)) : "memory");
+        mbar_init(k_full, 1);
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(q_full + 8 * s, 1);
+            mbar_init(q_empty + 8 * s, kEpi + 1);  // the products, and the warps that read the denominators
         }
-        float *dst = p.weights + (static_cast<size_t>(page) * p.Hkv + g) * kPage + j % kPage;
-        if (p.assign_new && j >= base)
-            *dst = sum;
-        else
-            atomicAdd(dst, sum);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(t_full + 8 * s, 1);
+            mbar_init(t_empty + 8 * s, kEpi);
+        }
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_failed = 0;
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const MwKeys k = mw_keys(p, b);
+    if (!k.ok) return;
+    const int first = k.lo0 / kMwKeys * kMwKeys + blockIdx.x * kKeys;
+    if (first >= k.L) return;
+    // the blocks of rows that see one of the keys
+    const int last = min(first + kKeys, k.L) - 1;
+    const int t0 = max(0, first - k.base), t1 = p.window > 0 ? min(k.n - 1, last - k.base + p.window - 1) : k.n - 1;
+    const int qb0 = t0 * p.G / kMwRowBlock, nb = max(0, (t1 * p.G + p.G - 1) / kMwRowBlock - qb0 + 1);
+    if (warp == kEpi + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
+                     "r"(Lay::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s_tmem;
+
+    bool failed = false;
+    if (warp == kEpi) {
+        // ---- TMA
+        mw_load_keys(p, &tmk, b, g, k.L, first, TILES * kMwTiles, k_s, k_full, evict_first_policy(), lane);
+        int i = 0;
+        for (; i < nb; ++i) {
+            const int slot = i % kSlots;
+            if (i >= kSlots && !warp_wait(q_empty + 8 * slot, ((i / kSlots) - 1) & 1)) {
+                failed = true;
+                break;
+            }
+            if (lane == 0) {
+                const int r0 = (qb0 + i) * kMwRowBlock;
+                mbar_expect_tx(q_full + 8 * slot, Lay::kQBytes + kMwRowBlock * 4);
+                tma_load_3d_plain(q_s + slot * Lay::kQBytes, &tmq, 0, g * p.G, b * p.T + r0 / p.G, q_full + 8 * slot);
+                bulk_load(smem_addr(s_lse + slot * kMwRowBlock), p.nlse + (static_cast<size_t>(b) * p.Hkv + g) * p.lse_ld + r0,
+                          kMwRowBlock * 4, q_full + 8 * slot);
+            }
+            __syncwarp();
+        }
+        // nothing may still be landing when the CTA leaves
+        warp_wait(k_full, 0);
+        for (int j = max(0, i - kSlots); j < i; ++j) warp_wait(q_full + 8 * (j % kSlots), (j / kSlots) & 1);
+    } else if (warp == kEpi + 1) {
+        // ---- products
+        if (lane == 0) {
+            const uint32_t idesc = umma_idesc_bf16(kMwKeys, kMwRowBlock, false);
+            if (!mbar_wait_bounded(k_full, 0)) failed = true;
+            for (int i = 0; i < nb && !failed; ++i) {
+                const int slot = i % kSlots, buf = i & 1;
+                if (!mbar_wait_bounded(q_full + 8 * slot, (i / kSlots) & 1) ||
+                    (i >= 2 && !mbar_wait_bounded(t_empty + 8 * buf, ((i >> 1) - 1) & 1))) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t qa = q_s + slot * Lay::kQBytes;
+#pragma unroll
+                for (int m = 0; m < TILES; ++m)
+#pragma unroll
+                    for (int kk = 0; kk < kD / 16; ++kk)
+                        umma_bf16_ss(tm + (buf * TILES + m) * kMwRowBlock, umma_sdesc(k_s + m * kMwKBytes + 32 * kk, 16, 1024),
+                                     umma_sdesc(qa + 32 * kk, 16, 1024), idesc, kk > 0);
+                umma_commit(t_full + 8 * buf);
+                umma_commit(q_empty + 8 * slot);
+            }
+            umma_commit(drain);  // completes when every product issued above has
+        }
+    } else {
+        // ---- exponentials and sums: one key per thread, half of each block's columns
+        const int m = warp >> 3, half = (warp >> 2) & 1, w = warp & 3, c0 = half * kCols;
+        const int2 rows = rows_of_key(p, k, first + m * kMwKeys + 32 * w + lane);
+        // rows seen by all of the warp's keys, and by any of them
+        const int all_lo = __reduce_max_sync(0xffffffffu, rows.x), all_hi = __reduce_min_sync(0xffffffffu, rows.y);
+        const int any_lo = __reduce_min_sync(0xffffffffu, rows.x), any_hi = __reduce_max_sync(0xffffffffu, rows.y);
+        const uint32_t ta0 = tm + (static_cast<uint32_t>(32 * w) << 16) + m * kMwRowBlock + c0;
+        float sum = 0.f, lost = 0.f;  // compensated: what the additions to sum have lost
+        for (int i = 0; i < nb; ++i) {
+            const int slot = i % kSlots, buf = i & 1;
+            // (the denominators came with the rows: their barrier has completed, this wait makes them visible)
+            if (!warp_wait(t_full + 8 * buf, (i >> 1) & 1) || !warp_wait(q_full + 8 * slot, (i / kSlots) & 1)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            const int r0 = (qb0 + i) * kMwRowBlock + c0;
+            const uint32_t ta = ta0 + buf * TILES * kMwRowBlock;
+            const float *nlse = s_lse + slot * kMwRowBlock + c0;
+            float add = 0.f;
+            if (r0 >= all_lo && r0 + kCols <= all_hi)
+                add = sum_tmem<kCols, false>(ta, nlse, p.scale_log2, 0, kCols);
+            else if (r0 < any_hi && r0 + kCols > any_lo)
+                add = sum_tmem<kCols, true>(ta, nlse, p.scale_log2, rows.x - r0, rows.y - r0);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(t_empty + 8 * buf);
+                mbar_arrive(q_empty + 8 * slot);
+            }
+            const float y = add - lost, t = sum + y;
+            lost = (t - sum) - y;
+            sum = t;
+        }
+        s_acc[(m * 2 + half) * kMwKeys + 32 * w + lane] = make_float2(sum, lost);
+    }
+    if (failed) {
+        flag_status(DA_STATUS_TIMEOUT);
+        s_failed = 1;
+    }
+
+    // ---- every product done before TMEM is released, every sum made before it is added
+    if (tid == (kEpi + 1) * 32) mbar_wait_bounded(drain, 0);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kEpi + 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(Lay::kCols));
+    }
+    if (s_failed) return;
+    mw_add(p, k, b, g, first, kKeys, [&](int i) {
+        const float2 a = s_acc[i / kMwKeys * 2 * kMwKeys + i % kMwKeys], c = s_acc[(i / kMwKeys * 2 + 1) * kMwKeys + i % kMwKeys];
+        return (a.x + c.x) - (a.y + c.y);
+    });
 }
