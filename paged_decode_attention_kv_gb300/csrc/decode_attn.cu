@@ -2202,7 +2202,7 @@ struct DeviceState {
     std::atomic<int> sm_count{0};
     std::atomic<bool> attr_set[128] = {};
     std::atomic<bool> multi_attr_set[8] = {};
-    std::atomic<bool> evict_attr_set[2] = {};
+    std::atomic<int> evict_clusters[2] = {-1, -1};  // resident clusters of 16 of the eviction kernel, -1: not asked yet
     std::atomic<bool> mw_attr_set[6] = {};
 };
 DeviceState g_dev[kMaxDevices];
@@ -2871,11 +2871,12 @@ size_t lse_bytes(const da_shape &s, int T) {
     return (n + 255) & ~static_cast<size_t>(255);
 }
 
-// The weights workspace: the denominators, and for a one-token call (T = 0) its scores, 16 tokens
-// and G heads per tile of the longest sequences.
+// The weights workspace: the evictions' histograms (zero at rest, which no other call touches), the
+// denominators, and for a one-token call (T = 0) its scores, 16 tokens and G heads per tile of
+// the longest sequences.
 size_t weights_bytes(const da_shape &s, int T, int max_seq_len) {
     const size_t tiles = T == 0 ? (static_cast<size_t>(max_seq_len) + kPage - 1) / kPage : 0;
-    return lse_bytes(s, T) + static_cast<size_t>(s.batch) * s.num_q_heads * tiles * kPage * sizeof(float);
+    return kEvHistBytes + lse_bytes(s, T) + static_cast<size_t>(s.batch) * s.num_q_heads * tiles * kPage * sizeof(float);
 }
 
 // The weights workspace of a call on `stream`; *captured: the stream is capturing a graph.
@@ -3010,8 +3011,8 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     WeightsOut wo{nullptr, lse_rows(s, T), nullptr, false};
     rc = prepare_weights(dev, stream, weights_bytes(s, T, max_seq_len), &ws, &wo.captured);
     if (rc != DA_OK) return rc;
-    wo.nlse = static_cast<float *>(ws);
-    wo.scores = reinterpret_cast<float *>(static_cast<char *>(ws) + lse_bytes(s, T));
+    wo.nlse = reinterpret_cast<float *>(static_cast<char *>(ws) + kEvHistBytes);
+    wo.scores = wo.nlse + lse_bytes(s, T) / sizeof(float);
     rc = attention(s, &wo);
     if (rc != DA_OK || max_seq_len == 0) return rc;
 
@@ -3071,12 +3072,38 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
 
 // ------------------------------------------------------------------ eviction: host side
 size_t evict_bytes(const da_shape &s, int keep) {
-    return static_cast<size_t>(s.batch) * s.num_kv_heads * keep * 2 * sizeof(int2);
+    return kEvHistBytes + static_cast<size_t>(s.batch) * s.num_kv_heads * evict_list_ints(keep) * sizeof(int);
 }
 
 bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
     return x < y + nb && y < x + na;
+}
+
+// How many clusters of 16 CTAs (beyond the portable 8) of the kernel's largest size the device
+// holds at once; 0 where it takes none.
+template <typename Kernel>
+int evict_clusters_of_16(Kernel kern) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kEvMaxCluster);
+    cfg.blockDim = dim3(kEvMaxWarps * 32);
+    cfg.dynamicSmemBytes = kEvMaxKeys * 4;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kEvMaxCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
 }
 
 int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int32_t *block_table,
@@ -3113,7 +3140,8 @@ int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int3
     p.seq_lens = seq_lens;
     p.new_lens = new_lens;
     p.kept = kept;
-    p.lists = static_cast<int2 *>(ws);
+    p.hist = static_cast<uint32_t *>(ws);
+    p.lists = reinterpret_cast<int *>(static_cast<char *>(ws) + kEvHistBytes);
     p.Hkv = s.num_kv_heads;
     p.keep = keep;
     p.first = keep_first;
@@ -3121,22 +3149,27 @@ int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int3
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.max_seq_len = max_seq_len;
-    // CTAs per (sequence, KV head): as many as fill the GPU's SMs twice, each with at least a
-    // chunk of cells per warp
-    const int pairs = s.batch * s.num_kv_heads;
-    int C = 1;
-    while (C < kEvMaxCluster && 2 * C * pairs <= 2 * sm_count(dev) && 2 * C * kEvThreads <= max_seq_len) C *= 2;
-    const int chunks = (max_seq_len + 31) / 32, cpw = (chunks + C * kEvWarps - 1) / (C * kEvWarps);
-    p.key_cap = std::min<long long>(static_cast<long long>(kEvThreads) * std::max(cpw, 1), kEvMaxKeys);
+    // CTAs of 8 warps when there are several per SM, larger ones and clusters of them when there
+    // are not; at least a chunk of cells per warp
+    const int pairs = s.batch * s.num_kv_heads, sms = sm_count(dev);
+    const int warps = pairs >= 2 * sms ? 8 : pairs >= sms ? 16 : kEvMaxWarps;
     auto kern = kv8 ? kv_evict_kernel<true> : kv_evict_kernel<false>;
-    if (!g_dev[dev].evict_attr_set[kv8].load(std::memory_order_acquire)) {
+    int of16 = g_dev[dev].evict_clusters[kv8].load(std::memory_order_acquire);
+    if (of16 < 0) {  // first use on this device: shared memory, and clusters of 16
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvMaxKeys * 4);
         if (e != cudaSuccess) return set_cuda_error(e);
-        g_dev[dev].evict_attr_set[kv8].store(true, std::memory_order_release);
+        of16 = evict_clusters_of_16(kern);
+        g_dev[dev].evict_clusters[kv8].store(of16, std::memory_order_release);
     }
+    // (clusters of 16 only if all are resident at once: a second wave takes as long as the first)
+    const int most = pairs <= of16 ? kEvMaxCluster : 8;
+    int C = 1;
+    while (C < most && 2 * C * pairs <= sms && pairs <= kEvClusterPairs && 2 * C * warps * 32 <= max_seq_len) C *= 2;
+    const int chunks = (max_seq_len + 31) / 32, cpw = (chunks + C * warps - 1) / (C * warps);
+    p.key_cap = std::min<long long>(32ll * warps * std::max(cpw, 1), kEvMaxKeys);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C, s.num_kv_heads, s.batch);
-    cfg.blockDim = dim3(kEvThreads);
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = static_cast<size_t>(p.key_cap) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -10,31 +10,49 @@
 // One cluster of CTAs per (sequence, KV head), the warps of the cluster holding consecutive
 // runs of cells:
 //   1. weights -> order-preserving 32-bit keys (in shared memory when they fit)
-//   2. the n-th largest key by four 8-bit histogram rounds, the CTAs' histograms added up
-//      through distributed shared memory
+//   2. the n-th largest key by up to three histogram rounds (11, 11 and 10 bits; the first digit
+//      then holds two bits of the mantissa, so that weights of a few octaves do not all count
+//      in a few bins); the CTAs of a cluster add theirs up in global memory (L2: every CTA reading
+//      all 2048 bins of all others through distributed shared memory took 5 us a round)
 //   3. tallies per warp, their prefix over the cluster: every warp knows how many ties, holes
 //      and surplus cells lie before its run
-//   4. each warp lists its holes and surplus cells, in order (workspace)
-//   5. surplus -> holes: sources and destinations are disjoint, all moves at once
+//   4. each warp lists its holes and surplus cells, in order (workspace): a lane has the ballots of
+//      one 32-cell chunk, so the lists cost a few instructions per cell listed, not per cell
+//   5. surplus -> holes: sources and destinations are disjoint, all moves at once. fp8 blocks hold V
+//      transposed, a token's V in 64 places: there a warp takes a destination tile, puts the
+//      sources' bytes into its rows in registers and writes the tile's rows once (a byte store
+//      per value took twice as long)
 //   6. the last r cells, a round of rows at a time: read, cluster barrier, write. A source lies
 //      above its destination, so a round's writes never touch a later round's sources.
 // Bound by HBM on the moved rows and the weights, by the rounds' latency when few cells move.
 
-constexpr int kEvWarps = 16;
-constexpr int kEvThreads = kEvWarps * 32;
-constexpr int kEvMaxCluster = 8;                // portable cluster size
+// CTAs have 8, 16 or 32 warps: many small ones, so that one's selection overlaps another's moves
+// (64 registers: four of 8 warps on an SM), or clusters of large ones for a few long sequences.
+constexpr int kEvMaxWarps = 32;
+constexpr int kEvMaxCluster = 16;               // (over 8: where the device takes it)
 constexpr int kEvMaxKeys = 48 * 1024;           // keys one CTA holds in shared memory at most
 constexpr int kEvUnroll = 4;                    // rows in flight per half-warp
+constexpr int kEvTileUnroll = 4;                // fp8: sources in flight per warp
+constexpr int kEvLoad = 16;                     // weights in flight per lane
+constexpr int kEvBins = 2048;
+constexpr int kEvClusterPairs = kMaxSms / 2;    // clusters have two CTAs or more, at most one per SM
+constexpr size_t kEvHistBytes = static_cast<size_t>(kEvClusterPairs) * 3 * kEvBins * 4;  // ahead of the workspace
 
 struct EvictParams {
     uint8_t *k_cache, *v_cache;  // fp8: k_cache holds the blocks
     float *weights;              // [num_pages][Hkv][16]
     const int *block_table, *seq_lens;
     int *new_lens, *kept;        // [B], [B][Hkv][keep]
-    int2 *lists;                 // [B * Hkv][2][keep]: holes, surplus, as (cell, page)
+    int *lists;                  // [B * Hkv][evict_list_ints(keep)]: holes, surplus cells, and for each
+                                 // tile the number of holes before it
+    uint32_t *hist;              // clusters: [B * Hkv][3][kEvBins], zero at rest
     int Hkv, keep, first, last, max_pages, num_pages, max_seq_len;
     int key_cap;                 // keys a CTA's shared memory holds
 };
+
+__host__ __device__ constexpr size_t evict_list_ints(int keep) {
+    return 2 * static_cast<size_t>(keep) + (keep + kPage - 1) / kPage;
+}
 
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -106,19 +124,20 @@ __device__ __forceinline__ void ev_store(const EvictParams &p, const EvRow<KV8> 
 }
 
 template <bool KV8>
-__global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictParams p) {
     extern __shared__ uint32_t s_key[];
-    __shared__ uint32_t s_hist[4][256];
-    __shared__ int4 s_tally[kEvWarps];                   // gt_lo, eq_lo, gt_hi, eq_hi of each warp
-    __shared__ int4 s_all[kEvWarps * kEvMaxCluster];     // the cluster's tallies, then the prefixes
-    __shared__ uint32_t s_wsum[8];
-    __shared__ uint32_t s_digit, s_want;
+    __shared__ uint32_t s_hist[2][kEvBins];
+    __shared__ int4 s_tally[kEvMaxWarps];                  // gt_lo, eq_lo, gt_hi, eq_hi of each warp
+    __shared__ int4 s_all[kEvMaxWarps * kEvMaxCluster];    // the cluster's tallies, then the prefixes
+    __shared__ uint32_t s_wsum[kEvMaxWarps];
+    __shared__ uint32_t s_digit, s_want, s_cnt;
     __shared__ int s_moves;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int C = gridDim.x, rank = blockIdx.x;          // the cluster spans the grid's x
+    const int nt = blockDim.x, nwarps = nt >> 5;
+    const int C = gridDim.x, rank = blockIdx.x;            // the cluster spans the grid's x
     const int g = blockIdx.y, b = blockIdx.z;
-    for (int i = tid; i < 4 * 256; i += kEvThreads) (&s_hist[0][0])[i] = 0u;
+    for (int i = tid; i < 2 * kEvBins; i += nt) (&s_hist[0][0])[i] = 0u;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const size_t pair = static_cast<size_t>(b) * p.Hkv + g;
@@ -130,123 +149,213 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictParams 
     }
     if (tid == 0 && rank == 0 && g == 0) p.new_lens[b] = min(L, p.keep);
     if (L <= p.keep) {  // (every CTA of the cluster leaves here or none)
-        for (int i = rank * kEvThreads + tid; i < p.keep; i += C * kEvThreads) kept[i] = i < L ? i : -1;
+        for (int i = rank * nt + tid; i < p.keep; i += C * nt) kept[i] = i < L ? i : -1;
         return;
     }
     const int f = p.first, r = p.last, n = p.keep - f - r;
-    const int m0 = f, m1 = L - r, low = f + n;           // the middle cells, and where they may stay
+    const int m0 = f, m1 = L - r, low = f + n;             // the middle cells, and where they may stay
     const int *const bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
 
     // ---- 1. this warp's run of cells [c0, c1) (32 at a time), the CTA's first cell
-    const int chunks = (L + 31) / 32, cpw = (chunks + C * kEvWarps - 1) / (C * kEvWarps);
-    const int cta0 = rank * kEvWarps * cpw * 32;
+    const int chunks = (L + 31) / 32, cpw = (chunks + C * nwarps - 1) / (C * nwarps);
+    const int cta0 = rank * nwarps * cpw * 32;
     const int c0 = cta0 + warp * cpw * 32, c1 = min(c0 + cpw * 32, L);
-    const bool resident = kEvWarps * cpw * 32 <= p.key_cap;
+    const bool resident = nwarps * cpw * 32 <= p.key_cap;
     auto page_of = [&](int cell) {
         const int page = __ldg(bt + cell / kPage);
         return page >= 0 && page < p.num_pages ? page : -1;
     };
-    auto load_key = [&](int cell) -> uint32_t {
-        const int page = page_of(cell);
-        if (page < 0) {
-            flag_status(DA_STATUS_BAD_PAGE);
-            return 0u;
-        }
-        return weight_key(p.weights[(static_cast<size_t>(page) * p.Hkv + g) * kPage + cell % kPage]);
+    auto key_at = [&](int cell, int page) {
+        return page < 0 ? 0u : weight_key(p.weights[(static_cast<size_t>(page) * p.Hkv + g) * kPage + cell % kPage]);
     };
-    auto key_of = [&](int cell) { return resident ? s_key[cell - cta0] : load_key(cell); };
+    auto key_of = [&](int cell) { return resident ? s_key[cell - cta0] : key_at(cell, page_of(cell)); };
+    uint32_t *const ghist = p.hist + pair * (3 * kEvBins);
+    int rounds = 0;                                        // histogram rounds made
     __syncthreads();  // (the histograms are zero)
-#pragma unroll 4
-    for (int c = c0 + lane; c < c1; c += 32) {
-        const uint32_t key = load_key(c);
-        if (resident) s_key[c - cta0] = key;
-        if (c >= m0 && c < m1) atomicAdd(&s_hist[0][key >> 24], 1u);
+    for (int cb = c0; cb < c1; cb += 512) {                // 16 chunks: their 32 pages at once, one per lane
+        int pages = -1;
+        if (cb + 16 * lane < c1) {
+            pages = page_of(cb + 16 * lane);
+            if (pages < 0) flag_status(DA_STATUS_BAD_PAGE);
+        }
+#pragma unroll
+        for (int u = 0; u < 16; u += kEvLoad) {
+            if (cb + 32 * u >= c1) break;
+            uint32_t key[kEvLoad];
+#pragma unroll
+            for (int k = 0; k < kEvLoad; ++k) {
+                const int cell = cb + 32 * (u + k) + lane;
+                const int page = __shfl_sync(0xffffffffu, pages, 2 * (u + k) + (lane >> 4));
+                key[k] = cell < c1 ? key_at(cell, page) : 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < kEvLoad; ++k) {
+                const int cell = cb + 32 * (u + k) + lane;
+                if (cell < c1) {
+                    if (resident) s_key[cell - cta0] = key[k];
+                    if (cell >= m0 && cell < m1) atomicAdd(&s_hist[0][key[k] >> 21], 1u);
+                }
+            }
+        }
     }
 
-    // ---- 2. the n-th largest key of the middle: thr, and how many cells of exactly that key stay
+    // ---- 2. the n-th largest key of the middle: cells above thr stay, and `ties` of those at it
     uint32_t thr = 0xffffffffu, ties = 0;
     if (n > 0) {
         uint32_t prefix = 0, want = n;
 #pragma unroll 1
-        for (int round = 0; round < 4; ++round) {
-            const int sh = 24 - 8 * round;
+        for (int round = 0; round < 3; ++round) {
+            const int sh = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round < 2 ? 11 : 10;
+            uint32_t *const hist = s_hist[round & 1];
             if (round > 0) {
                 for (int c = c0 + lane; c < c1; c += 32) {
                     const uint32_t key = key_of(c);
-                    if (c >= m0 && c < m1 && (key >> (sh + 8)) == prefix) atomicAdd(&s_hist[round][(key >> sh) & 255u], 1u);
+                    if (c >= m0 && c < m1 && (key >> (sh + bits)) == prefix) atomicAdd(&hist[(key >> sh) & ((1u << bits) - 1u)], 1u);
                 }
             }
-            cluster_sync_all();
-            uint32_t cnt = 0, incl = 0;
-            if (tid < 256) {  // bin 255 - tid, summed over the cluster, scanned from the top
-                const uint32_t a = smem_addr(&s_hist[round][255 - tid]);
-                for (int k = 0; k < C; ++k) cnt += cluster_ld(cluster_map(a, k));
-                incl = cnt;
+            const int per = kEvBins / nt;                  // consecutive bins per thread, from the top
+            uint32_t cnt[8], sum = 0;
+            __syncthreads();
+            rounds = round + 1;
+            if (C > 1) {
+                uint32_t *const all = ghist + round * kEvBins;
+                for (int i = tid; i < kEvBins; i += nt)
+                    if (hist[i] != 0u) atomicAdd(all + i, hist[i]);
+                cluster_sync_all();
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += y;
+                for (int k = 0; k < 8; ++k) cnt[k] = k < per ? __ldcg(all + kEvBins - 1 - (tid * per + k)) : 0u;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) cnt[k] = k < per ? hist[kEvBins - 1 - (tid * per + k)] : 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += cnt[k];
+            uint32_t incl = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            if (lane == 31) s_wsum[warp] = incl;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) incl += s_wsum[w];
+            if (incl >= want && incl - sum < want) {       // exactly one thread: the bin is among its own
+                uint32_t above = incl - sum;
+                bool found = false;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (!found && above + cnt[k] >= want) {
+                        found = true;
+                        s_digit = kEvBins - 1 - (tid * per + k);
+                        s_want = want - above;
+                        s_cnt = cnt[k];
+                    }
+                    above += cnt[k];
                 }
-                if (lane == 31) s_wsum[warp] = incl;
             }
             __syncthreads();
-            if (tid < 256) {
-                for (int w = 0; w < warp; ++w) incl += s_wsum[w];
-                if (incl >= want && incl - cnt < want) {  // exactly one bin
-                    s_digit = 255 - tid;
-                    s_want = want - (incl - cnt);
-                }
-            }
-            __syncthreads();
-            prefix = (prefix << 8) | s_digit;
+            prefix = (prefix << bits) | s_digit;
             want = s_want;
+            if (sh > 0 && s_cnt == want && prefix > 0) {   // the whole bin stays: no need to look into it
+                thr = (prefix << sh) - 1u;
+                break;
+            }
+            if (sh == 0) {
+                thr = prefix;
+                ties = want;
+            } else if (round == 1) {                       // the third round counts where the first did
+                for (int i = tid; i < kEvBins; i += nt) s_hist[0][i] = 0u;
+                __syncthreads();
+            }
         }
-        thr = prefix;
-        ties = want;
     }
 
-    // ---- 3. tallies: keys above and at the threshold, below and beyond `low`
-    int gt_lo = 0, eq_lo = 0, gt_hi = 0, eq_hi = 0;
-    for (int c = c0; c < c1; c += 32) {
-        const int cell = c + lane;
-        const bool mid = cell < c1 && cell >= m0 && cell < m1;
-        const uint32_t key = mid ? key_of(cell) : 0u;
-        const bool lo = cell < low;
-        gt_lo += __popc(__ballot_sync(0xffffffffu, mid && lo && key > thr));
-        eq_lo += __popc(__ballot_sync(0xffffffffu, mid && lo && key == thr));
-        gt_hi += __popc(__ballot_sync(0xffffffffu, mid && !lo && key > thr));
-        eq_hi += __popc(__ballot_sync(0xffffffffu, mid && !lo && key == thr));
+    // ---- 3. tallies: keys above and at the threshold, below and beyond `low`. Lane l holds the masks
+    // of chunk l of the run's block of 32 chunks (a run of more blocks works them out again in 4).
+    auto bits_below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
+    auto block_masks = [&](int cb, uint32_t &gt, uint32_t &eq) {
+        gt = eq = 0u;
+        const int cnt = min(32, (c1 - cb + 31) / 32);
+        for (int i = 0; i < cnt; ++i) {
+            const int cell = cb + 32 * i + lane;
+            const bool mid = cell < c1 && cell >= m0 && cell < m1;
+            const uint32_t key = mid ? key_of(cell) : 0u;
+            const uint32_t g_ = __ballot_sync(0xffffffffu, mid && key > thr), e_ = __ballot_sync(0xffffffffu, mid && key == thr);
+            if (lane == i) {
+                gt = g_;
+                eq = e_;
+            }
+        }
+    };
+    uint32_t gt = 0u, eq = 0u;
+    {
+        int4 t = make_int4(0, 0, 0, 0);
+        for (int cb = c0; cb < c1; cb += 1024) {
+            block_masks(cb, gt, eq);
+            const uint32_t lo = bits_below(low - (cb + 32 * lane));
+            t.x += __popc(gt & lo);
+            t.y += __popc(eq & lo);
+            t.z += __popc(gt & ~lo);
+            t.w += __popc(eq & ~lo);
+        }
+        t.x = __reduce_add_sync(0xffffffffu, t.x);
+        t.y = __reduce_add_sync(0xffffffffu, t.y);
+        t.z = __reduce_add_sync(0xffffffffu, t.z);
+        t.w = __reduce_add_sync(0xffffffffu, t.w);
+        if (lane == 0) s_tally[warp] = t;
     }
-    if (lane == 0) s_tally[warp] = make_int4(gt_lo, eq_lo, gt_hi, eq_hi);
     cluster_sync_all();
-    if (tid < C * kEvWarps) {
-        const uint32_t a = cluster_map(smem_addr(&s_tally[tid % kEvWarps]), tid / kEvWarps);
+    if (C > 1)  // every CTA has read the sums: zero again for the next call
+        for (int i = rank * nt + tid; i < rounds * kEvBins; i += C * nt) ghist[i] = 0u;
+    if (tid < C * nwarps) {
+        const uint32_t a = cluster_map(smem_addr(&s_tally[tid % nwarps]), tid / nwarps);
         s_all[tid] = make_int4(cluster_ld(a), cluster_ld(a + 4), cluster_ld(a + 8), cluster_ld(a + 12));
     }
     __syncthreads();
-    if (warp == 0) {  // ties, holes and surplus cells before each warp's run
-        int eq_run = 0, hole_run = 0, more_run = 0;
-        for (int w0 = 0; w0 < C * kEvWarps; w0 += 32) {
-            const int w = w0 + lane;
-            const int4 t = w < C * kEvWarps ? s_all[w] : make_int4(0, 0, 0, 0);
-            auto scan = [&](int v) {
+    if (warp == 0) {  // ties, holes and surplus cells before each warp's run: consecutive runs per lane
+        constexpr int kPer = 8;
+        auto scan = [&](int v) {                           // exclusive prefix over the lanes
+            int x = v;
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, v, off);
-                    if (lane >= off) v += y;
-                }
-                return v;
-            };
-            const int eq = t.y + t.w, eq_in = scan(eq), eq_before = eq_run + eq_in - eq;
-            const int left = max(0, static_cast<int>(ties) - eq_before);
-            const int eq_kept_lo = min(left, t.y), eq_kept_hi = min(left - eq_kept_lo, t.w);
-            const int a = max(w * cpw * 32, m0), e = min((w + 1) * cpw * 32, low);
-            const int holes = max(0, e - a) - t.x - eq_kept_lo, more = t.z + eq_kept_hi;
-            const int holes_in = scan(holes), more_in = scan(more);
-            if (w < C * kEvWarps) s_all[w] = make_int4(eq_before, hole_run + holes_in - holes, more_run + more_in - more, 0);
-            eq_run += __shfl_sync(0xffffffffu, eq_in, 31);
-            hole_run += __shfl_sync(0xffffffffu, holes_in, 31);
-            more_run += __shfl_sync(0xffffffffu, more_in, 31);
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off) x += y;
+            }
+            return x - v;
+        };
+        int eq_run = 0, hole_run = 0, more_run = 0;
+        for (int first = 0; first < C * nwarps; first += 32 * kPer) {
+            const int w0 = first + lane * kPer;
+            int4 t[kPer];
+            int eq_sum = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                t[k] = w0 + k < C * nwarps ? s_all[w0 + k] : make_int4(0, 0, 0, 0);
+                eq_sum += t[k].y + t[k].w;
+            }
+            int eq_at = eq_run + scan(eq_sum), hole_sum = 0, more_sum = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {               // t becomes (ties before, holes, surplus)
+                const int left = max(0, static_cast<int>(ties) - eq_at);
+                const int eq_lo = min(left, t[k].y), eq_hi = min(left - eq_lo, t[k].w);
+                const int a = max((w0 + k) * cpw * 32, m0), e = min((w0 + k + 1) * cpw * 32, low);
+                const int holes = w0 + k < C * nwarps ? max(0, e - a) - t[k].x - eq_lo : 0, more = t[k].z + eq_hi;
+                const int eq = t[k].y + t[k].w;
+                t[k] = make_int4(eq_at, holes, more, 0);
+                eq_at += eq;
+                hole_sum += holes;
+                more_sum += more;
+            }
+            int hole_at = hole_run + scan(hole_sum), more_at = more_run + scan(more_sum);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                if (w0 + k < C * nwarps) s_all[w0 + k] = make_int4(t[k].x, hole_at, more_at, 0);
+                hole_at += t[k].y;
+                more_at += t[k].z;
+            }
+            eq_run = __shfl_sync(0xffffffffu, eq_at, 31);
+            hole_run = __shfl_sync(0xffffffffu, hole_at, 31);
+            more_run = __shfl_sync(0xffffffffu, more_at, 31);
         }
         if (lane == 0) s_moves = hole_run;
     }
@@ -254,52 +363,136 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictParams 
     const int moves = s_moves;
 
     // ---- 4. the holes and the surplus cells, in order
-    int2 *const holes = p.lists + pair * 2 * p.keep, *const surplus = holes + p.keep;
+    int *const holes = p.lists + pair * evict_list_ints(p.keep), *const surplus = holes + p.keep;
+    int *const before = surplus + p.keep;                  // holes before each tile
+    auto scan_lanes = [&](int v) {                         // exclusive prefix over the lanes; total in lane 31's v + prefix
+        int x = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        return x - v;
+    };
     {
-        const int4 pre = s_all[rank * kEvWarps + warp];
+        const int4 pre = s_all[rank * nwarps + warp];
         int eq_at = pre.x, hole_at = pre.y, more_at = pre.z;
-        const uint32_t below = (1u << lane) - 1u;
-        for (int c = c0; c < c1; c += 32) {
-            const int cell = c + lane;
-            const bool mid = cell < c1 && cell >= m0 && cell < m1;
-            const uint32_t key = mid ? key_of(cell) : 0u;
-            const bool eq = mid && key == thr;
-            const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-            const bool stay = mid && (key > thr || (eq && eq_at + __popc(eqs & below) < static_cast<int>(ties)));
-            const bool hole = mid && !stay && cell < low, more = stay && cell >= low;
-            const uint32_t hs = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, more);
-            if (hole) holes[hole_at + __popc(hs & below)] = make_int2(cell, page_of(cell));
-            if (more) surplus[more_at + __popc(ms & below)] = make_int2(cell, page_of(cell));
-            if (cell < m0 || (stay && cell < low)) kept[cell] = cell;
-            eq_at += __popc(eqs);
-            hole_at += __popc(hs);
-            more_at += __popc(ms);
+        for (int cb = c0; cb < c1; cb += 1024) {
+            if (c1 - c0 > 1024) block_masks(cb, gt, eq);
+            const int base = cb + 32 * lane;               // this lane's chunk
+            const uint32_t lo = bits_below(low - base);
+            const uint32_t mid = base < c1 ? bits_below(min(m1, c1) - base) & ~bits_below(m0 - base) : 0u;
+            const int eqs = __popc(eq), eq_first = eq_at + scan_lanes(eqs);
+            // of the ties, the lowest cells stay
+            uint32_t eq_stay = eq;
+            for (int drop = eqs - max(0, min(eqs, static_cast<int>(ties) - eq_first)); drop > 0; --drop)
+                eq_stay &= ~(0x80000000u >> __clz(eq_stay));
+            const uint32_t stay = gt | eq_stay;
+            uint32_t hole = mid & ~stay & lo, more = stay & ~lo;
+            const int nh = __popc(hole), nm = __popc(more);
+            int h = hole_at + scan_lanes(nh), m = more_at + scan_lanes(nm);
+            eq_at = __shfl_sync(0xffffffffu, eq_first + eqs, 31);
+            hole_at = __shfl_sync(0xffffffffu, h + nh, 31);
+            more_at = __shfl_sync(0xffffffffu, m + nm, 31);
+            if (base < c1) {
+                if (base < p.keep) before[base / kPage] = h;
+                if (base + kPage < p.keep) before[base / kPage + 1] = h + __popc(hole & 0xffffu);
+            }
+            for (; hole; hole &= hole - 1) holes[h++] = base + __ffs(hole) - 1;
+            for (; more; more &= more - 1) surplus[m++] = base + __ffs(more) - 1;
+            const uint32_t same = base < c1 ? (stay & lo) | bits_below(m0 - base) : 0u;
+            for (int i = 0; i < 32 && cb + 32 * i < min(c1, low); ++i)
+                if (__shfl_sync(0xffffffffu, same, i) >> lane & 1u) kept[cb + 32 * i + lane] = cb + 32 * i + lane;
         }
     }
     cluster_sync_all();
 
     // ---- 5. surplus cells into the holes
     const int hl = lane & 15;
-    const int halves = 2 * kEvWarps * C, half = 2 * (rank * kEvWarps + warp) + (lane >> 4);
-    for (int j0 = half; j0 < moves; j0 += halves * kEvUnroll) {
-        EvRow<KV8> row[kEvUnroll];
-        int2 to[kEvUnroll], from[kEvUnroll];
-#pragma unroll
-        for (int u = 0; u < kEvUnroll; ++u) {
-            const int j = j0 + u * halves;
-            to[u] = from[u] = make_int2(0, -1);
-            if (j < moves) {
-                to[u] = __ldcg(holes + j);
-                from[u] = __ldcg(surplus + j);
+    const int halves = 2 * nwarps * C, half = 2 * (rank * nwarps + warp) + (lane >> 4);
+    if constexpr (KV8) {
+        const int tiles = (low + kPage - 1) / kPage;
+        for (int t = rank * nwarps + warp; t < tiles; t += C * nwarps) {
+            const int h0 = __ldcg(before + t), cnt = (t + 1 < tiles ? __ldcg(before + t + 1) : moves) - h0;
+            if (cnt == 0) continue;
+            // lane i: the tile's i-th hole, where its token comes from and that page
+            int to = 0, from = 0, page = -1;
+            if (lane < cnt) {
+                to = __ldcg(holes + h0 + lane);
+                from = __ldcg(surplus + h0 + lane);
+                kept[to] = from;
+                page = page_of(from);
             }
+            const int dst = page_of(t * kPage);
+            if (dst < 0) continue;
+            uint8_t *blk = p.k_cache + (static_cast<size_t>(dst) * p.Hkv + g) * kBlk8Bytes;
+            uint4 *vrow = reinterpret_cast<uint4 *>(blk + kBlk8V);
+            uint4 v[2] = {vrow[lane], vrow[lane + 32]};    // rows d = lane, lane + 32 of V^T
+            for (int i0 = 0; i0 < cnt; i0 += kEvTileUnroll) {
+                uint4 krow[kEvTileUnroll];
+                uint32_t src[kEvTileUnroll][2];            // the words of rows lane, lane + 32 that hold the byte
+                float x[kEvTileUnroll];
+                int pg[kEvTileUnroll], ss[kEvTileUnroll], sd[kEvTileUnroll];
+#pragma unroll
+                for (int u = 0; u < kEvTileUnroll; ++u) {
+                    const int i = min(i0 + u, cnt - 1);
+                    pg[u] = __shfl_sync(0xffffffffu, page, i);
+                    ss[u] = __shfl_sync(0xffffffffu, from, i) % kPage;
+                    sd[u] = __shfl_sync(0xffffffffu, to, i) % kPage;
+                    if (i0 + u >= cnt) pg[u] = -1;
+                    if (pg[u] >= 0) {
+                        const uint8_t *from_blk = p.k_cache + (static_cast<size_t>(pg[u]) * p.Hkv + g) * kBlk8Bytes;
+                        const uint32_t *vs = reinterpret_cast<const uint32_t *>(from_blk + kBlk8V) + (ss[u] >> 2);
+                        src[u][0] = vs[4 * lane];
+                        src[u][1] = vs[4 * (lane + 32)];
+                        if (lane < 4) krow[u] = *reinterpret_cast<const uint4 *>(from_blk + ss[u] * kD + 16 * lane);
+                        if (lane == 4 || lane == 5) x[u] = reinterpret_cast<const float *>(from_blk + kBlk8S)[(lane - 4) * kPage + ss[u]];
+                        if (lane == 6) x[u] = p.weights[(static_cast<size_t>(pg[u]) * p.Hkv + g) * kPage + ss[u]];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kEvTileUnroll; ++u) {
+                    if (pg[u] < 0) continue;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {          // byte ss of the source row into byte sd of the row
+                        const uint32_t byte = (src[u][k] >> (8 * (ss[u] & 3))) & 255u, shift = 8 * (sd[u] & 3), mask = ~(255u << shift);
+                        const int word = sd[u] >> 2;
+                        if (word == 0) v[k].x = (v[k].x & mask) | byte << shift;
+                        else if (word == 1) v[k].y = (v[k].y & mask) | byte << shift;
+                        else if (word == 2) v[k].z = (v[k].z & mask) | byte << shift;
+                        else v[k].w = (v[k].w & mask) | byte << shift;
+                    }
+                    if (lane < 4) *reinterpret_cast<uint4 *>(blk + sd[u] * kD + 16 * lane) = krow[u];
+                    if (lane == 4 || lane == 5) reinterpret_cast<float *>(blk + kBlk8S)[(lane - 4) * kPage + sd[u]] = x[u];
+                    if (lane == 6) p.weights[(static_cast<size_t>(dst) * p.Hkv + g) * kPage + sd[u]] = x[u];
+                }
+            }
+            vrow[lane] = v[0];
+            vrow[lane + 32] = v[1];
         }
+    } else {
+        for (int j0 = half; j0 < moves; j0 += halves * kEvUnroll) {
+            EvRow<KV8> row[kEvUnroll];
+            int to[kEvUnroll], from[kEvUnroll], pt[kEvUnroll], pf[kEvUnroll];
 #pragma unroll
-        for (int u = 0; u < kEvUnroll; ++u)
-            if (from[u].y >= 0) ev_load(p, row[u], from[u].y, from[u].x % kPage, g, hl);
+            for (int u = 0; u < kEvUnroll; ++u) {
+                const int j = j0 + u * halves;
+                to[u] = j < moves ? __ldcg(holes + j) : -1;
+                from[u] = j < moves ? __ldcg(surplus + j) : -1;
+            }
 #pragma unroll
-        for (int u = 0; u < kEvUnroll; ++u) {
-            if (j0 + u * halves < moves && hl == 7) kept[to[u].x] = from[u].x;
-            if (from[u].y >= 0 && to[u].y >= 0) ev_store(p, row[u], to[u].y, to[u].x % kPage, g, hl);
+            for (int u = 0; u < kEvUnroll; ++u) {
+                pt[u] = to[u] >= 0 ? page_of(to[u]) : -1;
+                pf[u] = from[u] >= 0 ? page_of(from[u]) : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < kEvUnroll; ++u)
+                if (pf[u] >= 0) ev_load(p, row[u], pf[u], from[u] % kPage, g, hl);
+#pragma unroll
+            for (int u = 0; u < kEvUnroll; ++u) {
+                if (to[u] >= 0 && hl == 7) kept[to[u]] = from[u];
+                if (pf[u] >= 0 && pt[u] >= 0) ev_store(p, row[u], pt[u], to[u] % kPage, g, hl);
+            }
         }
     }
 

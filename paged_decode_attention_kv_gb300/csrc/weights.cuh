@@ -26,8 +26,8 @@ struct WeightParams {
 
 // ------------------------------------------------------------------ one token per sequence
 // Warps take equal contiguous shares of the call's units (16-token tiles in the attention
-// kernel's order), 32 at a time: lane l works out the address of the batch's unit l, then the
-// warp takes the units four at a time, two lanes per token and half its heads each.
+// kernel's order), one (sequence, KV head) after another with its denominators in registers: one
+// token per lane, two tiles per pass, several passes' scores in flight.
 constexpr int kSwThreads = 256;
 constexpr int kSwCtasPerSm = 4;
 
@@ -49,8 +49,7 @@ __device__ __forceinline__ void load_floats(float (&v)[K], const float *p) {
 
 template <int G>
 __global__ void __launch_bounds__(kSwThreads, kSwCtasPerSm) score_weights_kernel(const WeightParams p) {
-    constexpr int HPL = G > 1 ? G / 2 : 1;    // heads per lane
-    constexpr int kSwUnroll = G > 8 ? 2 : 4;  // tiles in flight (64 registers)
+    constexpr int kPasses = G > 8 ? 1 : G > 4 ? 3 : 4;  // passes in flight (64 registers)
     __shared__ int s_pre[kMaxBatch + 1], s_len[kMaxBatch], s_wsum[kSwThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = p.B, Hkv = p.Hkv;
@@ -92,59 +91,45 @@ __global__ void __launch_bounds__(kSwThreads, kSwCtasPerSm) score_weights_kernel
     const int ua = static_cast<int>(U * w / nw), ue = static_cast<int>(U * (w + 1) / nw);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const int tok = G > 1 ? lane >> 1 : lane;             // this lane's token of a tile (G = 1: lanes 0-15)
-    const int off = G > 1 ? lane * HPL : lane;            // its scores in the tile, and its heads
-    const int hoff = G > 1 ? (lane & 1) * HPL : 0;
-    for (int u0 = ua; u0 < ue; u0 += 32) {
-        // lane l: cells of unit u0 + l (-1: bad page), its denominators, its attended tokens
-        // [lo, hi) and the token appended by this call (16: none)
-        int cell = -1, bg = 0, range = 0;
-        if (u0 + lane < ue) {
-            const int x = u0 + lane;
-            const int b = find_seq(s_pre, B, x);
-            const int tiles = (s_pre[b + 1] - s_pre[b]) / Hkv, r = x - s_pre[b];
-            const int g = r / tiles, t = r - g * tiles;
-            const int L = s_len[b], lo = (p.window > 0 && L > p.window) ? L - p.window : 0;
-            const int pt = lo / kPage + t;
-            const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + pt);
-            if (page >= 0 && page < p.num_pages) cell = page * Hkv + g;
-            bg = b * Hkv + g;
-            const int fresh = p.assign_new ? L - 1 - pt * kPage : 16;
-            range = max(0, lo - pt * kPage) | (min(16, L - pt * kPage) << 8) | (min(fresh, 16) << 16);
+    for (int u = ua; u < ue;) {
+        const int b = find_seq(s_pre, B, u);
+        const int tiles = (s_pre[b + 1] - s_pre[b]) / Hkv, r = u - s_pre[b];
+        const int g = r / tiles, t0 = r - g * tiles;
+        const int L = s_len[b], lo = (p.window > 0 && L > p.window) ? L - p.window : 0;
+        const int pt = lo / kPage + t0, cnt = min(32, min(tiles - t0, ue - u));  // tiles of this batch
+        float nl[G];
+        load_floats(nl, p.nlse + (static_cast<size_t>(b) * Hkv + g) * G);
+        int pages = -1;                                    // lane l: page of tile l
+        if (lane < cnt) {
+            pages = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + pt + lane);
+            if (pages >= p.num_pages) pages = -1;
         }
-        const int cnt = min(32, ue - u0);
-        for (int i = 0; i < cnt; i += kSwUnroll) {
-            float s[kSwUnroll][HPL], l[kSwUnroll][HPL];
-            int c[kSwUnroll], rg[kSwUnroll];
+        const float *sc = p.scores + static_cast<size_t>(u) * (kPage * G) + lane * G;
+        for (int i = 0; i < cnt; i += 2 * kPasses) {
+            float s[kPasses][G];
+            int page[kPasses];
 #pragma unroll
-            for (int k = 0; k < kSwUnroll; ++k) {
-                const int src = min(i + k, cnt - 1);
-                c[k] = __shfl_sync(0xffffffffu, cell, src);
-                rg[k] = __shfl_sync(0xffffffffu, range, src);
-                const int bgk = __shfl_sync(0xffffffffu, bg, src);
-                if (i + k >= cnt || (G == 1 && lane >= 16)) c[k] = -1;
-                if (c[k] >= 0) {
-                    load_floats(s[k], p.scores + static_cast<size_t>(u0 + i + k) * (kPage * G) + off);
-                    load_floats(l[k], p.nlse + static_cast<size_t>(bgk) * G + hoff);
-                }
+            for (int k = 0; k < kPasses; ++k) {
+                const int tile = i + 2 * k + (lane >> 4), j = (pt + tile) * kPage + (lane & 15);
+                page[k] = __shfl_sync(0xffffffffu, pages, tile & 31);
+                if (tile >= cnt || j < lo || j >= L) page[k] = -1;
+                if (page[k] >= 0) load_floats(s[k], sc + (i + 2 * k) * (kPage * G));
             }
 #pragma unroll
-            for (int k = 0; k < kSwUnroll; ++k) {
+            for (int k = 0; k < kPasses; ++k) {
+                if (page[k] < 0) continue;
                 float sum = 0.f;
-                if (c[k] >= 0)
 #pragma unroll
-                    for (int h = 0; h < HPL; ++h) sum += fast_exp2(s[k][h] + l[k][h]);
-                if (G > 1) sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                const int lo = rg[k] & 255, hi = (rg[k] >> 8) & 255, fresh = rg[k] >> 16;
-                if (c[k] >= 0 && tok >= lo && tok < hi && (G == 1 || (lane & 1) == 0)) {
-                    float *dst = p.weights + static_cast<size_t>(c[k]) * kPage + tok;
-                    if (tok == fresh)
-                        *dst = sum;
-                    else
-                        atomicAdd(dst, sum);
-                }
+                for (int h = 0; h < G; ++h) sum += fast_exp2(s[k][h] + nl[h]);
+                const int j = (pt + i + 2 * k + (lane >> 4)) * kPage + (lane & 15);
+                float *dst = p.weights + (static_cast<size_t>(page[k]) * Hkv + g) * kPage + (lane & 15);
+                if (p.assign_new && j == L - 1)
+                    *dst = sum;
+                else
+                    atomicAdd(dst, sum);
             }
         }
+        u += cnt;
     }
 }
 
