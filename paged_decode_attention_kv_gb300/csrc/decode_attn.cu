@@ -305,6 +305,10 @@ __device__ __forceinline__ uint64_t evict_first_policy() {
     return pol;
 }
 
+__device__ __forceinline__ void store_hint(float *p, float a, float b, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(p), "f"(a), "f"(b), "l"(policy) : "memory");
+}
+
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2,
                                         uint32_t &r3) {
     asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -1414,14 +1418,20 @@ __global__ void __launch_bounds__(kThreads, CPS)
                     }
                 }
                 if constexpr (WTS && !MT) {  // this lane's two tokens, two heads each
+                    // kept in L2 for the kernel that reads them back: with plain stores the key and
+                    // value stream pushed part of them out to memory (64 sequences: 131 us a call,
+                    // 122 so, 116 with the lines dropped once read)
+                    uint64_t keep;
+                    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
                     const int h = n * 8 + (lane & 3) * 2;
+                    float *const tile = p.scores + static_cast<size_t>(ua + i) * (kPage * p.G);
 #pragma unroll
                     for (int u = 0; u < UT; ++u) {
-                        float *dst = p.scores + (static_cast<size_t>(ua + i + u) * kPage + row_tok) * p.G + h;
+                        float *dst = tile + ((u * kPage + row_tok) * p.G + h);
                         float *dst2 = dst + (KV8 ? 2 : 8) * p.G;
                         if (h + 1 < p.G) {
-                            *reinterpret_cast<float2 *>(dst) = make_float2(sv[u][0], sv[u][1]);
-                            *reinterpret_cast<float2 *>(dst2) = make_float2(sv[u][2], sv[u][3]);
+                            store_hint(dst, sv[u][0], sv[u][1], keep);
+                            store_hint(dst2, sv[u][2], sv[u][3], keep);
                         } else if (h < p.G) {  // (G = 1)
                             *dst = sv[u][0];
                             *dst2 = sv[u][2];
@@ -3182,6 +3192,10 @@ int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int3
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    // At the early levels the next attention call may read its lengths, here new_lens, before it
+    // waits for the kernel launched just before it: let that be a kernel that started after
+    // the eviction ended.
+    if (e == cudaSuccess && g_early_inputs.load() > 0) evict_done_kernel<<<1, 32, 0, stream>>>();
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? DA_OK : set_cuda_error(e);
 }

@@ -524,3 +524,5 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
         }
     }
 }
+
+__global__ void evict_done_kernel() {}  // an ordinary launch: it starts when the eviction has ended

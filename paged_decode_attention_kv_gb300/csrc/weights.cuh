@@ -17,7 +17,7 @@ struct WeightParams {
     const int *block_table, *seq_lens, *q_lens;
     const float *nlse;               // [B * Hkv][lse_ld]
     int lse_ld;
-    const float *scores;             // one token: [unit][16][G]
+    float *scores;                   // one token: [unit][16][G]
     float scale_log2;
     int B, Hkv, G, T, window, max_pages, num_pages, max_seq_len;
     int assign_new;                  // the call appended its new tokens
@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(kSwThreads, kSwCtasPerSm) score_weights_kernel
     const long long w = static_cast<long long>(blockIdx.x) * (kSwThreads / 32) + warp;
     const int ua = static_cast<int>(U * w / nw), ue = static_cast<int>(U * (w + 1) / nw);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // every CTA of this grid is resident: the next kernel may set itself up as they leave
+    if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     for (int u = ua; u < ue;) {
         const int b = find_seq(s_pre, B, u);
@@ -107,28 +109,30 @@ __global__ void __launch_bounds__(kSwThreads, kSwCtasPerSm) score_weights_kernel
         const float *sc = p.scores + static_cast<size_t>(u) * (kPage * G) + lane * G;
         for (int i = 0; i < cnt; i += 2 * kPasses) {
             float s[kPasses][G];
-            int page[kPasses];
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k)  // (not behind the page: that load is under way too)
+                if (i + 2 * k + (lane >> 4) < cnt) load_floats(s[k], sc + (i + 2 * k) * (kPage * G));
 #pragma unroll
             for (int k = 0; k < kPasses; ++k) {
                 const int tile = i + 2 * k + (lane >> 4), j = (pt + tile) * kPage + (lane & 15);
-                page[k] = __shfl_sync(0xffffffffu, pages, tile & 31);
-                if (tile >= cnt || j < lo || j >= L) page[k] = -1;
-                if (page[k] >= 0) load_floats(s[k], sc + (i + 2 * k) * (kPage * G));
-            }
-#pragma unroll
-            for (int k = 0; k < kPasses; ++k) {
-                if (page[k] < 0) continue;
+                const int page = __shfl_sync(0xffffffffu, pages, tile & 31);
+                if (tile >= cnt || j < lo || j >= L || page < 0) continue;
                 float sum = 0.f;
 #pragma unroll
                 for (int h = 0; h < G; ++h) sum += fast_exp2(s[k][h] + nl[h]);
-                const int j = (pt + i + 2 * k + (lane >> 4)) * kPage + (lane & 15);
-                float *dst = p.weights + (static_cast<size_t>(page[k]) * Hkv + g) * kPage + (lane & 15);
+                float *dst = p.weights + (static_cast<size_t>(page) * Hkv + g) * kPage + (lane & 15);
                 if (p.assign_new && j == L - 1)
                     *dst = sum;
                 else
                     atomicAdd(dst, sum);
             }
         }
+        // The scores are read once: their lines leave L2 without being written to memory (whole lines
+        // of this warp's own tiles; at G = 1 two tiles share one).
+        __syncwarp();
+        if constexpr (G >= 2)
+            for (int i = lane; i < cnt * (G / 2); i += 32)
+                asm volatile("discard.global.L2 [%0], 128;" ::"l"(p.scores + static_cast<size_t>(u) * (kPage * G) + 32 * i) : "memory");
         u += cnt;
     }
 }
@@ -338,6 +342,7 @@ __global__ void __launch_bounds__(SkLayout<N>::kThreads, SkLayout<N>::kCtas)
         s_failed = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const MwKeys k = mw_keys(p, b);
     if (!k.ok) return;
     const int s0 = k.lo0 / kMwKeys + blockIdx.x * p.run;  // first stage: positions 128 s0 on
@@ -501,6 +506,7 @@ __global__ void __launch_bounds__(SrLayout<TILES>::kThreads, SrLayout<TILES>::kC
         s_failed = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const MwKeys k = mw_keys(p, b);
     if (!k.ok) return;
     const int first = k.lo0 / kMwKeys * kMwKeys + blockIdx.x * kKeys;
