@@ -240,6 +240,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         return tn < n;
     };
 
+    // Tiles below full_cache and those from ncache to below full_new hold 16 keys each (keys only end
+    // at a tile's top). A block of such tiles, all cached or all new, has 64 consecutive positions:
+    // most blocks, told by two comparisons (key_at tile by tile cost the row warps 280 cycles a
+    // block, and the check of the V rows warp 0 another 700).
+    const int full_cache = RING ? 0 : min(ncache, base / kPage - pt_lo), full_new = RING ? 0 : ncache + n / kPage - nt_base;
+    auto whole_block = [&](int k0) {
+        return !RING && k0 + kTcTilesPerBlock <= ke &&
+               (k0 + kTcTilesPerBlock <= full_cache || (k0 >= ncache && k0 + kTcTilesPerBlock <= full_new));
+    };
+
     bool failed = false;
     if (warp == 4) {
         // ---- TMA producer
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const uint64_t policy = evict_first_policy();
             for (int j = 0; j < nblk && !failed; ++j) {
                 const int s = j % kTcStages;
-                if (j >= kTcStages && !mbar_wait_bounded(kv_empty + 8 * s, ((j / kTcStages) - 1) & 1)) {
+                if (j >= kTcStages && !mbar_wait_idle(kv_empty + 8 * s, ((j / kTcStages) - 1) & 1)) {
                     failed = true;
                     break;
                 }
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             }
             // nothing may still be landing when the CTA leaves: the last copy of every stage
             for (int j = max(0, nblk - kTcStages); j < nblk; ++j)
-                mbar_wait_bounded(kv_full + 8 * (j % kTcStages), (j / kTcStages) & 1);
+                mbar_wait_idle(kv_full + 8 * (j % kTcStages), (j / kTcStages) & 1);
         }
     } else if (warp == 5) {
         // ---- MMA issuer: S_j = Q K_j^T, then O += P_{j-1} V_{j-1}
@@ -288,13 +298,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             for (int j = 0; j <= nblk && !failed; ++j) {
                 if (j < nblk) {
                     const int s = j % kTcStages;
-                    if (!mbar_wait_bounded(kv_full + 8 * s, (j / kTcStages) & 1)) {
+                    if (!mbar_wait_idle(kv_full + 8 * s, (j / kTcStages) & 1)) {
                         failed = true;
                         break;
                     }
                     // buffer j % kTcSBufs last held P_{j-kTcSBufs}: its PV must be done
                     const int sb = j % kTcSBufs;
-                    if (j >= kTcSBufs && !mbar_wait_bounded(o_done + 8 * sb, ((j / kTcSBufs) - 1) & 1)) {
+                    if (j >= kTcSBufs && !mbar_wait_idle(o_done + 8 * sb, ((j / kTcSBufs) - 1) & 1)) {
                         failed = true;
                         break;
                     }
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 }
                 if (j >= 1) {
                     const int jj = j - 1, s = jj % kTcStages, pb = jj % kTcSBufs;
-                    if (!mbar_wait_bounded(p_full + 8 * pb, (jj / kTcSBufs) & 1)) {
+                    if (!mbar_wait_idle(p_full + 8 * pb, (jj / kTcSBufs) & 1)) {
                         failed = true;
                         break;
                     }
@@ -360,10 +370,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
                 // a block whose 64 keys are consecutive positions, all present and all inside
                 // the row's window [lor, pr] needs no per-key mask (most blocks of a long sequence)
-                int jf = 0, jl = 0;
-                const bool okf = key_at(k0, 0, jf);
-                const bool okl = k0 + kTcTilesPerBlock - 1 < ke && key_at(k0 + kTcTilesPerBlock - 1, kPage - 1, jl);
-                const bool interior = valid && okf && okl && jl - jf == kTcKeys - 1 && jf >= lor && jl <= pr;
+                const bool whole = whole_block(k0);
+                const int jf = k0 < ncache ? (pt_lo + k0) * kPage : base + (nt_base + k0 - ncache) * kPage;
+                const bool interior = valid && whole && jf >= lor && jf + kTcKeys - 1 <= pr;
                 if (!interior) {
 #pragma unroll
                     for (int u = 0; u < kTcTilesPerBlock; ++u) {
@@ -390,15 +399,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         }
                     }
                 }
-                // maximum as a pairwise tree (6 dependent steps instead of 64)
-                float mx[32];
+                // maximum: four chains of three-operand steps
+                float m4[4];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) mx[c] = fmaxf(x[c], x[c + 32]);
+                for (int c = 0; c < 4; ++c) m4[c] = max3(x[c], x[c + 4], x[c + 8]);
 #pragma unroll
-                for (int w = 16; w > 0; w >>= 1)
+                for (int c = 12; c < 60; c += 8)
 #pragma unroll
-                    for (int c = 0; c < w; ++c) mx[c] = fmaxf(mx[c], mx[c + w]);
-                const float mraw = mx[0];
+                    for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], x[c + i], x[c + 4 + i]);
+                const float mraw = fmaxf(max3(m4[0], m4[1], max3(x[60], x[61], x[62])), max3(m4[2], m4[3], x[63]));
                 const float mb = mraw * p.scale_log2;  // the scale is positive
                 const bool need = valid && mb > m_ref + kTcRescale;
                 const float m_new = need ? mb : m_ref;
@@ -433,26 +442,33 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     m_ref = m_new;
                 }
                 const float mr = m_ref == -INFINITY ? 0.f : m_ref;
-                float ls4[4] = {0.f, 0.f, 0.f, 0.f};  // four independent partial sums
+                // two values per instruction where there is one; four independent partial sums
+                float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-mr, -mr);
+                const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {  // keys 32h .. 32h + 31: hi and lo, 16 columns each
                     uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float p0 = fast_exp2(fmaf(x[32 * h + 2 * c], p.scale_log2, -mr));
-                        const float p1 = fast_exp2(fmaf(x[32 * h + 2 * c + 1], p.scale_log2, -mr));
-                        ls4[c & 3] += p0 + p1;
-                        hi[c] = pack_bf16(p0, p1);
-                        const float2 r2 = unpack_bf16(hi[c]);
-                        lo[c] = pack_bf16(p0 - r2.x, p1 - r2.y);
+                    for (int c = 0; c < 16; c += 2) {
+                        const float *xc = x + 32 * h + 2 * c;
+                        const float2 a = fma2(make_float2(xc[0], xc[1]), sc2, nm2), e = fma2(make_float2(xc[2], xc[3]), sc2, nm2);
+                        const float a0 = fast_exp2(a.x), a1 = fast_exp2(a.y), e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+                        ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], add2(make_float2(a0, e0), make_float2(a1, e1)));
+                        hi[c] = pack_bf16(a0, a1);
+                        hi[c + 1] = pack_bf16(e0, e1);
+                        const float2 ra = fma2(unpack_bf16(hi[c]), minus, make_float2(a0, a1));
+                        const float2 re = fma2(unpack_bf16(hi[c + 1]), minus, make_float2(e0, e1));
+                        lo[c] = pack_bf16(ra.x, ra.y);
+                        lo[c + 1] = pack_bf16(re.x, re.y);
                     }
                     tmem_st16(tm + lanes + kTcColS + 64 * sb + 16 * h, hi);
                     tmem_st16(tm + lanes + kTcColS + 64 * sb + 32 + 16 * h, lo);
                     tmem_wait_st();
                 }
-                l += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
             }
-            if (warp == 0) {  // V rows of keys that do not exist may hold anything: zero them
+            if (warp == 0 && !whole_block(k0)) {  // V rows of keys that do not exist may hold anything: zero them
                 uint8_t *vb = sKV + (j % kTcStages) * kTcStageBytes + kTcBlockBytes;
                 bool touched = false;
                 for (int u = 0; u < kTcTilesPerBlock; ++u) {
