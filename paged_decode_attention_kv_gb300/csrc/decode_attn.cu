@@ -263,6 +263,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity)
 // The same for the warps that only issue copies or products: they sleep longer between looks, so
 // that they take fewer issue slots from the warps that compute.
 __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
         uint32_t ok;

@@ -83,6 +83,13 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
                  : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -290,53 +297,62 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 mbar_wait_idle(kv_full + 8 * (j % kTcStages), (j / kTcStages) & 1);
         }
     } else if (warp == 5) {
-        // ---- MMA issuer: S_j = Q K_j^T, then O += P_{j-1} V_{j-1}
-        if (lane == 0) {
-            const uint32_t id_qk = umma_idesc_bf16(kTcRows, kTcKeys, false);
-            const uint32_t id_pv = umma_idesc_bf16(kTcRows, kD, true);
-            const uint32_t q_s = smem_addr(sQ);
-            for (int j = 0; j <= nblk && !failed; ++j) {
-                if (j < nblk) {
-                    const int s = j % kTcStages;
-                    if (!mbar_wait_idle(kv_full + 8 * s, (j / kTcStages) & 1)) {
-                        failed = true;
-                        break;
-                    }
-                    // buffer j % kTcSBufs last held P_{j-kTcSBufs}: its PV must be done
-                    const int sb = j % kTcSBufs;
-                    if (j >= kTcSBufs && !mbar_wait_idle(o_done + 8 * sb, ((j / kTcSBufs) - 1) & 1)) {
-                        failed = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t k_s = smem_addr(sKV + s * kTcStageBytes);
+        // ---- MMA issuer: S_j = Q K_j^T, then O += P_{j-1} V_{j-1}. The whole warp walks the blocks and
+        // waits, one elected lane issues.
+        const bool leader = elect_one();
+        const uint32_t id_qk = umma_idesc_bf16(kTcRows, kTcKeys, false);
+        const uint32_t id_pv = umma_idesc_bf16(kTcRows, kD, true);
+        // descriptors once: a stage or a step along the contraction only moves the start address
+        const uint64_t dq = umma_sdesc(smem_addr(sQ), 16, 1024), dk = umma_sdesc(smem_addr(sKV), 16, 1024);
+        const uint64_t dv = umma_sdesc(smem_addr(sKV) + kTcBlockBytes, 2048, 1024);
+        auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity)); };
+        for (int j = 0; j <= nblk && !failed; ++j) {
+            if (j < nblk) {
+                const int s = j % kTcStages;
+                // buffer j % kTcSBufs last held P_{j-kTcSBufs}: its PV must be done
+                const int sb = j % kTcSBufs;
+                if (!wait_all(kv_full + 8 * s, (j / kTcStages) & 1) ||
+                    (j >= kTcSBufs && !wait_all(o_done + 8 * sb, ((j / kTcSBufs) - 1) & 1))) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t dks = dk + s * (kTcStageBytes / 16);
+                if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kD / 16; ++kk)
-                        umma_bf16_ss(tm + kTcColS + 64 * sb, umma_sdesc(q_s + 32 * kk, 16, 1024),
-                                     umma_sdesc(k_s + 32 * kk, 16, 1024), id_qk, kk > 0);
+                        umma_bf16_ss(tm + kTcColS + 64 * sb, dq + 2 * kk, dks + 2 * kk, id_qk, kk > 0);
                     umma_commit(s_full + 8 * sb);
                 }
-                if (j >= 1) {
-                    const int jj = j - 1, s = jj % kTcStages, pb = jj % kTcSBufs;
-                    if (!mbar_wait_idle(p_full + 8 * pb, (jj / kTcSBufs) & 1)) {
-                        failed = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t v_s = smem_addr(sKV + s * kTcStageBytes + kTcBlockBytes);
+                __syncwarp();
+            }
+            if (j >= 1) {
+                const int jj = j - 1, s = jj % kTcStages, pb = jj % kTcSBufs;
+                if (!wait_all(p_full + 8 * pb, (jj / kTcSBufs) & 1)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t dvs = dv + s * (kTcStageBytes / 16);
+                const uint32_t acc = jj > 0 ? 1u : 0u;
+                if (leader) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part)  // P = hi + lo
 #pragma unroll
                         for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                            umma_bf16_ts(tm + kTcColO, tm + kTcColS + 64 * pb + 32 * part + 8 * kk,
-                                         umma_sdesc(v_s + 2048 * kk, 2048, 1024), id_pv,
-                                         (jj > 0 || part > 0 || kk > 0) ? 1u : 0u);
+                            umma_bf16_ts(tm + kTcColO, tm + kTcColS + 64 * pb + 32 * part + 8 * kk, dvs + 128 * kk, id_pv,
+                                         part > 0 || kk > 0 ? 1u : acc);
                     umma_commit(o_done + 8 * pb);
                     umma_commit(kv_empty + 8 * s);
                 }
+                __syncwarp();
             }
-            umma_commit(drain);  // completes when every MMA issued above has
         }
+        if (leader) {
+            umma_commit(drain);  // completes when every MMA issued above has
+            mbar_wait_bounded(drain, 0);
+        }
+        __syncwarp();
     } else {
         // ---- query rows: one per thread
         const int r = r0 + tid;
@@ -552,8 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         s_failed = 1;
     }
 
-    // ---- teardown: every MMA done before TMEM is released
-    if (tid == 5 * 32) mbar_wait_bounded(drain, 0);
+    // ---- teardown: every MMA done (the issuer has waited) before TMEM is released
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {

@@ -366,6 +366,8 @@ __global__ void __launch_bounds__(SkLayout<N>::kThreads, SkLayout<N>::kCtas)
         // ---- products
         if (lane == 0) {
             const uint32_t idesc = umma_idesc_bf16(kMwKeys, N, false);
+            // (a stage or a step along the contraction only moves a descriptor's start address)
+            const uint64_t dk = umma_sdesc(k_s, 16, 1024), dq = umma_sdesc(q_s, 16, 1024);
             if (!mbar_wait_bounded(q_full, 0)) failed = true;
             for (int st = 0; st < ns && !failed; ++st) {
                 const int slot = st % kRing, buf = st & 1;
@@ -375,11 +377,9 @@ __global__ void __launch_bounds__(SkLayout<N>::kThreads, SkLayout<N>::kCtas)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t ka = k_s + slot * kMwKBytes;
+                const uint64_t dks = dk + slot * (kMwKBytes / 16);
 #pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk)
-                    umma_bf16_ss(tm + buf * N, umma_sdesc(ka + 32 * kk, 16, 1024), umma_sdesc(q_s + 32 * kk, 16, 1024), idesc,
-                                 kk > 0);
+                for (int kk = 0; kk < kD / 16; ++kk) umma_bf16_ss(tm + buf * N, dks + 2 * kk, dq + 2 * kk, idesc, kk > 0);
                 umma_commit(t_full + 8 * buf);
                 umma_commit(k_empty + 8 * slot);
             }
@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(SrLayout<TILES>::kThreads, SrLayout<TILES>::kC
         // ---- products
         if (lane == 0) {
             const uint32_t idesc = umma_idesc_bf16(kMwKeys, kMwRowBlock, false);
+            const uint64_t dk = umma_sdesc(k_s, 16, 1024), dq = umma_sdesc(q_s, 16, 1024);
             if (!mbar_wait_bounded(k_full, 0)) failed = true;
             for (int i = 0; i < nb && !failed; ++i) {
                 const int slot = i % kSlots, buf = i & 1;
@@ -543,13 +544,13 @@ __global__ void __launch_bounds__(SrLayout<TILES>::kThreads, SrLayout<TILES>::kC
                     break;
                 }
                 tc_fence_after();
-                const uint32_t qa = q_s + slot * Lay::kQBytes;
+                const uint64_t dqs = dq + slot * (Lay::kQBytes / 16);
 #pragma unroll
                 for (int m = 0; m < TILES; ++m)
 #pragma unroll
                     for (int kk = 0; kk < kD / 16; ++kk)
-                        umma_bf16_ss(tm + (buf * TILES + m) * kMwRowBlock, umma_sdesc(k_s + m * kMwKBytes + 32 * kk, 16, 1024),
-                                     umma_sdesc(qa + 32 * kk, 16, 1024), idesc, kk > 0);
+                        umma_bf16_ss(tm + (buf * TILES + m) * kMwRowBlock, dk + m * (kMwKBytes / 16) + 2 * kk, dqs + 2 * kk,
+                                     idesc, kk > 0);
                 umma_commit(t_full + 8 * buf);
                 umma_commit(q_empty + 8 * slot);
             }
