@@ -451,47 +451,51 @@ def decode_attn_test_expire_wait(tile: int):
     _check(load_library().decode_attn_test_expire_wait(int(tile)))
 
 
-def _tensor(name, t, dtype, *shape):
-    """t as the library reads it: of this type and shape, contiguous, on the current device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}, got {t.dtype} "
-                         f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
-    if t.get_device() != torch.cuda.current_device():
+def _refuse(name, t, dtype, shape):
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}, got {t.dtype} "
+                     f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _paged_tensors(bf16_pool, k, v, weights, block_table, seq_lens):
-    """Checked pointers of a paged cache (v None: fp8 blocks), and its sizes."""
-    if k.dim() != (4 if bf16_pool else 3) or block_table.dim() != 2:
+def _tensor(name, t, dtype, shape, dev):
+    """t's address, if it is as the library reads it: this type and shape, contiguous, on device dev."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse(name, t, dtype, shape)
+
+
+def _paged_tensors(k, v, weights, block_table, seq_lens, dev):
+    """Checked addresses of a paged cache (v None: fp8 blocks) and its tables, and its sizes."""
+    if k.dim() != (3 if v is None else 4) or block_table.dim() != 2:
         raise ValueError(f"the cache is {tuple(k.shape)}, the block table {tuple(block_table.shape)}")
     num_pages, Hkv = k.shape[0], k.shape[1]
     B, max_pages = block_table.shape
-    if bf16_pool:
-        kp = _tensor("k_cache", k, torch.bfloat16, num_pages, Hkv, 16, 64)
-        vp = _tensor("v_cache", v, torch.bfloat16, num_pages, Hkv, 16, 64)
+    if v is None:
+        kp, vp = _tensor("kv_cache", k, torch.uint8, (num_pages, Hkv, FP8_BLOCK_BYTES), dev), None
     else:
-        kp, vp = _tensor("kv_cache", k, torch.uint8, num_pages, Hkv, FP8_BLOCK_BYTES), None
-    return (kp, vp, _tensor("weights", weights, torch.float32, num_pages, Hkv, 16),
-            _tensor("block_table", block_table, torch.int32, B, max_pages),
-            _tensor("seq_lens", seq_lens, torch.int32, B), B, Hkv, max_pages, num_pages)
+        pool = (num_pages, Hkv, 16, 64)
+        kp = _tensor("k_cache", k, torch.bfloat16, pool, dev)
+        vp = _tensor("v_cache", v, torch.bfloat16, pool, dev)
+    return (kp, vp, _tensor("weights", weights, torch.float32, (num_pages, Hkv, 16), dev),
+            _tensor("block_table", block_table, torch.int32, (B, max_pages), dev),
+            _tensor("seq_lens", seq_lens, torch.int32, (B,), dev), B, Hkv, max_pages, num_pages)
 
 
-def _new_tensors(q, k_new, v_new, sinks, out, lead, Hkv):
-    Hq = q.shape[-2]
+def _new_tensors(q, k_new, v_new, sinks, out, lead, Hkv, dev):
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new are given together")
-    return (_tensor("q", q, torch.bfloat16, *lead, Hq, 64),
-            None if k_new is None else _tensor("k_new", k_new, torch.bfloat16, *lead, Hkv, 64),
-            None if v_new is None else _tensor("v_new", v_new, torch.bfloat16, *lead, Hkv, 64),
-            None if sinks is None else _tensor("sinks", sinks, torch.float32, Hq),
-            _tensor("out", out, torch.bfloat16, *lead, Hq, 64), Hq)
+    Hq = q.shape[-2]
+    rows, new = lead + (Hq, 64), lead + (Hkv, 64)
+    return (_tensor("q", q, torch.bfloat16, rows, dev),
+            None if k_new is None else _tensor("k_new", k_new, torch.bfloat16, new, dev),
+            None if v_new is None else _tensor("v_new", v_new, torch.bfloat16, new, dev),
+            None if sinks is None else _tensor("sinks", sinks, torch.float32, (Hq,), dev),
+            _tensor("out", out, torch.bfloat16, rows, dev), Hq)
 
 
-def _raw_stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def decode_attn_paged_weights(q, k_new, v_new, k_cache, v_cache, weights, block_table, seq_lens, sinks,
@@ -499,24 +503,25 @@ def decode_attn_paged_weights(q, k_new, v_new, k_cache, v_cache, weights, block_
     """decode_attn_paged that also adds every attended token's attention weight (its probabilities
     summed over the query heads of its KV head) to its cell of weights, fp32
     [num_pages, Hkv, 16]; the appended token's cell is set to its weight."""
-    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(True, k_cache, v_cache, weights, block_table,
-                                                                       seq_lens)
-    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv)
+    dev = torch.cuda.current_device()
+    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(k_cache, v_cache, weights, block_table, seq_lens,
+                                                                       dev)
+    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv, dev)
     _check(load_library().decode_attn_paged_weights(
         qp, knp, vnp, kp, vp, wp, bp, lp, sp, window, scale, op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
-        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
     return out
 
 
 def decode_attn_paged_fp8_weights(q, k_new, v_new, kv_cache, weights, block_table, seq_lens, sinks, window,
                                   scale, out, max_seq_len=None, stream=None):
     """decode_attn_paged_weights over an fp8 cache (kv_cache as in decode_attn_paged_fp8)."""
-    kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(False, kv_cache, None, weights, block_table,
-                                                                      seq_lens)
-    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv)
+    dev = torch.cuda.current_device()
+    kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(kv_cache, None, weights, block_table, seq_lens, dev)
+    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv, dev)
     _check(load_library().decode_attn_paged_fp8_weights(
         qp, knp, vnp, kp, wp, bp, lp, sp, window, scale, op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
-        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
     return out
 
 
@@ -525,16 +530,17 @@ def decode_attn_paged_multi_weights(q, k_new, v_new, k_cache, v_cache, weights, 
     """decode_attn_paged_multi that also adds every attended token's attention weight, summed over
     the new tokens and the query heads of its KV head, to its cell of weights; the new tokens'
     cells are set to theirs."""
-    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(True, k_cache, v_cache, weights, block_table,
-                                                                       seq_lens)
+    dev = torch.cuda.current_device()
+    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(k_cache, v_cache, weights, block_table, seq_lens,
+                                                                       dev)
     if q.dim() != 4 or k_new is None:
         raise ValueError("q is [B, T, Hq, 64] and k_new, v_new are required")
     T = q.shape[1]
-    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B, T), Hkv)
+    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B, T), Hkv, dev)
     _check(load_library().decode_attn_paged_multi_weights(
-        qp, knp, vnp, kp, vp, wp, bp, lp, None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, B), sp,
+        qp, knp, vnp, kp, vp, wp, bp, lp, None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev), sp,
         window, scale, op, da_shape(B, Hq, Hkv, 64), T, 16, max_pages, num_pages,
-        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
     return out
 
 
@@ -544,26 +550,27 @@ def kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_lens, kept, k
     place: the first keep_first and the last keep_last cells stay, and of those between them the
     ones of the largest accumulated weight. new_lens [B] int32 receives the lengths, kept
     [B, Hkv, keep] int32 the old cell of each kept cell (-1 beyond a shorter sequence's end)."""
-    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(True, k_cache, v_cache, weights, block_table,
-                                                                       seq_lens)
-    keep = kept.shape[-1]
+    dev = torch.cuda.current_device()
+    kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(k_cache, v_cache, weights, block_table, seq_lens,
+                                                                       dev)
+    keep = kept.shape[-1] if kept.dim() else 0
     _check(load_library().kv_evict(
-        kp, vp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, B),
-        _tensor("kept", kept, torch.int32, B, Hkv, keep), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
-        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+        kp, vp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, (B,), dev),
+        _tensor("kept", kept, torch.int32, (B, Hkv, keep), dev), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
+        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
     return new_lens
 
 
 def kv_evict_fp8(kv_cache, weights, block_table, seq_lens, new_lens, kept, keep_first=0, keep_last=0,
                  max_seq_len=None, stream=None):
     """kv_evict over an fp8 cache: codes and scales move as they are."""
-    kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(False, kv_cache, None, weights, block_table,
-                                                                      seq_lens)
-    keep = kept.shape[-1]
+    dev = torch.cuda.current_device()
+    kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(kv_cache, None, weights, block_table, seq_lens, dev)
+    keep = kept.shape[-1] if kept.dim() else 0
     _check(load_library().kv_evict_fp8(
-        kp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, B),
-        _tensor("kept", kept, torch.int32, B, Hkv, keep), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
-        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream)))
+        kp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, (B,), dev),
+        _tensor("kept", kept, torch.int32, (B, Hkv, keep), dev), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
+        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
     return new_lens
 
 
@@ -580,4 +587,4 @@ def kv_evict_workspace_bytes(batch, num_kv_heads, keep):
 def decode_attn_weights_reserve(nbytes: int, stream=None):
     """Grow the weights workspace that calls on `stream` use (the stream's own after
     decode_attn_stream_reserve, else the device's) to at least nbytes; call before a capture."""
-    _check(load_library().decode_attn_weights_reserve(_raw_stream(stream), int(nbytes)))
+    _check(load_library().decode_attn_weights_reserve(_raw_stream(stream, torch.cuda.current_device()), int(nbytes)))

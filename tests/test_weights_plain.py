@@ -107,7 +107,8 @@ def test_workspace_bytes(lib):
     assert da.kv_evict_workspace_bytes(2, 8, 0) == 0
 
 
-def test_python_checks_name_the_tensor():
+def test_python_checks_name_the_tensor(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     q, kn = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(2, 1, 64, dtype=bf)
     pool, w = torch.zeros(4, 1, 16, 64, dtype=bf), torch.zeros(4, 1, 16, dtype=f32)
