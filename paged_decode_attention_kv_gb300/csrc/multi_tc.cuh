@@ -461,7 +461,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 // two values per instruction where there is one; four independent partial sums
                 float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
                 const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-mr, -mr);
-                const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {  // keys 32h .. 32h + 31: hi and lo, 16 columns each
                     uint32_t hi[16], lo[16];
@@ -473,10 +472,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], add2(make_float2(a0, e0), make_float2(a1, e1)));
                         hi[c] = pack_bf16(a0, a1);
                         hi[c + 1] = pack_bf16(e0, e1);
-                        const float2 ra = fma2(unpack_bf16(hi[c]), minus, make_float2(a0, a1));
-                        const float2 re = fma2(unpack_bf16(hi[c + 1]), minus, make_float2(e0, e1));
-                        lo[c] = pack_bf16(ra.x, ra.y);
-                        lo[c + 1] = pack_bf16(re.x, re.y);
+                        const float2 ha = unpack_bf16(hi[c]), he = unpack_bf16(hi[c + 1]);
+                        lo[c] = pack_bf16(a0 - ha.x, a1 - ha.y);
+                        lo[c + 1] = pack_bf16(e0 - he.x, e1 - he.y);
                     }
                     tmem_st16(tm + lanes + kTcColS + 64 * sb + 16 * h, hi);
                     tmem_st16(tm + lanes + kTcColS + 64 * sb + 32 + 16 * h, lo);
