@@ -3108,13 +3108,17 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
         return DA_ERR_CUDA;
     }
     if (rows > kMwMaxRows) {
-        const bool two = stages / 2 * pairs >= 3 * sm_count(dev);
+        // 256 keys per CTA where that still gives every SM one (512 tokens behind 7680: 280 us against
+        // 285 with 128 keys and two CTAs per SM; four prompts of up to 2048: 390 against 397)
+        const bool two = stages * pairs >= 2 * sm_count(dev);
         const long long blocks = two ? (stages + 1) / 2 : stages;
         return two ? launch_stream_rows<2>(5, mk, mq, p, blocks, dev, stream)
                    : launch_stream_rows<1>(4, mk, mq, p, blocks, dev, stream);
     }
-    // runs of stages, so that the GPU has several CTAs per slot, within what a CTA can hold
-    const int want = sm_count(dev) * (N < kMwMaxRows ? 8 : 4);
+    // runs of stages, so that the GPU has several CTAs per slot, within what a CTA can hold (four per
+    // slot where two CTAs share an SM: 4 tokens x 32 sequences 128 us against 130 with two and 134
+    // with eight; two where one has it: 32 tokens behind 131k 190 us against 193 and 200)
+    const int want = sm_count(dev) * (N < kMwMaxRows ? 8 : 2);
     p.run = static_cast<int>(std::max<long long>(1, std::min<long long>(kMwMaxRun, stages * pairs / want)));
     const long long runs = (stages + p.run - 1) / p.run;
     return N == 32    ? launch_stream_keys<32>(0, mk, mq, p, runs, dev, stream)
@@ -3202,10 +3206,11 @@ int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int3
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.max_seq_len = max_seq_len;
-    // CTAs of 8 warps when there are several per SM, larger ones and clusters of them when there
-    // are not; at least a chunk of cells per warp
+    // CTAs of 16 warps when there is one per SM or more (64 sequences of 8 KV heads: 95 us, 98 with 8
+    // warps, 114 with 32), larger ones and clusters of them when there are not; at least a chunk of
+    // cells per warp
     const int pairs = s.batch * s.num_kv_heads, sms = sm_count(dev);
-    const int warps = pairs >= 2 * sms ? 8 : pairs >= sms ? 16 : kEvMaxWarps;
+    const int warps = pairs >= sms ? 16 : kEvMaxWarps;
     auto kern = kv8 ? kv_evict_kernel<true> : kv_evict_kernel<false>;
     int of16 = g_dev[dev].evict_clusters[kv8].load(std::memory_order_acquire);
     if (of16 < 0) {  // first use on this device: shared memory, and clusters of 16

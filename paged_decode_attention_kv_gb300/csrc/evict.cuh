@@ -26,8 +26,7 @@
 //      above its destination, so a round's writes never touch a later round's sources.
 // Bound by HBM on the moved rows and the weights, by the rounds' latency when few cells move.
 
-// CTAs have 8, 16 or 32 warps: many small ones, so that one's selection overlaps another's moves
-// (64 registers: four of 8 warps on an SM), or clusters of large ones for a few long sequences.
+// CTAs have 16 warps (two on an SM), or 32 and work in clusters for a few long sequences.
 constexpr int kEvMaxWarps = 32;
 constexpr int kEvMaxCluster = 16;               // (over 8: where the device takes it)
 constexpr int kEvMaxKeys = 48 * 1024;           // keys one CTA holds in shared memory at most
@@ -35,6 +34,7 @@ constexpr int kEvUnroll = 4;                    // rows in flight per half-warp
 constexpr int kEvTileUnroll = 4;                // fp8: sources in flight per warp
 constexpr int kEvLoad = 16;                     // weights in flight per lane
 constexpr int kEvBins = 2048;
+constexpr int kEvMaxBins = kEvBins / 512;       // per thread
 constexpr int kEvClusterPairs = kMaxSms / 2;    // clusters have two CTAs or more, at most one per SM
 constexpr size_t kEvHistBytes = static_cast<size_t>(kEvClusterPairs) * 3 * kEvBins * 4;  // ahead of the workspace
 
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
                 }
             }
             const int per = kEvBins / nt;                  // consecutive bins per thread, from the top
-            uint32_t cnt[8], sum = 0;
+            uint32_t cnt[kEvMaxBins], sum = 0;
             __syncthreads();
             rounds = round + 1;
             if (C > 1) {
@@ -223,13 +223,13 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
                     if (hist[i] != 0u) atomicAdd(all + i, hist[i]);
                 cluster_sync_all();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) cnt[k] = k < per ? __ldcg(all + kEvBins - 1 - (tid * per + k)) : 0u;
+                for (int k = 0; k < kEvMaxBins; ++k) cnt[k] = k < per ? __ldcg(all + kEvBins - 1 - (tid * per + k)) : 0u;
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) cnt[k] = k < per ? hist[kEvBins - 1 - (tid * per + k)] : 0u;
+                for (int k = 0; k < kEvMaxBins; ++k) cnt[k] = k < per ? hist[kEvBins - 1 - (tid * per + k)] : 0u;
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += cnt[k];
+            for (int k = 0; k < kEvMaxBins; ++k) sum += cnt[k];
             uint32_t incl = sum;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
                 uint32_t above = incl - sum;
                 bool found = false;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < kEvMaxBins; ++k) {
                     if (!found && above + cnt[k] >= want) {
                         found = true;
                         s_digit = kEvBins - 1 - (tid * per + k);
@@ -415,56 +415,59 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
         for (int t = rank * nwarps + warp; t < tiles; t += C * nwarps) {
             const int h0 = __ldcg(before + t), cnt = (t + 1 < tiles ? __ldcg(before + t + 1) : moves) - h0;
             if (cnt == 0) continue;
-            // lane i: the tile's i-th hole, where its token comes from and that page
-            int to = 0, from = 0, page = -1;
+            // lane i: slot of the tile's i-th hole, slot and tile (-1: bad page) its token comes from
+            int slots = 0, src_tile = -1;
             if (lane < cnt) {
-                to = __ldcg(holes + h0 + lane);
-                from = __ldcg(surplus + h0 + lane);
+                const int to = __ldcg(holes + h0 + lane), from = __ldcg(surplus + h0 + lane);
                 kept[to] = from;
-                page = page_of(from);
+                const int page = page_of(from);
+                src_tile = page < 0 ? -1 : page * p.Hkv + g;
+                slots = to % kPage | (from % kPage) << 8;
             }
             const int dst = page_of(t * kPage);
             if (dst < 0) continue;
-            uint8_t *blk = p.k_cache + (static_cast<size_t>(dst) * p.Hkv + g) * kBlk8Bytes;
+            const size_t dst_tile = static_cast<size_t>(dst) * p.Hkv + g;
+            uint8_t *blk = p.k_cache + dst_tile * kBlk8Bytes;
             uint4 *vrow = reinterpret_cast<uint4 *>(blk + kBlk8V);
             uint4 v[2] = {vrow[lane], vrow[lane + 32]};    // rows d = lane, lane + 32 of V^T
             for (int i0 = 0; i0 < cnt; i0 += kEvTileUnroll) {
                 uint4 krow[kEvTileUnroll];
                 uint32_t src[kEvTileUnroll][2];            // the words of rows lane, lane + 32 that hold the byte
                 float x[kEvTileUnroll];
-                int pg[kEvTileUnroll], ss[kEvTileUnroll], sd[kEvTileUnroll];
+                int tile[kEvTileUnroll], sl[kEvTileUnroll];
 #pragma unroll
                 for (int u = 0; u < kEvTileUnroll; ++u) {
-                    const int i = min(i0 + u, cnt - 1);
-                    pg[u] = __shfl_sync(0xffffffffu, page, i);
-                    ss[u] = __shfl_sync(0xffffffffu, from, i) % kPage;
-                    sd[u] = __shfl_sync(0xffffffffu, to, i) % kPage;
-                    if (i0 + u >= cnt) pg[u] = -1;
-                    if (pg[u] >= 0) {
-                        const uint8_t *from_blk = p.k_cache + (static_cast<size_t>(pg[u]) * p.Hkv + g) * kBlk8Bytes;
-                        const uint32_t *vs = reinterpret_cast<const uint32_t *>(from_blk + kBlk8V) + (ss[u] >> 2);
-                        src[u][0] = vs[4 * lane];
-                        src[u][1] = vs[4 * (lane + 32)];
-                        if (lane < 4) krow[u] = *reinterpret_cast<const uint4 *>(from_blk + ss[u] * kD + 16 * lane);
-                        if (lane == 4 || lane == 5) x[u] = reinterpret_cast<const float *>(from_blk + kBlk8S)[(lane - 4) * kPage + ss[u]];
-                        if (lane == 6) x[u] = p.weights[(static_cast<size_t>(pg[u]) * p.Hkv + g) * kPage + ss[u]];
+                    tile[u] = __shfl_sync(0xffffffffu, src_tile, min(i0 + u, cnt - 1));
+                    sl[u] = __shfl_sync(0xffffffffu, slots, min(i0 + u, cnt - 1));
+                    if (i0 + u >= cnt) tile[u] = -1;
+                    if (tile[u] >= 0) {
+                        const int ss = sl[u] >> 8;
+                        const uint8_t *from_blk = p.k_cache + static_cast<size_t>(tile[u]) * kBlk8Bytes;
+                        const uint32_t *vs = reinterpret_cast<const uint32_t *>(from_blk + kBlk8V) + (ss >> 2) + 4 * lane;
+                        src[u][0] = vs[0];
+                        src[u][1] = vs[128];
+                        if (lane < 4) krow[u] = *reinterpret_cast<const uint4 *>(from_blk + ss * kD + 16 * lane);
+                        if (lane == 4 || lane == 5) x[u] = reinterpret_cast<const float *>(from_blk + kBlk8S)[(lane - 4) * kPage + ss];
+                        if (lane == 6) x[u] = p.weights[static_cast<size_t>(tile[u]) * kPage + ss];
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < kEvTileUnroll; ++u) {
-                    if (pg[u] < 0) continue;
+                    if (tile[u] < 0) continue;
+                    const int ss = sl[u] >> 8, sd = sl[u] & 255;
+                    // byte ss % 4 of the source's word into byte sd % 4 of word sd / 4 of the row
+                    const int at = 4 * (sd & 3);
+                    const uint32_t pick = (0x3210u & ~(15u << at)) | (4u + (ss & 3)) << at;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {          // byte ss of the source row into byte sd of the row
-                        const uint32_t byte = (src[u][k] >> (8 * (ss[u] & 3))) & 255u, shift = 8 * (sd[u] & 3), mask = ~(255u << shift);
-                        const int word = sd[u] >> 2;
-                        if (word == 0) v[k].x = (v[k].x & mask) | byte << shift;
-                        else if (word == 1) v[k].y = (v[k].y & mask) | byte << shift;
-                        else if (word == 2) v[k].z = (v[k].z & mask) | byte << shift;
-                        else v[k].w = (v[k].w & mask) | byte << shift;
+                    for (int k = 0; k < 2; ++k) {
+                        if (sd < 4) v[k].x = __byte_perm(v[k].x, src[u][k], pick);
+                        else if (sd < 8) v[k].y = __byte_perm(v[k].y, src[u][k], pick);
+                        else if (sd < 12) v[k].z = __byte_perm(v[k].z, src[u][k], pick);
+                        else v[k].w = __byte_perm(v[k].w, src[u][k], pick);
                     }
-                    if (lane < 4) *reinterpret_cast<uint4 *>(blk + sd[u] * kD + 16 * lane) = krow[u];
-                    if (lane == 4 || lane == 5) reinterpret_cast<float *>(blk + kBlk8S)[(lane - 4) * kPage + sd[u]] = x[u];
-                    if (lane == 6) p.weights[(static_cast<size_t>(dst) * p.Hkv + g) * kPage + sd[u]] = x[u];
+                    if (lane < 4) *reinterpret_cast<uint4 *>(blk + sd * kD + 16 * lane) = krow[u];
+                    if (lane == 4 || lane == 5) reinterpret_cast<float *>(blk + kBlk8S)[(lane - 4) * kPage + sd] = x[u];
+                    if (lane == 6) p.weights[dst_tile * kPage + sd] = x[u];
                 }
             }
             vrow[lane] = v[0];
