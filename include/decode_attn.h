@@ -302,9 +302,10 @@ DA_API int decode_attn_multi_launches(da_shape s, int q_tokens, int ring_window,
  * correctly, in no fixed order. Cells of a page outside the pool are skipped
  * (DA_STATUS_BAD_PAGE). Cells appended by other calls hold whatever they held before: set a
  * page's weights to zero when it is handed out.
- * scale must be positive and finite. Workspace: the one-token workspace, and the weights
- * workspace (decode_attn_weights_workspace_bytes); both grow on first use outside graph
- * capture, else DA_ERR_WORKSPACE. Results (out, caches), status and errors otherwise as in
+ * scale must be positive and finite. Two launches. Workspace: the one-token workspace, and the
+ * weights workspace (decode_attn_weights_workspace_bytes: 4 bytes per query head and position
+ * of max_seq_len, or of the window, so give the true max_seq_len); both grow on first use
+ * outside graph capture, else DA_ERR_WORKSPACE. Results (out, caches), status and errors otherwise as in
  * decode_attn_paged / decode_attn_paged_fp8; after DA_STATUS_TIMEOUT the weights are garbage
  * too.
  */
@@ -361,8 +362,9 @@ DA_API int decode_attn_paged_multi_weights(const void *q, const void *k_new, con
  * Evicted sequences must not share pages with each other or with sequences that still need
  * them. A page outside the pool sets DA_STATUS_BAD_PAGE and the moves into or out of it are
  * skipped; a bad length sets DA_STATUS_BAD_SEQ_LEN and the slot is treated as inactive. One
- * launch, and the weights workspace (kv_evict_workspace_bytes). Other arguments and errors as
- * in decode_attn_paged.
+ * launch; at early-input levels 1 and 2 an empty one after it, so that the next attention call
+ * may read new_lens early. Weights workspace: kv_evict_workspace_bytes. Other arguments and
+ * errors as in decode_attn_paged.
  */
 DA_API int kv_evict(void *k_cache, void *v_cache, float *weights, const int32_t *block_table,
                     const int32_t *seq_lens, int32_t *new_lens, int32_t *kept, int keep, int keep_first,

@@ -508,8 +508,8 @@ def decode_attn_paged_weights(q, k_new, v_new, k_cache, v_cache, weights, block_
                                                                        dev)
     qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv, dev)
     _check(load_library().decode_attn_paged_weights(
-        qp, knp, vnp, kp, vp, wp, bp, lp, sp, window, scale, op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
-        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
+        qp, knp, vnp, kp, vp, wp, bp, lp, sp, int(window), float(scale), op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
+        max_pages * 16 if max_seq_len is None else int(max_seq_len), _raw_stream(stream, dev)))
     return out
 
 
@@ -520,8 +520,8 @@ def decode_attn_paged_fp8_weights(q, k_new, v_new, kv_cache, weights, block_tabl
     kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(kv_cache, None, weights, block_table, seq_lens, dev)
     qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv, dev)
     _check(load_library().decode_attn_paged_fp8_weights(
-        qp, knp, vnp, kp, wp, bp, lp, sp, window, scale, op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
-        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
+        qp, knp, vnp, kp, wp, bp, lp, sp, int(window), float(scale), op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
+        max_pages * 16 if max_seq_len is None else int(max_seq_len), _raw_stream(stream, dev)))
     return out
 
 
@@ -539,8 +539,8 @@ def decode_attn_paged_multi_weights(q, k_new, v_new, k_cache, v_cache, weights, 
     qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B, T), Hkv, dev)
     _check(load_library().decode_attn_paged_multi_weights(
         qp, knp, vnp, kp, vp, wp, bp, lp, None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev), sp,
-        window, scale, op, da_shape(B, Hq, Hkv, 64), T, 16, max_pages, num_pages,
-        max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
+        int(window), float(scale), op, da_shape(B, Hq, Hkv, 64), T, 16, max_pages, num_pages,
+        max_pages * 16 if max_seq_len is None else int(max_seq_len), _raw_stream(stream, dev)))
     return out
 
 
@@ -556,8 +556,8 @@ def kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_lens, kept, k
     keep = kept.shape[-1] if kept.dim() else 0
     _check(load_library().kv_evict(
         kp, vp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, (B,), dev),
-        _tensor("kept", kept, torch.int32, (B, Hkv, keep), dev), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
-        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
+        _tensor("kept", kept, torch.int32, (B, Hkv, keep), dev), keep, int(keep_first), int(keep_last), da_shape(B, Hkv, Hkv, 64), 16,
+        max_pages, num_pages, max_pages * 16 if max_seq_len is None else int(max_seq_len), _raw_stream(stream, dev)))
     return new_lens
 
 
@@ -569,8 +569,8 @@ def kv_evict_fp8(kv_cache, weights, block_table, seq_lens, new_lens, kept, keep_
     keep = kept.shape[-1] if kept.dim() else 0
     _check(load_library().kv_evict_fp8(
         kp, wp, bp, lp, _tensor("new_lens", new_lens, torch.int32, (B,), dev),
-        _tensor("kept", kept, torch.int32, (B, Hkv, keep), dev), keep, keep_first, keep_last, da_shape(B, Hkv, Hkv, 64), 16,
-        max_pages, num_pages, max_pages * 16 if max_seq_len is None else max_seq_len, _raw_stream(stream, dev)))
+        _tensor("kept", kept, torch.int32, (B, Hkv, keep), dev), keep, int(keep_first), int(keep_last), da_shape(B, Hkv, Hkv, 64), 16,
+        max_pages, num_pages, max_pages * 16 if max_seq_len is None else int(max_seq_len), _raw_stream(stream, dev)))
     return new_lens
 
 

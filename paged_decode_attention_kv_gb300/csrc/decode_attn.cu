@@ -2927,8 +2927,9 @@ size_t lse_bytes(const da_shape &s, int T) {
 // The weights workspace: the evictions' histograms (zero at rest, which no other call touches), the
 // denominators, and for a one-token call (T = 0) its scores, 16 tokens and G heads per tile of
 // the longest sequences.
-size_t weights_bytes(const da_shape &s, int T, int max_seq_len) {
-    const size_t tiles = T == 0 ? (static_cast<size_t>(max_seq_len) + kPage - 1) / kPage : 0;
+size_t weights_bytes(const da_shape &s, int T, int max_seq_len, int window = 0) {
+    size_t tiles = T == 0 ? (static_cast<size_t>(max_seq_len) + kPage - 1) / kPage : 0;
+    if (window > 0) tiles = std::min(tiles, static_cast<size_t>(window) / kPage + 2);
     return kEvHistBytes + lse_bytes(s, T) + static_cast<size_t>(s.batch) * s.num_q_heads * tiles * kPage * sizeof(float);
 }
 
@@ -3062,7 +3063,7 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     void *ws = nullptr;
     WeightsOut wo{nullptr, lse_rows(s, T), nullptr, false};
-    rc = prepare_weights(dev, stream, weights_bytes(s, T, max_seq_len), &ws, &wo.captured);
+    rc = prepare_weights(dev, stream, weights_bytes(s, T, max_seq_len, window), &ws, &wo.captured);
     if (rc != DA_OK) return rc;
     wo.nlse = reinterpret_cast<float *>(static_cast<char *>(ws) + kEvHistBytes);
     wo.scores = wo.nlse + lse_bytes(s, T) / sizeof(float);

@@ -306,48 +306,45 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const uint64_t dq = umma_sdesc(smem_addr(sQ), 16, 1024), dk = umma_sdesc(smem_addr(sKV), 16, 1024);
         const uint64_t dv = umma_sdesc(smem_addr(sKV) + kTcBlockBytes, 2048, 1024);
         auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity)); };
-        for (int j = 0; j <= nblk && !failed; ++j) {
-            if (j < nblk) {
-                const int s = j % kTcStages;
-                // buffer j % kTcSBufs last held P_{j-kTcSBufs}: its PV must be done
-                const int sb = j % kTcSBufs;
-                if (!wait_all(kv_full + 8 * s, (j / kTcStages) & 1) ||
-                    (j >= kTcSBufs && !wait_all(o_done + 8 * sb, ((j / kTcSBufs) - 1) & 1))) {
-                    failed = true;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t dks = dk + s * (kTcStageBytes / 16);
-                if (leader) {
+        auto scores = [&](int j) {  // S_j; false: a wait expired
+            const int s = j % kTcStages;
+            // buffer j % kTcSBufs last held P_{j-kTcSBufs}: its PV must be done
+            const int sb = j % kTcSBufs;
+            if (!wait_all(kv_full + 8 * s, (j / kTcStages) & 1) ||
+                (j >= kTcSBufs && !wait_all(o_done + 8 * sb, ((j / kTcSBufs) - 1) & 1)))
+                return false;
+            tc_fence_after();
+            const uint64_t dks = dk + s * (kTcStageBytes / 16);
+            if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk)
-                        umma_bf16_ss(tm + kTcColS + 64 * sb, dq + 2 * kk, dks + 2 * kk, id_qk, kk > 0);
-                    umma_commit(s_full + 8 * sb);
-                }
-                __syncwarp();
+                for (int kk = 0; kk < kD / 16; ++kk)
+                    umma_bf16_ss(tm + kTcColS + 64 * sb, dq + 2 * kk, dks + 2 * kk, id_qk, kk > 0);
+                umma_commit(s_full + 8 * sb);
             }
-            if (j >= 1) {
-                const int jj = j - 1, s = jj % kTcStages, pb = jj % kTcSBufs;
-                if (!wait_all(p_full + 8 * pb, (jj / kTcSBufs) & 1)) {
-                    failed = true;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t dvs = dv + s * (kTcStageBytes / 16);
-                const uint32_t acc = jj > 0 ? 1u : 0u;
-                if (leader) {
+            __syncwarp();
+            return true;
+        };
+        auto values = [&](int jj) {  // O += P_jj V_jj
+            const int s = jj % kTcStages, pb = jj % kTcSBufs;
+            if (!wait_all(p_full + 8 * pb, (jj / kTcSBufs) & 1)) return false;
+            tc_fence_after();
+            const uint64_t dvs = dv + s * (kTcStageBytes / 16);
+            const uint32_t acc = jj > 0 ? 1u : 0u;
+            if (leader) {
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)  // P = hi + lo
+                for (int part = 0; part < 2; ++part)  // P = hi + lo
 #pragma unroll
-                        for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                            umma_bf16_ts(tm + kTcColO, tm + kTcColS + 64 * pb + 32 * part + 8 * kk, dvs + 128 * kk, id_pv,
-                                         part > 0 || kk > 0 ? 1u : acc);
-                    umma_commit(o_done + 8 * pb);
-                    umma_commit(kv_empty + 8 * s);
-                }
-                __syncwarp();
+                    for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                        umma_bf16_ts(tm + kTcColO, tm + kTcColS + 64 * pb + 32 * part + 8 * kk, dvs + 128 * kk, id_pv,
+                                     part > 0 || kk > 0 ? 1u : acc);
+                umma_commit(o_done + 8 * pb);
+                umma_commit(kv_empty + 8 * s);
             }
-        }
+            __syncwarp();
+            return true;
+        };
+        for (int j = 0; j <= nblk && !failed; ++j)
+            if ((j < nblk && !scores(j)) || (j >= 1 && !values(j - 1))) failed = true;
         if (leader) {
             umma_commit(drain);  // completes when every MMA issued above has
             mbar_wait_bounded(drain, 0);

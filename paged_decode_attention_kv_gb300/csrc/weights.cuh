@@ -277,8 +277,10 @@ struct SkLayout {
     static constexpr int kEpi = N == kMwMaxRows ? 16 : 8;      // warps that sum
     static constexpr int kParts = kEpi / 4;                    // shares of the columns
     static constexpr int kThreads = (kEpi + 2) * 32;
-    static constexpr int kCtas = N == kMwMaxRows ? 1 : 2;      // resident per SM
-    static constexpr int kRing = N == kMwMaxRows ? 8 : 4;
+    // resident per SM (N = 32: 4 tokens x 32 sequences 122 us with three CTAs of three stages, 128 with
+    // two of four)
+    static constexpr int kCtas = N == kMwMaxRows ? 1 : N == 32 ? 3 : 2;
+    static constexpr int kRing = N == kMwMaxRows ? 8 : N == 32 ? 3 : 4;
     static constexpr int k = N * kD * 2;
     static constexpr int lse = k + kRing * kMwKBytes;
     static constexpr int acc = lse + N * 4;

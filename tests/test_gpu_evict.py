@@ -208,6 +208,42 @@ def test_graph_replay_and_repeated_calls():
         c.w = np.random.default_rng(12).random(c.w.shape).astype(np.float32)
 
 
+@pytest.mark.parametrize("level", [0, 1, 2])
+def test_the_next_call_reads_the_new_lengths(level):
+    """An eviction and an attention call on its new_lens right behind it, at every early-input level
+    (the early levels read the lengths before they wait for the kernel before): the same output
+    as with a wait between the two, every time. The lengths start as ones, so that a stale
+    read shows."""
+    c = Cache(13, 2, [700, 300, 1500, 64], False, width=120)
+    w0, bt, sl = dev(c.w), dev(c.bt), dev(c.lens)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    pages = c.k.shape[0]
+    k0, v0 = (torch.randn((pages, 2, 16, 64), generator=gen, device=DEV).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((4, 16, 64), generator=gen, device=DEV).to(torch.bfloat16)
+    kept = torch.zeros((4, 2, 150), dtype=torch.int32, device=DEV)
+
+    def run(wait):
+        k, v, w = k0.clone(), v0.clone(), w0.clone()
+        nl, out = torch.ones_like(sl), torch.empty_like(q)
+        torch.cuda.synchronize()
+        da.kv_evict(k, v, w, bt, sl, nl, kept, 4, 30)
+        if wait:
+            torch.cuda.synchronize()
+        da.decode_attn_paged(q, None, None, k, v, bt, nl, None, 0, 0.125, out)
+        torch.cuda.synchronize()
+        return out
+
+    prev = da.decode_attn_set_early_inputs(level)
+    try:
+        want = run(True)
+        for _ in range(10):
+            assert torch.equal(run(False).view(torch.int16), want.view(torch.int16))
+    finally:
+        da.decode_attn_set_early_inputs(prev)
+    assert da.decode_attn_device_status() == 0
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_prompt_then_decode_under_a_budget(fp8):
     """The calls as an engine uses them: a prompt with weights (bf16), decode steps that append and
