@@ -302,6 +302,11 @@ DA_API int decode_attn_multi_launches(da_shape s, int q_tokens, int ring_window,
  * correctly, in no fixed order. Cells of a page outside the pool are skipped
  * (DA_STATUS_BAD_PAGE). Cells appended by other calls hold whatever they held before: set a
  * page's weights to zero when it is handed out.
+ * fp8 cache: the new token's scale is max_d |x_d| * (1 / 448), the fp32 reciprocal of 448, and
+ * code_d the e4m3 value nearest to x_d / scale: the bytes of x.abs().amax(-1) / 448 and a cast
+ * to float8_e4m3fn in torch on a GPU, which divides by a constant that way, so that a token
+ * appended here and one quantised by torch code (a prompt's, say) are held alike. The scale is
+ * at most one unit in the last place from decode_attn_paged_fp8's, which divides.
  * scale must be positive and finite. Two launches. Workspace: the one-token workspace, and the
  * weights workspace (decode_attn_weights_workspace_bytes: 4 bytes per query head and position
  * of max_seq_len, or of the window, so give the true max_seq_len); both grow on first use

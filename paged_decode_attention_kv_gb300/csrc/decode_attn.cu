@@ -1772,8 +1772,13 @@ __global__ void __launch_bounds__(kThreads, CPS)
                             ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, off));
                             va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, off));
                         }
-                        knew_scale = ka > 0.f ? __fdiv_rn(ka, 448.f) : 1.f;
-                        vnew_scale = va > 0.f ? __fdiv_rn(va, 448.f) : 1.f;
+                        if constexpr (WTS) {  // the reciprocal rule of these calls
+                            knew_scale = ka > 0.f ? __fmul_rn(ka, 1.f / 448.f) : 1.f;
+                            vnew_scale = va > 0.f ? __fmul_rn(va, 1.f / 448.f) : 1.f;
+                        } else {
+                            knew_scale = ka > 0.f ? __fdiv_rn(ka, 448.f) : 1.f;
+                            vnew_scale = va > 0.f ? __fdiv_rn(va, 448.f) : 1.f;
+                        }
                         knew = f32x2_to_e4m3x2(__fdiv_rn(kf.x, knew_scale), __fdiv_rn(kf.y, knew_scale));
                         vnew = f32x2_to_e4m3x2(__fdiv_rn(vf.x, vnew_scale), __fdiv_rn(vf.y, vnew_scale));
                     }

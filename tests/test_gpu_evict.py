@@ -270,7 +270,7 @@ def test_prompt_then_decode_under_a_budget(fp8):
         if not fp8:
             return x.double().numpy()
         top = x.float().abs().amax(-1, keepdim=True)
-        sc = torch.where(top > 0, top / 448, torch.ones_like(top))
+        sc = torch.where(top > 0, top * torch.tensor(np.float32(1) / np.float32(448)), torch.ones_like(top))
         return ((x.float() / sc).to(torch.float8_e4m3fn).double() * sc.double()).numpy()
 
     def attend(b, q, n):

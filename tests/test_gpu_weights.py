@@ -12,7 +12,7 @@ import paged_decode_attention_kv_gb300 as da
 import plain_weights as pw
 from cases import bf16_to_f64, paged_identity, shuffle_pages
 from paged_decode_attention_kv_gb300 import workloads as wl
-from test_gpu_decode import DEV, dev, dev_bits
+from test_gpu_decode import DEV, assert_close, dev, dev_bits
 from test_gpu_multi import counts, ramp_keys
 from test_oracle_multi import Multi
 
@@ -240,25 +240,54 @@ def test_sequences_that_share_their_first_pages():
 
 
 # ---------------------------------------------------------------- fp8
+def quantised(bits):
+    """Codes (bytes) and scale of one row of bf16 bits: scale max |x| times the fp32 reciprocal of 448,
+    codes the nearest e4m3 to x / scale."""
+    x = torch.from_numpy(bf16_to_f64(bits).astype(np.float32))
+    top = x.abs().max().numpy()
+    scale = np.float32(top) * (np.float32(1) / np.float32(448)) if top > 0 else np.float32(1)
+    return (x / torch.tensor(scale)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy(), scale
+
+
+def append_fp8(blocks, c, bt):
+    """The new token of every active sequence into copies of the 2176-byte blocks."""
+    out = blocks.copy()
+    for b, L in enumerate(c.lens):
+        if L == 0:
+            continue
+        page, slot = bt[b, (L - 1) // 16], (L - 1) % 16
+        for g in range(c.Hkv):
+            (kc, ks), (vc, vs) = quantised(c.k_new[b, g]), quantised(c.v_new[b, g])
+            blk = out[page, g]
+            blk[slot * 64:slot * 64 + 64] = kc
+            blk[1024 + slot:2048:16] = vc
+            scales = blk[2048:].view(np.float32)
+            scales[slot], scales[16 + slot] = ks, vs
+    return out
+
+
 def run_fp8(m, window, seed=1, fused=True, sinks=True):
     c = m.c
     held = m.base if fused else c.lens
     kp, vp, bt = paged_identity(c, held)
     kp, vp, bt = shuffle_pages(kp, vp, bt, seed, spare=4)
     cache = oracle.scatter_fp8(c.hist_k, c.hist_v, held, oracle.Fp8Cache.empty_paged(kp.shape[0], c.Hkv, 16, c.D), block_table=bt)
-    after = oracle.kv_append_fp8(c.k_new, c.v_new, cache, c.lens, block_table=bt) if fused else cache
+    start = np.ascontiguousarray(cache.blocks.reshape(kp.shape[0], c.Hkv, -1))
+    blocks = append_fp8(start, c, bt) if fused else start
     w0 = start_weights(kp.shape[0], c.Hkv, bt, held, seed)
-    kv, kv2, w = torch.from_numpy(cache.blocks.copy()).to(DEV), torch.from_numpy(cache.blocks.copy()).to(DEV), dev(w0)
+    kv, w = dev(start), dev(w0)
     q = dev_bits(m.q)[:, 0].contiguous()
     kn, vn = (dev_bits(c.k_new), dev_bits(c.v_new)) if fused else (None, None)
-    out, ref = torch.full_like(q, float("nan")), torch.full_like(q, float("nan"))
+    out = torch.full_like(q, float("nan"))
     sk = dev(c.sinks) if sinks else None
     da.decode_attn_paged_fp8_weights(q, kn, vn, kv, w, dev(bt), dev(c.lens), sk, window, c.scale, out)
-    da.decode_attn_paged_fp8(q, kn, vn, kv2, dev(bt), dev(c.lens), sk, window, c.scale, ref)
     torch.cuda.synchronize()
     assert da.decode_attn_device_status() == 0
-    assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(kv, kv2)
-    blocks = after.blocks.reshape(kp.shape[0], c.Hkv, -1)
+    np.testing.assert_array_equal(kv.cpu().numpy(), blocks)
+    if not fused:  # nothing is quantised: the output of the call without weights, bit for bit
+        ref = torch.full_like(q, float("nan"))
+        da.decode_attn_paged_fp8(q, None, None, kv, dev(bt), dev(c.lens), sk, window, c.scale, ref)
+        assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
     codes = torch.from_numpy(np.ascontiguousarray(blocks[..., :2048])).view(torch.float8_e4m3fn).double().numpy()
     scales = np.ascontiguousarray(blocks[..., 2048:]).view(np.float32).astype(np.float64)
     k = codes[..., :1024].reshape(-1, c.Hkv, 16, 64) * scales[..., :16, None]
@@ -268,6 +297,12 @@ def run_fp8(m, window, seed=1, fused=True, sinks=True):
         at = np.arange(L)
         keys.append(k[bt[b, at // 16], :, at % 16])
         values.append(v[bt[b, at // 16], :, at % 16])
+    want = np.zeros(q.shape)
+    for b, L in enumerate(c.lens):
+        if L > 0:
+            want[b] = pw.step(bf16_to_f64(m.q[b]), keys[b], values[b], int(L), 1, c.sinks.astype(np.float64) if sinks else None,
+                              window, c.scale)[0][0]
+    assert_close(out.double().cpu().numpy(), want, f"fp8 weights window={window}")
     # twice the bound: a score is (codes . q) * scale_k, one rounding more, and a query value below
     # fp16's normal range is off by up to 2^-25
     check_weights(w.cpu().numpy(), w0, bt, c.lens, m.n, bf16_to_f64(m.q), keys, values,
@@ -278,6 +313,33 @@ def run_fp8(m, window, seed=1, fused=True, sinks=True):
 @pytest.mark.parametrize("window", [0, 7, 100])
 def test_fp8(Hq, Hkv, window):
     run_fp8(one_token(1400 + Hq + window, Hq, Hkv, EDGE), window, seed=Hq)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(64, 8), (16, 1)])
+def test_fp8_rows_as_torch_quantises_them(Hq, Hkv):
+    """The appended bytes of rows whose largest values make the reciprocal and the division differ
+    (and codes near a tie with them) are those of the torch expression on the GPU."""
+    lens = [1 + i for i in range(128)]
+    m = one_token(1420 + Hq, Hq, Hkv, lens)
+    gen = np.random.default_rng(Hq)
+    for b in range(128):  # every bf16 mantissa as a row's largest value
+        for x in (m.c.k_new, m.c.v_new):
+            x[b] = (gen.integers(0, 128, x[b].shape) | 0x3f00 | gen.integers(0, 2, x[b].shape) << 15).astype(np.uint16)
+            x[b, :, 5] = 0x4000 | b
+    kp, vp, bt = paged_identity(m.c, m.base)
+    kv = torch.zeros((kp.shape[0], Hkv, 2176), dtype=torch.uint8, device=DEV)
+    q, kn, vn = dev_bits(m.q)[:, 0].contiguous(), dev_bits(m.c.k_new), dev_bits(m.c.v_new)
+    w = torch.zeros((kp.shape[0], Hkv, 16), device=DEV)
+    da.decode_attn_paged_fp8_weights(q, kn, vn, kv, w, dev(bt), dev(m.c.lens), None, 0, m.c.scale, torch.empty_like(q))
+    for x, at, scale_at in ((kn, None, 0), (vn, 1024, 16)):
+        top = x.float().abs().amax(-1, keepdim=True)
+        scale = top / 448
+        codes = (x.float() / scale).to(torch.float8_e4m3fn).view(torch.uint8)
+        for b in range(128):
+            blk, slot = kv[int(bt[b, b // 16])], b % 16
+            got = blk[:, slot * 64:slot * 64 + 64] if at is None else blk[:, at + slot:at + 1024:16]
+            assert torch.equal(got, codes[b])
+            assert torch.equal(blk[:, 2048:].contiguous().view(torch.float32)[:, scale_at + slot], scale[b, :, 0])
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(64, 8), (16, 1)])
