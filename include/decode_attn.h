@@ -331,7 +331,8 @@ DA_API int decode_attn_paged_fp8_weights(const void *q, const void *k_new, const
  * summed over the new tokens' query rows too: weights[cell(j), g] += sum over t < n and the
  * query heads of g of P[t][h][j]. The cells of the n new tokens are set to their sums. A prompt
  * of which only the last tokens' attention is to count goes through decode_attn_paged_multi up
- * to them and through this call from there. Workspaces: the multi-token one and the weights
+ * to them and through this call from there. One launch more than decode_attn_multi_launches
+ * says. Workspaces: the multi-token one and the weights
  * one. scale must be positive and finite; everything else as in decode_attn_paged_multi.
  */
 DA_API int decode_attn_paged_multi_weights(const void *q, const void *k_new, const void *v_new, void *k_cache,

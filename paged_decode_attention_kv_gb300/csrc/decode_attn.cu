@@ -3225,8 +3225,10 @@ int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int3
         of16 = evict_clusters_of_16(kern);
         g_dev[dev].evict_clusters[kv8].store(of16, std::memory_order_release);
     }
-    // (clusters of 16 only if all are resident at once: a second wave takes as long as the first)
-    const int most = pairs <= of16 ? kEvMaxCluster : 8;
+    // (clusters of 16 only if all are resident at once: a second wave takes as long as the first; none
+    // below 8192 cells, where their barriers cost more than their warps save: 8 sequences of 4160
+    // cells 19 us with one CTA, 21 with two; one of 16384 27 us with four, 23 with eight)
+    const int most = max_seq_len < 8192 ? 1 : pairs <= of16 ? kEvMaxCluster : 8;
     int C = 1;
     while (C < most && 2 * C * pairs <= sms && pairs <= kEvClusterPairs && 2 * C * warps * 32 <= max_seq_len) C *= 2;
     const int chunks = (max_seq_len + 31) / 32, cpw = (chunks + C * warps - 1) / (C * warps);

@@ -137,6 +137,10 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
     const int nt = blockDim.x, nwarps = nt >> 5;
     const int C = gridDim.x, rank = blockIdx.x;            // the cluster spans the grid's x
     const int g = blockIdx.y, b = blockIdx.z;
+    auto sync_cluster = [&]() {
+        if (C > 1) cluster_sync_all();
+        else __syncthreads();
+    };
     for (int i = tid; i < 2 * kEvBins; i += nt) (&s_hist[0][0])[i] = 0u;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
                 uint32_t *const all = ghist + round * kEvBins;
                 for (int i = tid; i < kEvBins; i += nt)
                     if (hist[i] != 0u) atomicAdd(all + i, hist[i]);
-                cluster_sync_all();
+                sync_cluster();
 #pragma unroll
                 for (int k = 0; k < kEvMaxBins; ++k) cnt[k] = k < per ? __ldcg(all + kEvBins - 1 - (tid * per + k)) : 0u;
             } else {
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
         t.w = __reduce_add_sync(0xffffffffu, t.w);
         if (lane == 0) s_tally[warp] = t;
     }
-    cluster_sync_all();
+    sync_cluster();
     if (C > 1)  // every CTA has read the sums: zero again for the next call
         for (int i = rank * nt + tid; i < rounds * kEvBins; i += C * nt) ghist[i] = 0u;
     if (tid < C * nwarps) {
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
                 if (__shfl_sync(0xffffffffu, same, i) >> lane & 1u) kept[cb + 32 * i + lane] = cb + 32 * i + lane;
         }
     }
-    cluster_sync_all();
+    sync_cluster();
 
     // ---- 5. surplus cells into the holes
     const int hl = lane & 15;
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kEvMaxWarps * 32) kv_evict_kernel(const EvictP
                 if (from[u] >= 0) ev_load(p, row[u], from[u], (dst + shift) % kPage, g, hl);
             }
         }
-        if (i0 == 0 || overlap) cluster_sync_all();
+        if (i0 == 0 || overlap) sync_cluster();
 #pragma unroll
         for (int u = 0; u < kEvUnroll; ++u) {
             const int i = i0 + half + u * halves;
