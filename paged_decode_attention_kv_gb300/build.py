@@ -1,6 +1,6 @@
 """Build the CUDA library libdecode_attn.so in-tree for GB300 (sm_103a).
 
-One translation unit (decode_attn.cu, which includes multi_attn.cuh), nvcc, static CUDA runtime; the driver API entry used
+One translation unit (decode_attn.cu, which includes the .cuh files), nvcc, static CUDA runtime; the driver API entry used
 for tensor maps is resolved at run time, so the library loads on a machine
 without a GPU (for the ABI checks) and needs no libcuda at link time.
 """
