@@ -165,6 +165,14 @@ def test_prompt_chunks(T, lens):
     run_multi(m, 0, sinks=False)
 
 
+def test_most_query_tokens_and_most_slots():
+    """4096 new tokens of 16 query heads per KV head (65536 rows), and 1024 slots."""
+    run_multi(Multi(1290, 16, 1, [4096, 100], [4096, 100], 4096), 0)
+    lens = [1 + i % 40 for i in range(1024)]
+    run_multi(Multi(1291, 2, 1, lens, [min(L, 3) for L in lens], 3), 0)
+    run_multi(Multi(1292, 8, 1, lens, [min(L, 9) for L in lens], 9), 5)
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (64, 8)])
 @pytest.mark.parametrize("T", [4, 6, 16, 32])
 def test_several_tokens_behind_a_long_history(Hq, Hkv, T):
