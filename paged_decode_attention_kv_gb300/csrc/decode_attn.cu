@@ -3089,7 +3089,7 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     p.Hkv = s.num_kv_heads;
     p.G = G;
     p.T = T;
-    p.window = window;
+    p.window = window < max_seq_len ? window : 0;  // (a window no sequence fills is none: sums with it stay in 32 bits)
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.max_seq_len = max_seq_len;
@@ -3103,7 +3103,7 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
                         : launch_score_weights<16>(p, dev, stream);
     // the 128-key stages of the longest range that any sequence's rows can see
     const int rows = T * G;
-    const long long span = window > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(window) + T + kMwKeys) : max_seq_len;
+    const long long span = p.window > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(p.window) + T + kMwKeys) : max_seq_len;
     const long long stages = (span + kMwKeys - 1) / kMwKeys;
     const long long pairs = static_cast<long long>(s.batch) * s.num_kv_heads;
     const int N = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : kMwMaxRows;  // (rows that stay)

@@ -180,6 +180,14 @@ def test_several_tokens_behind_a_long_history(Hq, Hkv, T):
     run_multi(m, 0)
 
 
+def test_windows_that_no_sequence_fills():
+    """A window of the largest integer is no window."""
+    for window in (1000, 1001, 2 ** 31 - 1):
+        run_multi(one_token(1305, 16, 2, [1000, 17, 0, 300]), window, one=True)
+        for T in (3, 9, 70):
+            run_multi(Multi(1306 + T, 16, 2, [1000, 17, 0, 300], [T, min(T, 17), 0, T], T), window)
+
+
 def test_counts_beyond_a_sequence_do_not_touch_it():
     m = Multi(1310, 8, 8, [10, 20], [2, 2], 2)
     kp, vp, bt = m.paged(1)
