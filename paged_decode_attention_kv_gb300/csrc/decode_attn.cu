@@ -3005,7 +3005,7 @@ int launch_score_weights(const WeightParams &p, int dev, cudaStream_t stream) {
 // One of the several-token weight kernels, `idx` its attribute flag.
 template <typename Kernel>
 int launch_row_weights(Kernel kern, int idx, int threads, size_t smem, const CUtensorMap &mk, const CUtensorMap &mq,
-                       const WeightParams &p, long long blocks, int dev, cudaStream_t stream) {
+                       const WeightParams &p, dim3 grid, int dev, cudaStream_t stream) {
     if (!g_dev[dev].mw_attr_set[idx].load(std::memory_order_acquire)) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e == cudaSuccess)
@@ -3014,7 +3014,7 @@ int launch_row_weights(Kernel kern, int idx, int threads, size_t smem, const CUt
         g_dev[dev].mw_attr_set[idx].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), p.Hkv, p.B);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -3029,15 +3029,17 @@ int launch_row_weights(Kernel kern, int idx, int threads, size_t smem, const CUt
 template <int N>
 int launch_stream_keys(int idx, const CUtensorMap &mk, const CUtensorMap &mq, const WeightParams &p, long long runs,
                        int dev, cudaStream_t stream) {
-    return launch_row_weights(stream_keys_weights_kernel<N>, idx, SkLayout<N>::kThreads, SkLayout<N>::bytes, mk, mq, p, runs,
-                              dev, stream);
+    return launch_row_weights(stream_keys_weights_kernel<N>, idx, SkLayout<N>::kThreads, SkLayout<N>::bytes, mk, mq, p,
+                              dim3(static_cast<unsigned>(runs), p.Hkv, p.B), dev, stream);
 }
 
 template <int TILES>
 int launch_stream_rows(int idx, const CUtensorMap &mk, const CUtensorMap &mq, const WeightParams &p, long long blocks,
                        int dev, cudaStream_t stream) {
+    const long long ctas = blocks * p.Hkv * p.B;
+    if (ctas > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
     return launch_row_weights(stream_rows_weights_kernel<TILES>, idx, SrLayout<TILES>::kThreads, SrLayout<TILES>::bytes, mk,
-                              mq, p, blocks, dev, stream);
+                              mq, p, dim3(static_cast<unsigned>(ctas)), dev, stream);
 }
 
 // One step of attention (T = 0: one token per sequence; else T, with q_lens) over a paged cache

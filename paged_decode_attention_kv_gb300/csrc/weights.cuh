@@ -472,7 +472,10 @@ __global__ void __launch_bounds__(SrLayout<TILES>::kThreads, SrLayout<TILES>::kC
     __shared__ int s_failed;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = blockIdx.y, b = blockIdx.z;
+    // Key blocks are the slowest index: behind a causal mask the first keys are seen by the most rows,
+    // so the longest CTAs of every (sequence, KV head) start first.
+    const int pairs = p.B * p.Hkv, block = blockIdx.x / pairs, pair = blockIdx.x % pairs;
+    const int g = pair % p.Hkv, b = pair / p.Hkv;
     if (tid == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmq)) : "memory");
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(SrLayout<TILES>::kThreads, SrLayout<TILES>::kC
     if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const MwKeys k = mw_keys(p, b);
     if (!k.ok) return;
-    const int first = k.lo0 / kMwKeys * kMwKeys + blockIdx.x * kKeys;
+    const int first = k.lo0 / kMwKeys * kMwKeys + block * kKeys;
     if (first >= k.L) return;
     // the blocks of rows that see one of the keys
     const int last = min(first + kKeys, k.L) - 1;
