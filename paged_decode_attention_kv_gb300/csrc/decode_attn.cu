@@ -3116,8 +3116,8 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
         return DA_ERR_CUDA;
     }
     if (rows > kMwMaxRows) {
-        // 256 keys per CTA where that still gives every SM one (512 tokens behind 7680: 280 us against
-        // 285 with 128 keys and two CTAs per SM; four prompts of up to 2048: 390 against 397)
+        // 256 keys per CTA where that still gives every SM one (512 tokens behind 7680: 278 us against
+        // 284 with 128 keys and two CTAs per SM; four prompts of up to 2048: 360 against 363)
         const bool two = stages * pairs >= 2 * sm_count(dev);
         const long long blocks = two ? (stages + 1) / 2 : stages;
         return two ? launch_stream_rows<2>(5, mk, mq, p, blocks, dev, stream)
