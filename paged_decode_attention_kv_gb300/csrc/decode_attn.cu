@@ -627,8 +627,9 @@ __device__ __forceinline__ void state_write_out_mt(SegState<NT> &s, const float 
 }
 
 // Minus log2 of a row's softmax denominator: running maximum M (sink included, log2 units) and
-// the sum under it; -inf for a row that saw no key and has no sink (not a query row), so that
-// every weight 2^(s + nlse) of it is 0.
+// the sum under it; -inf for a row of no finite score and no sink, so that every weight
+// 2^(s + nlse) of it is 0. Every query row's is written by every call: what an earlier call left
+// in the workspace (a NaN, say) must not reach the weights.
 __device__ __forceinline__ float neg_log2_den(float M, float den) { return M == -INFINITY ? -INFINITY : -(M + log2f(den)); }
 
 // The same for a segment finished by one warp: column c is query row r0 + c, nlse_bg its

@@ -532,11 +532,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     const int h = g * p.G + (r - t * p.G);
                     const float sg = p.sinks != nullptr ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
                     const float M = fmaxf(m_ref, sg);
+                    float den = 0.f;
                     if (M != -INFINITY) {
-                        const float den = l * exp2f(m_ref - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
+                        den = l * exp2f(m_ref - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
                         f = den > 0.f ? exp2f(m_ref - M) / den : 0.f;
-                        if (p.nlse != nullptr) p.nlse[bg * p.lse_ld + r] = neg_log2_den(M, den);
                     }
+                    if (p.nlse != nullptr) p.nlse[bg * p.lse_ld + r] = neg_log2_den(M, den);
                 }
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out + row_off(r));
 #pragma unroll
