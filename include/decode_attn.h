@@ -40,7 +40,9 @@
  *     a larger workspace returns DA_ERR_WORKSPACE instead of allocating.
  *     Calls that run concurrently on different streams of one device share
  *     this workspace and must not overlap, unless each of those streams has a
- *     workspace of its own (decode_attn_stream_reserve).
+ *     workspace of its own (decode_attn_stream_reserve). A buffer that a captured call put
+ *     into a graph is kept when the workspace outgrows it, so that the graph can still be
+ *     launched (until the process ends, or decode_attn_stream_release for a stream's own).
  */
 #ifndef DECODE_ATTN_H
 #define DECODE_ATTN_H
@@ -387,9 +389,7 @@ DA_API size_t decode_attn_weights_workspace_bytes(da_shape s, int q_tokens, int 
 DA_API size_t kv_evict_workspace_bytes(da_shape s, int keep);
 /* Grow the weights workspace that calls on `stream` use (the stream's own after
  * decode_attn_stream_reserve, else the device's) to at least `bytes`; call before capturing.
- * DA_ERR_WORKSPACE if that would allocate while `stream` is capturing. A buffer that a captured
- * graph uses is kept when the workspace grows past it (until the process ends, or
- * decode_attn_stream_release for a stream's own). */
+ * DA_ERR_WORKSPACE if that would allocate while `stream` is capturing. */
 DA_API int decode_attn_weights_reserve(void *stream, size_t bytes);
 
 /*

@@ -2337,9 +2337,9 @@ int grow_locked(Workspace &w, size_t bytes) {
 }
 
 // The workspace a call on `stream` uses (the stream's own if it has one, else the
-// device's), grown to `need` unless the stream is capturing. Under g_mu. captured: the stream
-// is known to be capturing, the buffer goes into a graph.
-int workspace_locked(int dev, cudaStream_t stream, WorkspaceKind kind, size_t need, void **ptr, bool captured = false) {
+// device's), grown to `need` unless the stream is capturing. Under g_mu. A call that is captured
+// puts the buffer's address into a graph, whatever the call: from then on the buffer is kept.
+int workspace_locked(int dev, cudaStream_t stream, WorkspaceKind kind, size_t need, void **ptr) {
     Workspace *w = &g_dev[dev].ws[kind];
     if (g_n_stream_ws.load(std::memory_order_relaxed) > 0) {
         auto it = g_stream_ws.find(stream);
@@ -2348,11 +2348,12 @@ int workspace_locked(int dev, cudaStream_t stream, WorkspaceKind kind, size_t ne
             w = &it->second.ws[kind];
         }
     }
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &cs);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    const bool captured = cs != cudaStreamCaptureStatusNone;
     if (w->bytes < need) {
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        cudaError_t e = cudaStreamIsCapturing(stream, &cs);
-        if (e != cudaSuccess) return set_cuda_error(e);
-        if (cs != cudaStreamCaptureStatusNone) return DA_ERR_WORKSPACE;
+        if (captured) return DA_ERR_WORKSPACE;
         int rc = grow_locked(*w, need);
         if (rc != DA_OK) return rc;
     }
@@ -2408,12 +2409,12 @@ int launch_attn(const CUtensorMap &mk, const CUtensorMap &mv, const Params &prm,
     return DA_OK;
 }
 
-int prepare_workspace(int dev, int G, cudaStream_t stream, float **part, int **counters, bool captured = false) {
+int prepare_workspace(int dev, int G, cudaStream_t stream, float **part, int **counters) {
     const size_t need = workspace_for(G, sm_count(dev));
     void *ws = nullptr;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        int rc = workspace_locked(dev, stream, kWsDecode, need, &ws, captured);
+        int rc = workspace_locked(dev, stream, kWsDecode, need, &ws);
         if (rc != DA_OK) return rc;
     }
     *counters = static_cast<int *>(ws);
@@ -2428,12 +2429,11 @@ std::atomic<int> g_expire_next{-1};
 std::atomic<int> g_early_inputs{0};
 
 // What a call that accumulates attention weights adds to the attention it runs: where the
-// denominators and (one token) the scores go, and whether the stream is capturing a graph.
+// denominators and (one token) the scores go.
 struct WeightsOut {
     float *nlse;
     int lse_ld;
     float *scores;
-    bool captured;
 };
 
 int run_attention(bool ring, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
@@ -2500,7 +2500,7 @@ int run_attention(bool ring, const void *q, const void *k_new, const void *v_new
     prm.nlse = wts ? wts->nlse : nullptr;
     prm.lse_ld = wts ? wts->lse_ld : 0;
     prm.scores = wts ? wts->scores : nullptr;
-    rc = prepare_workspace(dev, G, stream, &prm.part, &prm.counters, wts != nullptr && wts->captured);
+    rc = prepare_workspace(dev, G, stream, &prm.part, &prm.counters);
     if (rc != DA_OK) return rc;
 
     CUtensorMap mk, mv;
@@ -2760,8 +2760,7 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
     {
         std::lock_guard<std::mutex> lk(g_mu);
         rc = workspace_locked(dev, stream, kWsMulti,
-                              rope ? rope_off + rope_scratch_bytes(s, T) : m.counter_bytes + m.part_bytes, &ws,
-                              wts != nullptr && wts->captured);
+                              rope ? rope_off + rope_scratch_bytes(s, T) : m.counter_bytes + m.part_bytes, &ws);
         if (rc != DA_OK) return rc;
     }
     if (rope) {  // rotate q and k_new into the workspace; the attention reads them from there
@@ -2939,14 +2938,10 @@ size_t weights_bytes(const da_shape &s, int T, int max_seq_len, int window = 0) 
     return kEvHistBytes + lse_bytes(s, T) + static_cast<size_t>(s.batch) * s.num_q_heads * tiles * kPage * sizeof(float);
 }
 
-// The weights workspace of a call on `stream`; *captured: the stream is capturing a graph.
-int prepare_weights(int dev, cudaStream_t stream, size_t need, void **ws, bool *captured) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(stream, &cs);
-    if (e != cudaSuccess) return set_cuda_error(e);
-    *captured = cs != cudaStreamCaptureStatusNone;
+// The weights workspace of a call on `stream`.
+int prepare_weights(int dev, cudaStream_t stream, size_t need, void **ws) {
     std::lock_guard<std::mutex> lk(g_mu);
-    return workspace_locked(dev, stream, kWsWeights, need, ws, *captured);
+    return workspace_locked(dev, stream, kWsWeights, need, ws);
 }
 
 // q [B][T][Hq][64] as blocks of `rows` query rows (t, h) of one KV head: dims {64, Hq, B T}, box
@@ -3070,8 +3065,8 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     if (rc != DA_OK) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     void *ws = nullptr;
-    WeightsOut wo{nullptr, lse_rows(s, T), nullptr, false};
-    rc = prepare_weights(dev, stream, weights_bytes(s, T, max_seq_len, window), &ws, &wo.captured);
+    WeightsOut wo{nullptr, lse_rows(s, T), nullptr};
+    rc = prepare_weights(dev, stream, weights_bytes(s, T, max_seq_len, window), &ws);
     if (rc != DA_OK) return rc;
     wo.nlse = reinterpret_cast<float *>(static_cast<char *>(ws) + kEvHistBytes);
     wo.scores = wo.nlse + lse_bytes(s, T) / sizeof(float);
@@ -3194,8 +3189,7 @@ int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int3
     if (rc != DA_OK) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     void *ws = nullptr;
-    bool captured;
-    rc = prepare_weights(dev, stream, evict_bytes(s, keep), &ws, &captured);
+    rc = prepare_weights(dev, stream, evict_bytes(s, keep), &ws);
     if (rc != DA_OK) return rc;
 
     EvictParams p;
