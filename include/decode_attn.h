@@ -290,8 +290,8 @@ DA_API int decode_attn_multi_reserve(size_t bytes);
 DA_API int decode_attn_multi_launches(da_shape s, int q_tokens, int ring_window, int max_seq_len);
 
 /*
- * decode_attn_paged_weights / decode_attn_paged_fp8_weights -- decode_attn_paged and
- * decode_attn_paged_fp8 that also accumulate how much each cached token is attended, for
+ * decode_attn_paged_weights / decode_attn_paged_fp8_weights / decode_attn_paged_fp8_weights_rule
+ * -- decode_attn_paged and decode_attn_paged_fp8 that also accumulate how much each cached token is attended, for
  * kv_evict. (The pages describe nothing like it; a bounded cache is this library's choice.)
  *   weights  [num_pages, Hkv, page_size] fp32, laid out as the cache's cells. With P the
  *            step's probabilities (sink in the denominator),
@@ -304,11 +304,17 @@ DA_API int decode_attn_multi_launches(da_shape s, int q_tokens, int ring_window,
  * correctly, in no fixed order. Cells of a page outside the pool are skipped
  * (DA_STATUS_BAD_PAGE). Cells appended by other calls hold whatever they held before: set a
  * page's weights to zero when it is handed out.
- * fp8 cache: the new token's scale is max_d |x_d| * (1 / 448), the fp32 reciprocal of 448, and
- * code_d the e4m3 value nearest to x_d / scale: the bytes of x.abs().amax(-1) / 448 and a cast
- * to float8_e4m3fn in torch on a GPU, which divides by a constant that way, so that a token
- * appended here and one quantised by torch code (a prompt's, say) are held alike. The scale is
- * at most one unit in the last place from decode_attn_paged_fp8's, which divides.
+ * fp8 cache: code_d of the new token is the e4m3 value nearest to x_d / scale, and its scale
+ *   DA_FP8_SCALE_RECIPROCAL  max_d |x_d| * (1 / 448), the fp32 reciprocal of 448: the bytes of
+ *       x.abs().amax(-1) / 448 and a cast to float8_e4m3fn in torch on a GPU, which divides by
+ *       a constant that way: for caches that torch code quantises too (a prompt's tokens, say).
+ *       What decode_attn_paged_fp8_weights does.
+ *   DA_FP8_SCALE_DIVIDE      max_d |x_d| / 448, as decode_attn_paged_fp8 and its _rope form
+ *       append: output and cache are those of decode_attn_paged_fp8, bit for bit. For caches
+ *       that those calls append to as well (an engine that accumulates weights on some of its
+ *       steps or layers).
+ *   decode_attn_paged_fp8_weights_rule takes the rule; any other value: DA_ERR_INVALID_ARG. The
+ *   two scales differ by at most one unit in the last place; codes next to a tie may then differ.
  * scale must be positive and finite. Two launches. Workspace: the one-token workspace, and the
  * weights workspace (decode_attn_weights_workspace_bytes: 4 bytes per query head and position
  * of max_seq_len, or of the window, so give the true max_seq_len); both grow on first use
@@ -327,6 +333,15 @@ DA_API int decode_attn_paged_fp8_weights(const void *q, const void *k_new, const
                                          float scale, void *out, da_shape s, int page_size,
                                          int max_pages_per_seq, int num_pages, int max_seq_len,
                                          void *stream);
+#define DA_FP8_SCALE_RECIPROCAL 0
+#define DA_FP8_SCALE_DIVIDE 1
+DA_API int decode_attn_paged_fp8_weights_rule(const void *q, const void *k_new, const void *v_new,
+                                              void *kv_cache, float *weights,
+                                              const int32_t *block_table, const int32_t *seq_lens,
+                                              const float *sinks, int window, float scale,
+                                              int scale_rule, void *out, da_shape s, int page_size,
+                                              int max_pages_per_seq, int num_pages, int max_seq_len,
+                                              void *stream);
 
 /*
  * decode_attn_paged_multi_weights -- decode_attn_paged_multi that also accumulates the weights,

@@ -29,6 +29,7 @@ __all__ = [
     "decode_attn_workspace_bytes", "decode_attn_reserve", "decode_attn_device_status",
     "decode_attn_error_string", "library_path", "load_library",
     "DA_STATUS_BAD_SEQ_LEN", "DA_STATUS_BAD_PAGE", "DA_STATUS_TIMEOUT", "DA_STATUS_BAD_POSITION",
+    "DA_FP8_SCALE_RECIPROCAL", "DA_FP8_SCALE_DIVIDE",
     "decode_attn_paged_rope", "decode_attn_ring_rope", "decode_attn_paged_fp8", "decode_attn_ring_fp8",
     "decode_attn_paged_multi", "decode_attn_ring_multi", "decode_attn_multi_workspace_bytes",
     "decode_attn_multi_reserve", "decode_attn_multi_launches", "decode_attn_test_expire_wait",
@@ -52,6 +53,8 @@ DA_STATUS_BAD_SEQ_LEN = 1
 DA_STATUS_BAD_PAGE = 2
 DA_STATUS_TIMEOUT = 4
 DA_STATUS_BAD_POSITION = 8
+DA_FP8_SCALE_RECIPROCAL = 0  # scale of a row appended to fp8 blocks: amax * (1 / 448), or
+DA_FP8_SCALE_DIVIDE = 1      # amax / 448 (fp32)
 
 
 class da_shape(ctypes.Structure):
@@ -132,6 +135,8 @@ def load_library():
                                               da_shape, c_int, c_int, c_int, c_int, vp]
     lib.decode_attn_paged_fp8_weights.argtypes = [vp, vp, vp, vp, f32p, i32p, i32p, f32p, c_int, c_float, vp,
                                                   da_shape, c_int, c_int, c_int, c_int, vp]
+    lib.decode_attn_paged_fp8_weights_rule.argtypes = [vp, vp, vp, vp, f32p, i32p, i32p, f32p, c_int, c_float, c_int,
+                                                       vp, da_shape, c_int, c_int, c_int, c_int, vp]
     lib.decode_attn_paged_multi_weights.argtypes = [vp, vp, vp, vp, vp, f32p, i32p, i32p, i32p, f32p, c_int,
                                                     c_float, vp, da_shape, c_int, c_int, c_int, c_int, c_int, vp]
     lib.kv_evict.argtypes = [vp, vp, f32p, i32p, i32p, i32p, i32p, c_int, c_int, c_int, da_shape, c_int, c_int,
@@ -144,7 +149,7 @@ def load_library():
     lib.kv_evict_workspace_bytes.restype = ctypes.c_size_t
     lib.decode_attn_weights_reserve.argtypes = [vp, ctypes.c_size_t]
     for fn in (lib.decode_attn_paged_weights, lib.decode_attn_paged_fp8_weights,
-               lib.decode_attn_paged_multi_weights, lib.kv_evict, lib.kv_evict_fp8,
+               lib.decode_attn_paged_fp8_weights_rule, lib.decode_attn_paged_multi_weights, lib.kv_evict, lib.kv_evict_fp8,
                lib.decode_attn_weights_reserve, lib.decode_attn_paged, lib.decode_attn_ring, lib.kv_append, lib.decode_attn_reserve,
                lib.decode_attn_device_status, lib.decode_attn_paged_rope, lib.decode_attn_ring_rope,
                lib.decode_attn_paged_fp8, lib.decode_attn_ring_fp8, lib.decode_attn_paged_multi,
@@ -514,14 +519,16 @@ def decode_attn_paged_weights(q, k_new, v_new, k_cache, v_cache, weights, block_
 
 
 def decode_attn_paged_fp8_weights(q, k_new, v_new, kv_cache, weights, block_table, seq_lens, sinks, window,
-                                  scale, out, max_seq_len=None, stream=None):
-    """decode_attn_paged_weights over an fp8 cache (kv_cache as in decode_attn_paged_fp8)."""
+                                  scale, out, max_seq_len=None, stream=None, scale_rule=DA_FP8_SCALE_RECIPROCAL):
+    """decode_attn_paged_weights over an fp8 cache (kv_cache as in decode_attn_paged_fp8). scale_rule: how the
+    appended token is scaled, DA_FP8_SCALE_RECIPROCAL as torch code on a GPU does it, DA_FP8_SCALE_DIVIDE as
+    decode_attn_paged_fp8 does it (for a cache that both calls append to)."""
     dev = torch.cuda.current_device()
     kp, _, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(kv_cache, None, weights, block_table, seq_lens, dev)
     qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B,), Hkv, dev)
-    _check(load_library().decode_attn_paged_fp8_weights(
-        qp, knp, vnp, kp, wp, bp, lp, sp, int(window), float(scale), op, da_shape(B, Hq, Hkv, 64), 16, max_pages, num_pages,
-        max_pages * 16 if max_seq_len is None else int(max_seq_len), _raw_stream(stream, dev)))
+    _check(load_library().decode_attn_paged_fp8_weights_rule(
+        qp, knp, vnp, kp, wp, bp, lp, sp, int(window), float(scale), int(scale_rule), op, da_shape(B, Hq, Hkv, 64), 16,
+        max_pages, num_pages, max_pages * 16 if max_seq_len is None else int(max_seq_len), _raw_stream(stream, dev)))
     return out
 
 

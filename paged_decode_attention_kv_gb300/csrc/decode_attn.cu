@@ -222,6 +222,7 @@ struct Params {
     float *nlse;
     int lse_ld;
     float *scores;
+    int fp8_rule;  // how a token appended to fp8 blocks is scaled (DA_FP8_SCALE_*)
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -1773,7 +1774,8 @@ __global__ void __launch_bounds__(kThreads, CPS)
                             ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, off));
                             va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, off));
                         }
-                        if constexpr (WTS) {  // the reciprocal rule of these calls
+                        // (without weights: always the division, and no branch)
+                        if (WTS && p.fp8_rule == DA_FP8_SCALE_RECIPROCAL) {
                             knew_scale = ka > 0.f ? __fmul_rn(ka, 1.f / 448.f) : 1.f;
                             vnew_scale = va > 0.f ? __fmul_rn(va, 1.f / 448.f) : 1.f;
                         } else {
@@ -2434,6 +2436,7 @@ struct WeightsOut {
     float *nlse;
     int lse_ld;
     float *scores;
+    int fp8_rule;
 };
 
 int run_attention(bool ring, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
@@ -2500,6 +2503,7 @@ int run_attention(bool ring, const void *q, const void *k_new, const void *v_new
     prm.nlse = wts ? wts->nlse : nullptr;
     prm.lse_ld = wts ? wts->lse_ld : 0;
     prm.scores = wts ? wts->scores : nullptr;
+    prm.fp8_rule = wts ? wts->fp8_rule : DA_FP8_SCALE_DIVIDE;
     rc = prepare_workspace(dev, G, stream, &prm.part, &prm.counters);
     if (rc != DA_OK) return rc;
 
@@ -2808,6 +2812,7 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         dp.nlse = wts ? wts->nlse : nullptr;
         dp.lse_ld = wts ? wts->lse_ld : 0;
         dp.scores = nullptr;
+        dp.fp8_rule = DA_FP8_SCALE_DIVIDE;
         CUtensorMap mk, mv;
         const uint64_t slices = static_cast<uint64_t>(num_pages) * s.num_kv_heads;
         if (!make_kv_map(&mk, k_cache, kPage, slices) || !make_kv_map(&mv, v_cache, kPage, slices)) {
@@ -3043,10 +3048,11 @@ int launch_stream_rows(int idx, const CUtensorMap &mk, const CUtensorMap &mq, co
 int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                 float *weights, const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
                 const float *sinks, int window, float scale, void *out, const da_shape &s, int T, int page_size,
-                int max_pages, int num_pages, int max_seq_len, void *stream_v) {
+                int max_pages, int num_pages, int max_seq_len, void *stream_v, int fp8_rule = DA_FP8_SCALE_DIVIDE) {
     int rc = check_shape(s);
     if (rc != DA_OK) return rc;
     if (!weights || !aligned16(weights) || !(scale > 0.f) || !(scale < INFINITY)) return DA_ERR_INVALID_ARG;
+    if (fp8_rule != DA_FP8_SCALE_RECIPROCAL && fp8_rule != DA_FP8_SCALE_DIVIDE) return DA_ERR_INVALID_ARG;
     if (T > kMMaxTokens) return DA_ERR_UNSUPPORTED;
     // Everything else is checked by the attention call itself, which comes first: with no
     // workspace yet it is asked for an empty batch, which launches nothing.
@@ -3065,7 +3071,7 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     if (rc != DA_OK) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     void *ws = nullptr;
-    WeightsOut wo{nullptr, lse_rows(s, T), nullptr};
+    WeightsOut wo{nullptr, lse_rows(s, T), nullptr, fp8_rule};
     rc = prepare_weights(dev, stream, weights_bytes(s, T, max_seq_len, window), &ws);
     if (rc != DA_OK) return rc;
     wo.nlse = reinterpret_cast<float *>(static_cast<char *>(ws) + kEvHistBytes);
@@ -3350,6 +3356,7 @@ int run_paged_noalloc(const void *q, const void *k_new, const void *v_new, void 
     prm.nlse = nullptr;
     prm.lse_ld = 0;
     prm.scores = nullptr;
+    prm.fp8_rule = DA_FP8_SCALE_DIVIDE;
     prm.counters = static_cast<int *>(scratch);
     prm.part = reinterpret_cast<float *>(static_cast<char *>(scratch) + kNoAllocCounterBytes);
     // The array keeps whatever the previous call left: the arrival counters this call
@@ -3457,8 +3464,18 @@ int decode_attn_paged_fp8_weights(const void *q, const void *k_new, const void *
                                   const int32_t *block_table, const int32_t *seq_lens, const float *sinks, int window,
                                   float scale, void *out, da_shape s, int page_size, int max_pages_per_seq,
                                   int num_pages, int max_seq_len, void *stream) {
+    return decode_attn_paged_fp8_weights_rule(q, k_new, v_new, kv_cache, weights, block_table, seq_lens, sinks, window,
+                                              scale, DA_FP8_SCALE_RECIPROCAL, out, s, page_size, max_pages_per_seq,
+                                              num_pages, max_seq_len, stream);
+}
+
+int decode_attn_paged_fp8_weights_rule(const void *q, const void *k_new, const void *v_new, void *kv_cache,
+                                       float *weights, const int32_t *block_table, const int32_t *seq_lens,
+                                       const float *sinks, int window, float scale, int scale_rule, void *out,
+                                       da_shape s, int page_size, int max_pages_per_seq, int num_pages,
+                                       int max_seq_len, void *stream) {
     return run_weights(true, q, k_new, v_new, kv_cache, nullptr, weights, block_table, seq_lens, nullptr, sinks, window,
-                       scale, out, s, 0, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+                       scale, out, s, 0, page_size, max_pages_per_seq, num_pages, max_seq_len, stream, scale_rule);
 }
 
 int decode_attn_paged_multi_weights(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
