@@ -3037,10 +3037,8 @@ int launch_stream_keys(int idx, const CUtensorMap &mk, const CUtensorMap &mq, co
 template <int TILES>
 int launch_stream_rows(int idx, const CUtensorMap &mk, const CUtensorMap &mq, const WeightParams &p, long long blocks,
                        int dev, cudaStream_t stream) {
-    const long long ctas = blocks * p.Hkv * p.B;
-    if (ctas > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
     return launch_row_weights(stream_rows_weights_kernel<TILES>, idx, SrLayout<TILES>::kThreads, SrLayout<TILES>::bytes, mk,
-                              mq, p, dim3(static_cast<unsigned>(ctas)), dev, stream);
+                              mq, p, dim3(static_cast<unsigned>(blocks * p.Hkv * p.B)), dev, stream);
 }
 
 // One step of attention (T = 0: one token per sequence; else T, with q_lens) over a paged cache
@@ -3054,8 +3052,9 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     if (!weights || !aligned16(weights) || !(scale > 0.f) || !(scale < INFINITY)) return DA_ERR_INVALID_ARG;
     if (fp8_rule != DA_FP8_SCALE_RECIPROCAL && fp8_rule != DA_FP8_SCALE_DIVIDE) return DA_ERR_INVALID_ARG;
     if (T > kMMaxTokens) return DA_ERR_UNSUPPORTED;
-    // Everything else is checked by the attention call itself, which comes first: with no
-    // workspace yet it is asked for an empty batch, which launches nothing.
+    // Everything that can refuse the call comes before its first launch. Most of it is checked by the
+    // attention call itself: with no workspace yet it is asked for an empty batch, which launches
+    // nothing.
     auto attention = [&](const da_shape &sh, const WeightsOut *w) {
         return T > 0 ? run_multi(false, q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, q_lens, sinks, window,
                                  scale, out, sh, T, page_size, max_pages, num_pages, max_seq_len, stream_v, nullptr,
@@ -3066,6 +3065,12 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     };
     rc = attention(da_shape{0, s.num_q_heads, s.num_kv_heads, s.head_dim}, nullptr);
     if (rc != DA_OK || s.batch == 0) return rc;
+    const int G = s.num_q_heads / s.num_kv_heads, rows = T * G;
+    const int win = window < max_seq_len ? window : 0;  // (a window no sequence fills is none: sums with it stay in 32 bits)
+    // several tokens: the 128-key stages of the longest range that any sequence's rows can see
+    const long long span = win > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(win) + T + kMwKeys) : max_seq_len;
+    const long long stages = (span + kMwKeys - 1) / kMwKeys, pairs = static_cast<long long>(s.batch) * s.num_kv_heads;
+    if (rows > kMwMaxRows && (stages + 1) / 2 * pairs > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;  // one CTA per 256 keys
     int dev = 0;
     rc = current_device(&dev);
     if (rc != DA_OK) return rc;
@@ -3076,10 +3081,17 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     if (rc != DA_OK) return rc;
     wo.nlse = reinterpret_cast<float *>(static_cast<char *>(ws) + kEvHistBytes);
     wo.scores = wo.nlse + lse_bytes(s, T) / sizeof(float);
+    const int N = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : kMwMaxRows;  // (rows that stay)
+    CUtensorMap mk, mq;
+    if (T > 0 &&
+        (!make_kv_map(&mk, k_cache, kPage, static_cast<uint64_t>(num_pages) * s.num_kv_heads) ||
+         !make_q_map(&mq, q, s.num_q_heads, G, rows <= kMwMaxRows ? N : kMwRowBlock, static_cast<uint64_t>(s.batch) * T))) {
+        snprintf(t_err, sizeof t_err, "CUDA error: tensor map encoding failed");
+        return DA_ERR_CUDA;
+    }
     rc = attention(s, &wo);
     if (rc != DA_OK || max_seq_len == 0) return rc;
 
-    const int G = s.num_q_heads / s.num_kv_heads;
     WeightParams p;
     p.weights = weights;
     p.block_table = block_table;
@@ -3093,7 +3105,7 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
     p.Hkv = s.num_kv_heads;
     p.G = G;
     p.T = T;
-    p.window = window < max_seq_len ? window : 0;  // (a window no sequence fills is none: sums with it stay in 32 bits)
+    p.window = win;
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.max_seq_len = max_seq_len;
@@ -3105,18 +3117,6 @@ int run_weights(bool kv8, const void *q, const void *k_new, const void *v_new, v
                : G == 4 ? launch_score_weights<4>(p, dev, stream)
                : G == 8 ? launch_score_weights<8>(p, dev, stream)
                         : launch_score_weights<16>(p, dev, stream);
-    // the 128-key stages of the longest range that any sequence's rows can see
-    const int rows = T * G;
-    const long long span = p.window > 0 ? std::min<long long>(max_seq_len, static_cast<long long>(p.window) + T + kMwKeys) : max_seq_len;
-    const long long stages = (span + kMwKeys - 1) / kMwKeys;
-    const long long pairs = static_cast<long long>(s.batch) * s.num_kv_heads;
-    const int N = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : kMwMaxRows;  // (rows that stay)
-    CUtensorMap mk, mq;
-    if (!make_kv_map(&mk, k_cache, kPage, static_cast<uint64_t>(num_pages) * s.num_kv_heads) ||
-        !make_q_map(&mq, q, s.num_q_heads, G, rows <= kMwMaxRows ? N : kMwRowBlock, static_cast<uint64_t>(s.batch) * T)) {
-        snprintf(t_err, sizeof t_err, "CUDA error: tensor map encoding failed");
-        return DA_ERR_CUDA;
-    }
     if (rows > kMwMaxRows) {
         // 256 keys per CTA where that still gives every SM one (512 tokens behind 7680: 278 us against
         // 284 with 128 keys and two CTAs per SM; four prompts of up to 2048: 360 against 363)

@@ -1,0 +1,23 @@
+"""CPU: what the calls with weights cannot do they refuse before anything is launched (a refusal after
+the attention would leave the new tokens appended and their weights unwritten)."""
+import pytest
+
+import paged_decode_attention_kv_gb300 as da
+from test_abi import _shape
+from test_weights_plain import call
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from paged_decode_attention_kv_gb300 import build
+    build.build()
+    return da.load_library()
+
+
+def test_more_key_blocks_than_a_grid_holds(lib):
+    """512 query rows, 512 (sequence, KV head) pairs, 2^31 - 1 positions: 2^32 blocks of 256 keys. Refused
+    as a shape, ahead of the first CUDA call (which fails here, without a device)."""
+    wide = dict(s=_shape(B=64, Hq=64, Hkv=8), T=64, maxp=2 ** 27, maxlen=2 ** 31 - 1)
+    assert call(lib, "multi", **wide) == -2
+    assert call(lib, "multi", window=2 ** 30, **wide) == -2
+    # a window that leaves fewer is not refused for it
