@@ -490,7 +490,7 @@ def _paged_tensors(k, v, weights, block_table, seq_lens, dev):
 def _new_tensors(q, k_new, v_new, sinks, out, lead, Hkv, dev):
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new are given together")
-    Hq = q.shape[-2]
+    Hq = q.shape[-2] if q.dim() > 1 else 0
     rows, new = lead + (Hq, 64), lead + (Hkv, 64)
     return (_tensor("q", q, torch.bfloat16, rows, dev),
             None if k_new is None else _tensor("k_new", k_new, torch.bfloat16, new, dev),
