@@ -189,13 +189,12 @@ __device__ __noinline__ void multi_combine_rows(const MultiParams &p, const floa
             // the sink joins the denominator; no key and no sink: a zero row
             Mf[i] = fmaxf(M[i], sg[i]);
             inv[i] = 0.f;
-            float d = 0.f;
             if (Mf[i] != -INFINITY) {
-                d = den[i] * exp2f(M[i] - Mf[i]) + (sg[i] == -INFINITY ? 0.f : exp2f(sg[i] - Mf[i]));
+                const float d = den[i] * exp2f(M[i] - Mf[i]) + (sg[i] == -INFINITY ? 0.f : exp2f(sg[i] - Mf[i]));
                 inv[i] = d > 0.f ? 1.f / d : 0.f;
+                if (p.nlse != nullptr && lane == 0)
+                    p.nlse[(static_cast<size_t>(b) * p.Hkv + g) * p.lse_ld + r0 + rl[i]] = neg_log2_den(Mf[i], d);
             }
-            if (p.nlse != nullptr && lane == 0 && live[i])  // (rows past the block's are not the call's to write)
-                p.nlse[(static_cast<size_t>(b) * p.Hkv + g) * p.lse_ld + r0 + rl[i]] = neg_log2_den(Mf[i], d);
         }
         float o[kCombRows][8];
 #pragma unroll
@@ -307,6 +306,10 @@ __global__ void __launch_bounds__(NW * 32, MultiShape<NW>::kMinBlocks)
         return;
     }
     const int cnt = ke - kb;
+    // rows that end without a denominator: those of finite scores are written over when they are finished,
+    // behind a barrier or another CTA's arrival (a branch there made a 512-token chunk 2.6 us longer)
+    if (p.nlse != nullptr && split == 0)
+        for (int i = tid; i < r_end - r0; i += blockDim.x) p.nlse[bg * p.lse_ld + r0 + i] = -INFINITY;
     if (!RING) {  // the pages of the CTA's cached tiles, read once
         for (int i2 = tid; i2 < cnt && kb + i2 < ncache; i2 += blockDim.x) {
             int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + pt_lo + kb + i2);
@@ -522,12 +525,12 @@ __global__ void __launch_bounds__(NW * 32, MultiShape<NW>::kMinBlocks)
     // ---- finish: one split writes the rows, several leave partials for the last to combine
     auto finish_row = [&](float m, float l, float sg, float &f, int r) {  // f: factor on acc; false: zero row
         const float M = fmaxf(m, sg);
-        float den = 0.f;
-        f = 0.f;
-        if (M != -INFINITY) {
-            den = l * exp2f(m - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
-            f = den > 0.f ? exp2f(m - M) / den : 0.f;
+        if (M == -INFINITY) {
+            f = 0.f;
+            return;
         }
+        const float den = l * exp2f(m - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
+        f = den > 0.f ? exp2f(m - M) / den : 0.f;
         if (p.nlse != nullptr && lane < 4) p.nlse[bg * p.lse_ld + r] = neg_log2_den(M, den);
     };
     if (nsplit == 1) {
@@ -630,12 +633,12 @@ __global__ void __launch_bounds__(kCombWarps * 32) multi_combine_kernel(const Mu
     }
     const float sg = p.sinks != nullptr ? __ldg(p.sinks + g * p.G + hl) * kLog2e : -INFINITY;
     const float Mf = fmaxf(M, sg);  // the same on every lane: an exact maximum
-    float inv = 0.f, d = 0.f;
+    float inv = 0.f;
     if (Mf != -INFINITY) {
-        d = den * exp2f(M - Mf) + (sg == -INFINITY ? 0.f : exp2f(sg - Mf));
+        const float d = den * exp2f(M - Mf) + (sg == -INFINITY ? 0.f : exp2f(sg - Mf));
         inv = d > 0.f ? 1.f / d : 0.f;
+        if (p.nlse != nullptr && lane == 0) p.nlse[bg * p.lse_ld + r] = neg_log2_den(Mf, d);
     }
-    if (p.nlse != nullptr && lane == 0) p.nlse[bg * p.lse_ld + r] = neg_log2_den(Mf, d);
     // this lane's splits' weighted accumulators
     float o[kD];
 #pragma unroll

@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int r = r0 + tid;
         uint4 qv[8];
         const bool ok = r < r_valid;
+        // (until the row is finished, see multi_attn_kernel)
+        if (ok && split == 0 && p.nlse != nullptr) p.nlse[bg * p.lse_ld + r] = -INFINITY;
         const uint4 *src = ok ? reinterpret_cast<const uint4 *>(p.q + row_off(r)) : nullptr;
 #pragma unroll
         for (int c = 0; c < 8; ++c) qv[c] = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
@@ -532,12 +534,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     const int h = g * p.G + (r - t * p.G);
                     const float sg = p.sinks != nullptr ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
                     const float M = fmaxf(m_ref, sg);
-                    float den = 0.f;
                     if (M != -INFINITY) {
-                        den = l * exp2f(m_ref - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
+                        const float den = l * exp2f(m_ref - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
                         f = den > 0.f ? exp2f(m_ref - M) / den : 0.f;
+                        if (p.nlse != nullptr) p.nlse[bg * p.lse_ld + r] = neg_log2_den(M, den);
                     }
-                    if (p.nlse != nullptr) p.nlse[bg * p.lse_ld + r] = neg_log2_den(M, den);
                 }
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out + row_off(r));
 #pragma unroll
