@@ -90,3 +90,68 @@ def test_graph_outlives_its_workspace(T, ring, rope, lens, later, grow):
         del g, junk
     finally:
         da.decode_attn_stream_release(s)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("level", [0, 1, 2])
+def test_graphs_that_share_the_workspaces(fp8, level):
+    """A step with weights, a chunk with weights (bf16), an eviction by clusters and a step on the evicted
+    cache, a graph each, captured on one stream and so on the same workspaces: replayed in turn, twice,
+    they leave what the eager calls leave, bit for bit."""
+    gen = wl.cpu_generator(5000 + level)
+    B, Hq, Hkv, T, keep, pages = 2, 64, 8, 12, 500, 1300
+    lens = torch.tensor([9000, 8500], dtype=torch.int32)
+    table = torch.randperm(pages, generator=gen)[:2 * 600].to(torch.int32).view(2, 600)
+    bt, l1, l2 = dev(table), dev(lens), dev(lens + T)
+    q, kn, vn = (dev(wl.randn_bf16((B, h, 64), gen)) for h in (Hq, Hkv, Hkv))
+    qt, knt, vnt = (dev(wl.randn_bf16((B, T, h, 64), gen)) for h in (Hq, Hkv, Hkv))
+    if fp8:
+        kv = torch.randint(0, 256, (pages, Hkv, 2176), generator=gen, dtype=torch.uint8)
+        kv[..., :2048][(kv[..., :2048] & 127) == 127] = 0
+        kv[..., 2048:] = torch.full((pages, Hkv, 32), 0.005).view(torch.uint8)
+        first = [dev(kv)]
+    else:
+        first = [dev(wl.randn_bf16((pages, Hkv, 16, 64), gen)) for _ in range(2)]
+    first.append(torch.rand((pages, Hkv, 16), device="cuda"))
+
+    def state():
+        return [x.clone() for x in first] + [torch.zeros_like(l1), torch.zeros((B, Hkv, keep), dtype=torch.int32, device="cuda"),
+                                             torch.zeros_like(q), torch.zeros_like(qt), torch.zeros_like(q)]
+
+    def calls(s):
+        *pools, w, nl, kept, o1, ot, o2 = s
+        f = "_fp8" if fp8 else ""
+        yield lambda: getattr(da, f"decode_attn_paged{f}_weights")(q, kn, vn, *pools, w, bt, l1, None, 0, 0.125, o1)
+        if not fp8:
+            yield lambda: da.decode_attn_paged_multi_weights(qt, knt, vnt, *pools, w, bt, l2, None, 0, 0.125, ot)
+        yield lambda: getattr(da, "kv_evict" + f)(*pools, w, bt, l1 if fp8 else l2, nl, kept, 4, 64)
+        yield lambda: getattr(da, "decode_attn_paged" + f)(q, None, None, *pools, bt, nl, None, 0, 0.125, o2)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    da.decode_attn_stream_reserve(s)
+    prev = da.decode_attn_set_early_inputs(level)
+    try:
+        with torch.cuda.stream(s):
+            eager, replayed, graphs = state(), state(), []
+            for _ in range(2):
+                for f in calls(eager):
+                    f()
+            s.synchronize()
+            for f in calls(replayed):
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=s):
+                    f()
+                graphs.append(g)
+            for _ in range(2):
+                for g in graphs:
+                    g.replay()
+            s.synchronize()
+        assert da.decode_attn_device_status(s) == 0
+        for i, (a, b) in enumerate(zip(eager, replayed)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+        assert replayed[-5].tolist() == [keep, keep]
+        del graphs
+    finally:
+        da.decode_attn_set_early_inputs(prev)
+        da.decode_attn_stream_release(s)
