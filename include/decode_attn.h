@@ -382,6 +382,8 @@ DA_API int decode_attn_paged_multi_weights(const void *q, const void *k_new, con
  *             cell i; a sequence of L <= keep cells has kept[b][g][i] = i for i < L, then -1
  *   keep >= 1; keep_first, keep_last >= 0; keep_first + keep_last <= keep
  *   s         batch, num_q_heads = num_kv_heads = Hkv, head_dim
+ *   max_seq_len  the work is cut for sequences of this length, so give the true one: 64 sequences
+ *             of up to 8192 cells take half as long again under a bound of 131072
  * Evicted sequences must not share pages with each other or with sequences that still need
  * them. A page outside the pool sets DA_STATUS_BAD_PAGE and the moves into or out of it are
  * skipped; a bad length sets DA_STATUS_BAD_SEQ_LEN and the slot is treated as inactive. One

@@ -507,7 +507,9 @@ def decode_attn_paged_weights(q, k_new, v_new, k_cache, v_cache, weights, block_
                               window, scale, out, max_seq_len=None, stream=None):
     """decode_attn_paged that also adds every attended token's attention weight (its probabilities
     summed over the query heads of its KV head) to its cell of weights, fp32
-    [num_pages, Hkv, 16]; the appended token's cell is set to its weight."""
+    [num_pages, Hkv, 16]; the appended token's cell is set to its weight. The weights workspace
+    holds 4 bytes per query head and position up to max_seq_len (default: what the block table
+    can hold), so give the longest sequence's length where the table is much wider."""
     dev = torch.cuda.current_device()
     kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(k_cache, v_cache, weights, block_table, seq_lens,
                                                                        dev)
@@ -556,7 +558,9 @@ def kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_lens, kept, k
     """Shrink every sequence longer than keep = kept.shape[2] cells to keep cells per KV head, in
     place: the first keep_first and the last keep_last cells stay, and of those between them the
     ones of the largest accumulated weight. new_lens [B] int32 receives the lengths, kept
-    [B, Hkv, keep] int32 the old cell of each kept cell (-1 beyond a shorter sequence's end)."""
+    [B, Hkv, keep] int32 the old cell of each kept cell (-1 beyond a shorter sequence's end). The
+    work is cut for sequences of max_seq_len (default: what the block table can hold): give the
+    longest length where the table is much wider."""
     dev = torch.cuda.current_device()
     kp, vp, wp, bp, lp, B, Hkv, max_pages, num_pages = _paged_tensors(k_cache, v_cache, weights, block_table, seq_lens,
                                                                        dev)

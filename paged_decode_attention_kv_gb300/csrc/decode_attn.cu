@@ -28,7 +28,11 @@
 //     (mma.sync m16n8k16 bf16 -> fp32): keys are the M dimension and the G <= 8
 //     query heads of the group the N dimension, so nothing is padded; the
 //     probabilities are moved from the accumulator layout into the B-operand
-//     layout with movmatrix.
+//     layout with movmatrix. They are rounded to bf16 there (fp16 over fp8
+//     blocks), the only operand types of that product; their sum, the softmax's
+//     denominator, is kept in fp32 from the values before the rounding. An output
+//     is off by 2^-9 of its terms at most, beside its own rounding to bf16
+//     (against 64 bits 0.0022 of its norm, 0.0017 for the rounding alone).
 //   * K/V tiles (2 KiB each) arrive by TMA with 128-byte swizzle, so the
 //     ldmatrix reads are free of bank conflicts.
 #include <cuda.h>  // CUtensorMap and its enums (types only; resolved at run time)
@@ -3228,9 +3232,14 @@ int run_evict(bool kv8, void *k_cache, void *v_cache, float *weights, const int3
         of16 = evict_clusters_of_16(kern);
         g_dev[dev].evict_clusters[kv8].store(of16, std::memory_order_release);
     }
-    // (clusters of 16 only if all are resident at once: a second wave takes as long as the first; none
-    // below 8192 cells, where their barriers cost more than their warps save: 8 sequences of 4160
-    // cells 19 us with one CTA, 21 with two; one of 16384 27 us with four, 23 with eight)
+    // (Clusters of 16 only if all are resident at once: a second wave takes as long as the first. None
+    // below 8192 cells, where their barriers cost more than their warps save. One sequence of 8 KV
+    // heads cut by 64 cells, with one, two, four and eight CTAs: 6000 cells 17.2, 18.7, 17.9 us;
+    // 8191 18.1, 19.5, 17.4; 12000 19.9, 20.0, 18.0, 17.6; 32768 30.2, 24.2, 20.4, 18.6; cut to an
+    // eighth the same order. 64 pairs have clusters of two at most: 9000 cells 19.1 us with one,
+    // 20.9 with two, 16384 23.0 and 22.6, 32768 32.1 and 26.7. The host knows max_seq_len only: a
+    // table much wider than its sequences gets the clusters and the shared memory of its width, so
+    // that 64 sequences of up to 8192 cells take 129 us behind a table of 131072, 88 otherwise.)
     const int most = max_seq_len < 8192 ? 1 : pairs <= of16 ? kEvMaxCluster : 8;
     int C = 1;
     while (C < most && 2 * C * pairs <= sms && pairs <= kEvClusterPairs && 2 * C * warps * 32 <= max_seq_len) C *= 2;

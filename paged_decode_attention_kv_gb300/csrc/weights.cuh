@@ -128,7 +128,9 @@ __global__ void __launch_bounds__(kSwThreads, kSwCtasPerSm) score_weights_kernel
             }
         }
         // The scores are read once: their lines leave L2 without being written to memory (whole lines
-        // of this warp's own tiles; at G = 1 two tiles share one).
+        // of this warp's own tiles; at G = 1 two tiles share one, and a tile's scores are 64 bytes
+        // beside 4096 of keys and values: 64 sequences of 1000 to 8192 tokens 104.6 us without the
+        // weights, 117.4 with them, 104.8 and 116.7 at G = 2, where the lines are dropped).
         __syncwarp();
         if constexpr (G >= 2)
             for (int i = lane; i < cnt * (G / 2); i += 32)
