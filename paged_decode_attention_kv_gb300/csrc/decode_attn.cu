@@ -2160,6 +2160,7 @@ __global__ void kv_append_kernel(const __nv_bfloat16 *__restrict__ k_new,
 thread_local char t_err[256];
 
 int set_cuda_error(cudaError_t e) {
+    cudaGetLastError();  // reported here: the next call's launch check must not find it again
     snprintf(t_err, sizeof t_err, "CUDA error: %s", cudaGetErrorString(e));
     return DA_ERR_CUDA;
 }
