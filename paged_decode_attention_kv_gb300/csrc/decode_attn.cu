@@ -30,9 +30,10 @@
 //     probabilities are moved from the accumulator layout into the B-operand
 //     layout with movmatrix. They are rounded to bf16 there (fp16 over fp8
 //     blocks), the only operand types of that product; their sum, the softmax's
-//     denominator, is kept in fp32 from the values before the rounding. An output
-//     is off by 2^-9 of its terms at most, beside its own rounding to bf16
-//     (against 64 bits 0.0022 of its norm, 0.0017 for the rounding alone).
+//     denominator, is kept in fp32 from the values before the rounding. Each term
+//     of an output is off by half a step of bf16, 2^-8 of it at most, beside the
+//     output's own rounding (against 64 bits 0.0022 of the norm, 0.0017 for the
+//     output's rounding alone).
 //   * K/V tiles (2 KiB each) arrive by TMA with 128-byte swizzle, so the
 //     ldmatrix reads are free of bank conflicts.
 #include <cuda.h>  // CUtensorMap and its enums (types only; resolved at run time)
