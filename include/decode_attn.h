@@ -410,6 +410,97 @@ DA_API size_t kv_evict_workspace_bytes(da_shape s, int keep);
 DA_API int decode_attn_weights_reserve(void *stream, size_t bytes);
 
 /*
+ * qk_norm_rope -- what a step does to the projected rows of its new tokens before the attention,
+ * in one pass: the RMS norm of every query and key head, and the rotary embedding at positions
+ * that the caller gives. (The pages fuse the rotation alone, README, changes table, row "RoPE as one
+ * fused kernel at every batch size"; the norms and the axes are this library's choice.) For
+ * caches whose positions are not L - 1: after kv_evict, and for images and video. For each token
+ * and each query or key head x:
+ *     y = x * w / sqrt(sum_d x_d^2 / 64 + eps)     (w null: y = x)
+ *     pair i < 32:  (y_i c - y_{i+32} s,  y_{i+32} c + y_i s),
+ *                   c = rope_cos[positions[a][token]][i], s likewise, a = pair_axis[i]
+ * in fp32, rounded once to bf16 (nearest even); without a norm the bits are those of the _rope calls.
+ * Value rows are copied as they are (v null: there are none), so that the rows of one packed
+ * projection leave as the contiguous rows that the attention calls take.
+ *   q, k, v     bf16 rows: token i's heads at in + i * in_stride (elements; a multiple of 8, at
+ *               least heads * 64), written to out + i * out_stride; in and out 16-byte aligned, the
+ *               same rows or rows that do not overlap
+ *   positions   [axes][tokens] int32; outside [0, max_position): DA_STATUS_BAD_POSITION, row 0
+ *   axes        1 to 3; pair_axis: 32 bytes of HOST memory, each below axes, read during the call
+ *               (null with one axis)
+ *   rope_cos, rope_sin  [max_position][32] fp32, 16-byte aligned
+ *   q_weight, k_weight  [64] fp32, 16-byte aligned, or null: no norm of those rows
+ * num_q_heads and num_kv_heads up to 1024, any ratio. One launch, no workspace.
+ */
+typedef struct {
+    const void *in;
+    void *out;
+    long long in_stride, out_stride;
+} da_rows;
+DA_API int qk_norm_rope(const da_rows *q, const da_rows *k, const da_rows *v, int tokens, int num_q_heads,
+                        int num_kv_heads, int head_dim, const int32_t *positions, int axes,
+                        const unsigned char *pair_axis, const float *rope_cos, const float *rope_sin,
+                        int max_position, const float *q_weight, const float *k_weight, float eps,
+                        void *stream);
+
+/*
+ * kv_append_fp8 -- new tokens quantised into the blocks of an fp8 cache (decode_attn_paged_fp8 has
+ * the format): a prompt's, a chunk's, a step's.
+ *   k_new, v_new  [B][T][Hkv][64] bf16; of sequence b the first n = q_lens[b] (T when q_lens is
+ *                 null) go to positions L - n .. L - 1, L = seq_lens[b]; rows t >= n are ignored
+ *   block_table   paged: page_size, max_pages_per_seq, num_pages, max_seq_len as in
+ *                 decode_attn_paged (window ignored). NULL: ring kv_cache [B, Hkv, window / 16, 2176],
+ *                 which keeps the last `window` of them; window % 16 == 0
+ *   scale_rule    DA_FP8_SCALE_DIVIDE (the bytes of decode_attn_paged_fp8) or _RECIPROCAL
+ *   s             batch, num_kv_heads and head_dim count
+ * Only the new tokens' bytes are written. q_lens[b] outside 0 .. min(T, L), a length outside
+ * 0 .. max_seq_len: DA_STATUS_BAD_SEQ_LEN, nothing written for that sequence; a page outside the
+ * pool: DA_STATUS_BAD_PAGE, its tokens skipped. One launch, no workspace.
+ */
+DA_API int kv_append_fp8(const void *k_new, const void *v_new, void *kv_cache,
+                         const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                         int window, int scale_rule, da_shape s, int q_tokens, int page_size,
+                         int max_pages_per_seq, int num_pages, int max_seq_len, void *stream);
+
+/*
+ * kv_read_fp8 -- cached positions of an fp8 cache as bf16 rows, for code that wants them so: position
+ * starts[b] + i (starts null: i) of sequence b, as long as it is below seq_lens[b] and i < rows,
+ * to row i of k_out and v_out [B][rows][Hkv][64]: e4m3(code) * scale in fp32, rounded to bf16. The
+ * other rows are left as they were, also those of a page outside the pool (DA_STATUS_BAD_PAGE).
+ * A start outside 0 .. seq_lens[b], or in a ring below seq_lens[b] - window: DA_STATUS_BAD_SEQ_LEN,
+ * nothing read. Blocks, block_table, window and s as in kv_append_fp8. One launch, no workspace.
+ */
+DA_API int kv_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t *seq_lens,
+                       const int32_t *starts, int window, void *k_out, void *v_out, int rows,
+                       da_shape s, int page_size, int max_pages_per_seq, int num_pages,
+                       int max_seq_len, void *stream);
+
+/*
+ * decode_attn_paged_fp8_multi -- decode_attn_paged_multi over an fp8 cache. The n new tokens of a
+ * sequence are quantised into their cells as kv_append_fp8 does it, and every key and value is
+ * attended as it is cached, the new ones too: the output does not depend on how a prompt is cut into
+ * calls. Masks, q_lens, window, sinks and zero rows as in decode_attn_paged_multi; scale_rule as in
+ * kv_append_fp8. scale must be positive and finite. Query rows run in fp16 (|q| < 65504), and so do
+ * the cached values times their page's power of two: a token's factor is rounded against its page's
+ * largest one; V scales outside 2^-60 .. 2^60 lose bits. Cells outside a sequence's
+ * [window start, length) may hold anything; the cached and the new tokens of a sequence must be
+ * finite (a NaN may reach rows of its sequence that do not attend it).
+ * One launch for up to four tokens with T * G <= 32, else two, and one more where a sequence's keys
+ * are cut into many splits. Multi-token workspace
+ * (decode_attn_paged_fp8_multi_workspace_bytes, decode_attn_multi_reserve). The ring form is not
+ * there: a call's early tokens attend cells that its later ones overwrite.
+ */
+DA_API int decode_attn_paged_fp8_multi(const void *q, const void *k_new, const void *v_new,
+                                       void *kv_cache, const int32_t *block_table,
+                                       const int32_t *seq_lens, const int32_t *q_lens,
+                                       const float *sinks, int window, float scale, int scale_rule,
+                                       void *out, da_shape s, int q_tokens, int page_size,
+                                       int max_pages_per_seq, int num_pages, int max_seq_len,
+                                       void *stream);
+DA_API size_t decode_attn_paged_fp8_multi_workspace_bytes(da_shape s, int q_tokens, int window,
+                                                          int max_seq_len);
+
+/*
  * kv_append -- the append alone: bit-copies k_new/v_new [B, Hkv, D] of every
  * active sequence into the cell of position p = seq_lens[b] - 1.
  * block_table != NULL: paged cache (page_size, max_pages_per_seq, num_pages as

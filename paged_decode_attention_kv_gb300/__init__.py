@@ -39,6 +39,8 @@ __all__ = [
     "decode_attn_paged_weights", "decode_attn_paged_fp8_weights", "decode_attn_paged_multi_weights",
     "kv_evict", "kv_evict_fp8", "decode_attn_weights_workspace_bytes", "kv_evict_workspace_bytes",
     "decode_attn_weights_reserve",
+    "qk_norm_rope", "kv_append_fp8", "kv_read_fp8", "decode_attn_paged_fp8_multi",
+    "decode_attn_paged_fp8_multi_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -60,6 +62,11 @@ DA_FP8_SCALE_DIVIDE = 1      # amax / 448 (fp32)
 class da_shape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("num_q_heads", ctypes.c_int),
                 ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class da_rows(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("in_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong)]
 
 
 class DecodeAttnError(RuntimeError):
@@ -148,6 +155,17 @@ def load_library():
     lib.kv_evict_workspace_bytes.argtypes = [da_shape, c_int]
     lib.kv_evict_workspace_bytes.restype = ctypes.c_size_t
     lib.decode_attn_weights_reserve.argtypes = [vp, ctypes.c_size_t]
+    rows_p = ctypes.POINTER(da_rows)
+    lib.qk_norm_rope.argtypes = [rows_p, rows_p, rows_p, c_int, c_int, c_int, c_int, i32p, c_int, ctypes.c_char_p, f32p, f32p,
+                                 c_int, f32p, f32p, c_float, vp]
+    lib.kv_append_fp8.argtypes = [vp, vp, vp, i32p, i32p, i32p, c_int, c_int, da_shape, c_int, c_int, c_int, c_int, c_int, vp]
+    lib.kv_read_fp8.argtypes = [vp, i32p, i32p, i32p, c_int, vp, vp, c_int, da_shape, c_int, c_int, c_int, c_int, vp]
+    lib.decode_attn_paged_fp8_multi.argtypes = [vp, vp, vp, vp, i32p, i32p, i32p, f32p, c_int, c_float, c_int, vp,
+                                                da_shape, c_int, c_int, c_int, c_int, c_int, vp]
+    lib.decode_attn_paged_fp8_multi_workspace_bytes.argtypes = [da_shape, c_int, c_int, c_int]
+    lib.decode_attn_paged_fp8_multi_workspace_bytes.restype = ctypes.c_size_t
+    for fn in (lib.qk_norm_rope, lib.kv_append_fp8, lib.kv_read_fp8, lib.decode_attn_paged_fp8_multi):
+        fn.restype = c_int
     for fn in (lib.decode_attn_paged_weights, lib.decode_attn_paged_fp8_weights,
                lib.decode_attn_paged_fp8_weights_rule, lib.decode_attn_paged_multi_weights, lib.kv_evict, lib.kv_evict_fp8,
                lib.decode_attn_weights_reserve, lib.decode_attn_paged, lib.decode_attn_ring, lib.kv_append, lib.decode_attn_reserve,
@@ -599,3 +617,158 @@ def decode_attn_weights_reserve(nbytes: int, stream=None):
     """Grow the weights workspace that calls on `stream` use (the stream's own after
     decode_attn_stream_reserve, else the device's) to at least nbytes; call before a capture."""
     _check(load_library().decode_attn_weights_reserve(_raw_stream(stream, torch.cuda.current_device()), int(nbytes)))
+
+
+def _token_rows(name, x, heads, dev):
+    """The shape [..., heads, 64] of bf16 rows whose tokens are evenly spaced, their count and the elements from
+    one token to the next."""
+    if x.dim() < 3 or x.shape[-1] != 64 or x.shape[-2] != heads or x.dtype is not torch.bfloat16 or not x.is_cuda \
+            or x.get_device() != dev or x.stride(-1) != 1 or (heads > 1 and x.stride(-2) != 64):
+        _refuse_rows(name, x, heads)
+    tokens, step = 1, None
+    for n, st in zip(reversed(x.shape[:-2]), reversed(x.stride()[:-2])):
+        if n == 1:
+            continue
+        if step is None:
+            step = st
+        elif st != step * tokens:
+            _refuse_rows(name, x, heads)
+        tokens *= n
+    return tokens, heads * 64 if step is None else step
+
+
+def _refuse_rows(name, x, heads):
+    if x.is_cuda and x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} must be CUDA bf16 rows [..., {heads}, 64], contiguous within a token and evenly spaced, "
+                     f"got {x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
+
+
+def _pair_axes(axes, sections, interleaved):
+    """The axis of each of the 32 pairs: the sections one after the other, or the axes taking turns until theirs is
+    used up."""
+    if sections is None:
+        if axes > 1:
+            raise ValueError("positions of several axes need sections")
+        return None
+    left = [int(n) for n in sections]
+    if len(left) != axes or min(left) < 0 or sum(left) != 32:
+        raise ValueError(f"sections {tuple(sections)} must be {axes} counts of pairs that add up to 32")
+    if not interleaved:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    turn = []
+    while len(turn) < 32:
+        for a in range(axes):
+            if left[a]:
+                left[a] -= 1
+                turn.append(a)
+    return bytes(turn)
+
+
+def qk_norm_rope(q, k, positions, rope_cos, rope_sin, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6,
+                 sections=None, interleaved=False, v=None, v_out=None, stream=None):
+    """The RMS norm of every query and key head (q_weight, k_weight fp32 [64]; None: no norm) and the rotary embedding
+    at the given positions, in one pass; value rows (v, v_out) are copied along. q, k, v: bf16 [..., heads, 64], any
+    views whose tokens are evenly spaced (slices of one packed projection); the outputs likewise, or the inputs
+    themselves. positions int32 [tokens], or [axes, tokens] with sections (pairs per axis, 32 in all, in blocks or
+    interleaved: the axes taking turns); rope_cos / rope_sin fp32 [max_position, 32]. Returns q_out, k_out."""
+    dev = torch.cuda.current_device()
+    if (v is None) != (v_out is None):
+        raise ValueError("v and v_out are given together")
+    if q.dim() < 3 or k.dim() < 3:
+        raise ValueError(f"q and k are [..., heads, 64], got {tuple(q.shape)} and {tuple(k.shape)}")
+    Hq, Hkv = q.shape[-2], k.shape[-2]
+    if rope_cos.dim() != 2:
+        raise ValueError(f"rope_cos is [max_position, 32], got {tuple(rope_cos.shape)}")
+    lead, tables = q.shape[:-2], (rope_cos.shape[0], 32)
+    rows, tokens = [], None
+    for name, x, y, heads in (("q", q, q_out, Hq), ("k", k, k_out, Hkv), ("v", v, v_out, Hkv)):
+        if x is None:
+            rows.append(None)
+            continue
+        if x.shape[:-2] != lead or y.shape[:-2] != lead:
+            raise ValueError(f"{name} is {tuple(x.shape)} and {name}_out {tuple(y.shape)}, q is {tuple(q.shape)}")
+        tokens, step = _token_rows(name, x, heads, dev)
+        rows.append(da_rows(x.data_ptr(), y.data_ptr(), step, _token_rows(name + "_out", y, heads, dev)[1]))
+    axes = 1
+    if positions.dim() == 2 and sections is not None:
+        axes = positions.shape[0]
+        pp = _tensor("positions", positions, torch.int32, (axes, tokens), dev)
+    else:
+        pp = _tensor("positions", positions, torch.int32, lead if positions.dim() == len(lead) else (tokens,), dev)
+    weights = [None if w is None else _tensor(n, w, torch.float32, (64,), dev) for n, w in (("q_weight", q_weight), ("k_weight", k_weight))]
+    _check(load_library().qk_norm_rope(
+        ctypes.byref(rows[0]), ctypes.byref(rows[1]), None if rows[2] is None else ctypes.byref(rows[2]), tokens, Hq, Hkv, 64, pp, axes,
+        _pair_axes(axes, sections, interleaved), _tensor("rope_cos", rope_cos, torch.float32, tables, dev),
+        _tensor("rope_sin", rope_sin, torch.float32, tables, dev), rope_cos.shape[0], *weights, float(eps), _raw_stream(stream, dev)))
+    return q_out, k_out
+
+
+def _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev):
+    """Checked addresses of fp8 blocks (pages, or a ring without a block table), and their sizes."""
+    if kv_cache.dim() != (4 if block_table is None else 3):
+        raise ValueError(f"kv_cache is {tuple(kv_cache.shape)}: [num_pages, Hkv, {FP8_BLOCK_BYTES}] with a block table, "
+                         f"[B, Hkv, window / 16, {FP8_BLOCK_BYTES}] without")
+    B, Hkv = seq_lens.shape[0] if seq_lens.dim() else 0, kv_cache.shape[1]
+    lp = _tensor("seq_lens", seq_lens, torch.int32, (B,), dev)
+    if block_table is None:
+        kp = _tensor("kv_cache", kv_cache, torch.uint8, (B, Hkv, kv_cache.shape[2], FP8_BLOCK_BYTES), dev)
+        return kp, None, lp, B, Hkv, 16 * kv_cache.shape[2], (16, 0, 0, 0)
+    if block_table.dim() != 2:
+        raise ValueError(f"the block table is {tuple(block_table.shape)}")
+    kp = _tensor("kv_cache", kv_cache, torch.uint8, (kv_cache.shape[0], Hkv, FP8_BLOCK_BYTES), dev)
+    pages = block_table.shape[1]
+    bp = _tensor("block_table", block_table, torch.int32, (B, pages), dev)
+    return kp, bp, lp, B, Hkv, 0, (16, pages, kv_cache.shape[0], pages * 16 if max_seq_len is None else int(max_seq_len))
+
+
+def kv_append_fp8(k_new, v_new, kv_cache, seq_lens, block_table=None, q_lens=None, max_seq_len=None,
+                  scale_rule=DA_FP8_SCALE_DIVIDE, stream=None):
+    """New tokens quantised into fp8 blocks: k_new, v_new bf16 [B, T, Hkv, 64] (or [B, Hkv, 64]: one each), of which the
+    first q_lens[b] (or T) of sequence b go to the positions before seq_lens[b]. Paged with a block table
+    (kv_cache as in decode_attn_paged_fp8), else a ring (as in decode_attn_ring_fp8)."""
+    dev = torch.cuda.current_device()
+    kp, bp, lp, B, Hkv, window, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
+    T = k_new.shape[1] if k_new.dim() == 4 else 1
+    rows = (B, T, Hkv, 64) if k_new.dim() == 4 else (B, Hkv, 64)
+    _check(load_library().kv_append_fp8(
+        _tensor("k_new", k_new, torch.bfloat16, rows, dev), _tensor("v_new", v_new, torch.bfloat16, rows, dev), kp, bp, lp,
+        None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev), window, int(scale_rule),
+        da_shape(B, Hkv, Hkv, 64), T, *sizes, _raw_stream(stream, dev)))
+
+
+def kv_read_fp8(kv_cache, seq_lens, k_out, v_out, block_table=None, starts=None, max_seq_len=None, stream=None):
+    """Cached positions as bf16: position starts[b] + i (starts None: i) of sequence b to row i of k_out and v_out
+    [B, rows, Hkv, 64], as far as seq_lens[b] and the rows go; the other rows stay as they are. Paged with a block
+    table, else a ring (which holds the last window positions)."""
+    dev = torch.cuda.current_device()
+    kp, bp, lp, B, Hkv, window, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
+    rows = k_out.shape[1] if k_out.dim() > 1 else 0
+    _check(load_library().kv_read_fp8(
+        kp, bp, lp, None if starts is None else _tensor("starts", starts, torch.int32, (B,), dev), window,
+        _tensor("k_out", k_out, torch.bfloat16, (B, rows, Hkv, 64), dev), _tensor("v_out", v_out, torch.bfloat16, (B, rows, Hkv, 64), dev),
+        rows, da_shape(B, Hkv, Hkv, 64), *sizes, _raw_stream(stream, dev)))
+    return k_out, v_out
+
+
+def decode_attn_paged_fp8_multi(q, k_new, v_new, kv_cache, block_table, seq_lens, sinks, window, scale, out, q_lens=None,
+                                max_seq_len=None, scale_rule=DA_FP8_SCALE_DIVIDE, stream=None):
+    """decode_attn_paged_multi over an fp8 cache (kv_cache as in decode_attn_paged_fp8): the new tokens are quantised
+    into their pages, and attended as they are cached. max_seq_len (default: what the block table can hold) sizes
+    the workspace and the split of long sequences."""
+    dev = torch.cuda.current_device()
+    if q.dim() != 4 or block_table is None or k_new is None:
+        raise ValueError("q is [B, T, Hq, 64]; k_new, v_new and the block table are required")
+    kp, bp, lp, B, Hkv, _, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
+    T = q.shape[1]
+    qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B, T), Hkv, dev)
+    _check(load_library().decode_attn_paged_fp8_multi(
+        qp, knp, vnp, kp, bp, lp, None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev), sp, int(window),
+        float(scale), int(scale_rule), op, da_shape(B, Hq, Hkv, 64), T, *sizes, _raw_stream(stream, dev)))
+    return out
+
+
+def decode_attn_paged_fp8_multi_workspace_bytes(batch, num_q_heads, num_kv_heads, q_tokens, window=0, max_seq_len=0, head_dim=64):
+    """Bytes of the multi-token workspace for a decode_attn_paged_fp8_multi call of this shape."""
+    return int(load_library().decode_attn_paged_fp8_multi_workspace_bytes(
+        da_shape(batch, num_q_heads, num_kv_heads, head_dim), int(q_tokens), int(window), int(max_seq_len)))

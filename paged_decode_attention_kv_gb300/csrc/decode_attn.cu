@@ -97,7 +97,7 @@ template <int NT, bool ROPE, bool KV8, int CPS>
 __host__ __device__ constexpr int stages_for() {
     // fp8 tiles are half the size: more of them in flight for the same bytes; with two
     // CTAs per SM each gets half the shared memory
-    return KV8 ? (NT == 1 ? (CPS > 1 ? DA_STAGES_FP8_2CTA : 7) : (ROPE ? 5 : 6))
+    return KV8 ? (NT == 1 ? (CPS > 1 ? DA_STAGES_FP8_2CTA : 7) : NT == 2 ? (ROPE ? 5 : 6) : 4)
                : (NT == 1 ? (ROPE ? DA_STAGES_G8_ROPE : DA_STAGES_G8) : NT == 2 ? DA_STAGES_G16 : DA_STAGES_MT32);
 }
 #ifndef DA_PAIR_BF16
@@ -693,6 +693,38 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 // cover the four consecutive tokens 4t..4t+3 that one 32-bit word of a V^T row holds.
 __device__ __forceinline__ int fp8_row_token(int g) { return 4 * (g >> 1) + (g & 1); }
 
+// A warp's new token, one bf16 pair of its K and V rows per lane, quantised: kn, vn become the pairs'
+// e4m3 codes, ks and vs the rows' scales (the largest magnitude / 448; 1 for a row of zeros).
+__device__ __forceinline__ void fp8_row(uint32_t &kn, uint32_t &vn, bool reciprocal, float &ks, float &vs) {
+    const float2 kf = unpack_bf16(kn), vf = unpack_bf16(vn);
+    float ka = fmaxf(fabsf(kf.x), fabsf(kf.y)), va = fmaxf(fabsf(vf.x), fabsf(vf.y));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, off));
+        va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, off));
+    }
+    if (reciprocal) {
+        ks = ka > 0.f ? __fmul_rn(ka, 1.f / 448.f) : 1.f;
+        vs = va > 0.f ? __fmul_rn(va, 1.f / 448.f) : 1.f;
+    } else {
+        ks = ka > 0.f ? __fdiv_rn(ka, 448.f) : 1.f;
+        vs = va > 0.f ? __fdiv_rn(va, 448.f) : 1.f;
+    }
+    kn = f32x2_to_e4m3x2(__fdiv_rn(kf.x, ks), __fdiv_rn(kf.y, ks));
+    vn = f32x2_to_e4m3x2(__fdiv_rn(vf.x, vs), __fdiv_rn(vf.y, vs));
+}
+
+// It goes into row `row` of a block: a K row of codes, one column of the transposed V tile, both scales.
+__device__ __forceinline__ void fp8_put(uint8_t *blk, int row, uint32_t kn, uint32_t vn, float ks, float vs, int lane) {
+    *reinterpret_cast<uint16_t *>(blk + row * kD + 2 * lane) = static_cast<uint16_t>(kn);
+    blk[kBlk8V + (2 * lane) * kPage + row] = static_cast<uint8_t>(vn);
+    blk[kBlk8V + (2 * lane + 1) * kPage + row] = static_cast<uint8_t>(vn >> 8);
+    if (lane == 0) {
+        reinterpret_cast<float *>(blk + kBlk8S)[row] = ks;
+        reinterpret_cast<float *>(blk + kBlk8S)[kPage + row] = vs;
+    }
+}
+
 // Shared-memory layout of decode_attn_kernel<NT, ., ROPE, KV8, CPS>: byte offsets from a 1024-byte
 // aligned base. The kernel carves its buffers from these offsets and the launch
 // requests `bytes`, so the two cannot drift apart.
@@ -709,7 +741,8 @@ struct SmemLayout {
     // several query tokens: the GP query rows of this CTA's row group (the new tokens' k/v
     // rows go to registers straight from global memory)
     static constexpr int kQBytes = MT ? GP * kD * 2 : kRopeOff + (ROPE ? 2 * (kD / 2) * 4 : 0);
-    static constexpr int kWarpTileBytes = kStages * kStageBytes;  // the tiles of one warp
+    // the tiles of one warp (fp8 with 32 query rows: and room for a merge slot)
+    static constexpr int kWarpTileBytes = kStages * kStageBytes + (KV8 && NT == 4 ? 256 : 0);
     static constexpr int kInts = (kMaxBatch + 1) + kMaxBatch + 2 * kWarps + kWarps * kWinfo + 16 +
                                  (kMaxCtasPerSm * kMaxSms + 1) + (MT ? kMaxBatch : 0);
     static constexpr size_t qarea = static_cast<size_t>(kWarps) * kWarpTileBytes;
@@ -728,7 +761,7 @@ struct SmemLayout {
 };
 
 // ------------------------------------------------------------------ the kernel
-// MT: several query tokens per sequence (paged, bf16, T <= kMaxNewMT): the query rows of a
+// MT: several query tokens per sequence (paged, bf16 or fp8, T <= kMaxNewMT): the query rows of a
 // KV head are (token t, head h) pairs r = t G + h, one column of the products each; row t
 // sees the positions lo_t .. base + t (base = L - n, lo_t its window start), the n new tokens
 // are appended in the same pass, rows t >= n are zero. With more than 16 rows per KV head the
@@ -739,7 +772,8 @@ template <int NT, bool RING, bool ROPE, bool KV8, int CPS, bool MT = false, bool
 __global__ void __launch_bounds__(kThreads, CPS)
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const Params p) {
-    static_assert(!MT || (!RING && !ROPE && !KV8 && CPS == 1), "several query tokens: paged bf16 only");
+    static_assert(!MT || (!RING && !ROPE && CPS == 1), "several query tokens: paged only");
+    static_assert(!MT || !KV8 || !WTS, "several query tokens on fp8 blocks: no weights");
     using Lay = SmemLayout<NT, ROPE, KV8, CPS, MT>;
     constexpr int kTileB = KV8 ? kBlk8V : kTileBytes;  // bytes of one K (or V) tile
     constexpr int kStages = Lay::kStages;
@@ -1287,7 +1321,6 @@ __global__ void __launch_bounds__(kThreads, CPS)
                         const int pos = base + i2;
                         if (i2 < nq_seg && pos / kPage - ft == tt) {
                             const int row = pos % kPage;
-                            const uint32_t off = row * 128 + ((((lane >> 2) ^ (row & 7))) << 4) + (lane & 3) * 4;
                             uint32_t kn, vn;
                             if constexpr (kNewInRegs) {
                                 kn = knewm[i2];
@@ -1297,12 +1330,23 @@ __global__ void __launch_bounds__(kThreads, CPS)
                                 kn = __ldg(reinterpret_cast<const uint32_t *>(p.k_new + o) + lane);
                                 vn = __ldg(reinterpret_cast<const uint32_t *>(p.v_new + o) + lane);
                             }
-                            *reinterpret_cast<uint32_t *>(gK + off) = kn;
-                            *reinterpret_cast<uint32_t *>(gV + off) = vn;
-                            if (tp >= 0 && rgrp == 0) {
-                                const size_t c = (static_cast<size_t>(tp) * Hkv + sgk) * kPage + row;
-                                reinterpret_cast<uint32_t *>(p.k_cache + c * kD)[lane] = kn;
-                                reinterpret_cast<uint32_t *>(p.v_cache + c * kD)[lane] = vn;
+                            if constexpr (KV8) {  // quantised where it is appended
+                                float ks, vs;
+                                fp8_row(kn, vn, p.fp8_rule == DA_FP8_SCALE_RECIPROCAL, ks, vs);
+                                fp8_put(gK, row, kn, vn, ks, vs, lane);
+                                if (tp >= 0 && rgrp == 0)
+                                    fp8_put(reinterpret_cast<uint8_t *>(p.k_cache) +
+                                                (static_cast<size_t>(tp) * Hkv + sgk) * kBlk8Bytes,
+                                            row, kn, vn, ks, vs, lane);
+                            } else {
+                                const uint32_t off = row * 128 + ((((lane >> 2) ^ (row & 7))) << 4) + (lane & 3) * 4;
+                                *reinterpret_cast<uint32_t *>(gK + off) = kn;
+                                *reinterpret_cast<uint32_t *>(gV + off) = vn;
+                                if (tp >= 0 && rgrp == 0) {
+                                    const size_t c = (static_cast<size_t>(tp) * Hkv + sgk) * kPage + row;
+                                    reinterpret_cast<uint32_t *>(p.k_cache + c * kD)[lane] = kn;
+                                    reinterpret_cast<uint32_t *>(p.v_cache + c * kD)[lane] = vn;
+                                }
                             }
                             any = true;
                         }
@@ -1322,21 +1366,12 @@ __global__ void __launch_bounds__(kThreads, CPS)
                         cell = app_row;
                     }
                     if constexpr (KV8) {
-                        // K row of codes, one column of the transposed V tile and both scales, in
-                        // the staged block and in the cache block (the same bytes)
-                        auto put = [&](uint8_t *blk) {
-                            *reinterpret_cast<uint16_t *>(blk + app_row * kD + 2 * lane) = static_cast<uint16_t>(knew);
-                            blk[kBlk8V + (2 * lane) * kPage + app_row] = static_cast<uint8_t>(vnew);
-                            blk[kBlk8V + (2 * lane + 1) * kPage + app_row] = static_cast<uint8_t>(vnew >> 8);
-                            if (lane == 0) {
-                                reinterpret_cast<float *>(blk + kBlk8S)[app_row] = knew_scale;
-                                reinterpret_cast<float *>(blk + kBlk8S)[kPage + app_row] = vnew_scale;
-                            }
-                        };
-                        put(gK);
+                        // in the staged block and in the cache block (the same bytes)
+                        fp8_put(gK, app_row, knew, vnew, knew_scale, vnew_scale, lane);
                         if (ok) {
                             const size_t blk = RING ? slice * (p.window / kPage) + tt : slice;
-                            put(reinterpret_cast<uint8_t *>(p.k_cache) + blk * kBlk8Bytes);
+                            fp8_put(reinterpret_cast<uint8_t *>(p.k_cache) + blk * kBlk8Bytes, app_row, knew, vnew,
+                                    knew_scale, vnew_scale, lane);
                         }
                     } else {
                         const uint32_t off = app_row * 128 + ((((lane >> 2) ^ (app_row & 7))) << 4) + (lane & 3) * 4;
@@ -1450,8 +1485,8 @@ __global__ void __launch_bounds__(kThreads, CPS)
                     sv[u][2] = (sc[2] + sd[2]) * sl_hi;
                     sv[u][3] = (sc[3] + sd[3]) * sl_hi;
                     if (partial[u]) {
-                        if constexpr (MT) {  // key rows t0 + lane/4 and + 8 against each column's range
-                            const int kl = t0[u] + (lane >> 2), kh = kl + 8;
+                        if constexpr (MT) {  // this lane's two key rows against each column's range
+                            const int kl = t0[u] + row_tok, kh = kl + (KV8 ? 2 : 8);
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const int r = r0g + n * 8 + (lane & 3) * 2 + j, t = r / p.G;
@@ -1771,25 +1806,10 @@ __global__ void __launch_bounds__(kThreads, CPS)
                     }
                 }
                 if constexpr (KV8) {
-                    if (do_append) {  // quantise the new token: per row amax / 448, e4m3 codes
-                        const float2 kf = unpack_bf16(knew), vf = unpack_bf16(vnew);
-                        float ka = fmaxf(fabsf(kf.x), fabsf(kf.y)), va = fmaxf(fabsf(vf.x), fabsf(vf.y));
-#pragma unroll
-                        for (int off = 16; off > 0; off >>= 1) {
-                            ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, off));
-                            va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, off));
-                        }
-                        // (without weights: always the division, and no branch)
-                        if (WTS && p.fp8_rule == DA_FP8_SCALE_RECIPROCAL) {
-                            knew_scale = ka > 0.f ? __fmul_rn(ka, 1.f / 448.f) : 1.f;
-                            vnew_scale = va > 0.f ? __fmul_rn(va, 1.f / 448.f) : 1.f;
-                        } else {
-                            knew_scale = ka > 0.f ? __fdiv_rn(ka, 448.f) : 1.f;
-                            vnew_scale = va > 0.f ? __fdiv_rn(va, 448.f) : 1.f;
-                        }
-                        knew = f32x2_to_e4m3x2(__fdiv_rn(kf.x, knew_scale), __fdiv_rn(kf.y, knew_scale));
-                        vnew = f32x2_to_e4m3x2(__fdiv_rn(vf.x, vnew_scale), __fdiv_rn(vf.y, vnew_scale));
-                    }
+                    // quantise the new token (without weights: always the division, and no branch; several
+                    // tokens: where they are appended)
+                    if (!MT && do_append)
+                        fp8_row(knew, vnew, WTS && p.fp8_rule == DA_FP8_SCALE_RECIPROCAL, knew_scale, vnew_scale);
                 }
                 state_reset(st);
             }
@@ -2152,6 +2172,8 @@ __global__ void kv_append_kernel(const __nv_bfloat16 *__restrict__ k_new,
 // ------------------------------------------------------------------ several query tokens
 #include "multi_attn.cuh"
 #include "multi_tc.cuh"
+#include "fp8_step.cuh"
+#include "multi_tc8.cuh"
 
 // ------------------------------------------------------------------ accumulated weights, eviction
 #include "weights.cuh"
@@ -2271,6 +2293,7 @@ struct DeviceState {
     std::atomic<bool> multi_attr_set[8] = {};
     std::atomic<int> evict_clusters[2] = {-1, -1};  // resident clusters of 16 of the eviction kernel, -1: not asked yet
     std::atomic<bool> mw_attr_set[6] = {};
+    std::atomic<bool> fp8_multi_attr_set{false};
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -2732,6 +2755,49 @@ size_t rope_scratch_bytes(const da_shape &s, int T) {
     return up(rows * s.num_q_heads * kD * 2) + up(rows * s.num_kv_heads * kD * 2);
 }
 
+// The decode kernel's several-token form (m.dec) on the workspace ws.
+Params multi_decode_params(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                           const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                           const float *sinks, int window, float scale, void *out, const da_shape &s, int T,
+                           int max_pages, int num_pages, int max_seq_len, const MultiPlan &m, void *ws, int dev,
+                           const WeightsOut *wts) {
+    Params dp;
+    dp.q = static_cast<const __nv_bfloat16 *>(q);
+    dp.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+    dp.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+    dp.k_cache = static_cast<__nv_bfloat16 *>(k_cache);
+    dp.v_cache = static_cast<__nv_bfloat16 *>(v_cache);
+    dp.block_table = block_table;
+    dp.seq_lens = seq_lens;
+    dp.sinks = sinks;
+    dp.out = static_cast<__nv_bfloat16 *>(out);
+    dp.counters = static_cast<int *>(ws);
+    dp.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
+    dp.B = s.batch;
+    dp.Hq = s.num_q_heads;
+    dp.Hkv = s.num_kv_heads;
+    dp.G = s.num_q_heads / s.num_kv_heads;
+    dp.window = window;
+    dp.max_pages = max_pages;
+    dp.num_pages = num_pages;
+    dp.max_seq_len = max_seq_len;
+    dp.scale_log2 = scale * kLog2e;
+    dp.rope_cos = nullptr;
+    dp.rope_sin = nullptr;
+    dp.max_position = 0;
+    dp.T = T;
+    dp.q_lens = q_lens;
+    dp.ngrp = m.row_blocks;
+    dp.expire_at = -1;
+    dp.head_scratch = m.rows == 32 ? dp.part + static_cast<size_t>(sm_count(dev)) * 2 * slot_floats(m.rows) : nullptr;
+    dp.early = g_early_inputs.load();
+    dp.nlse = wts ? wts->nlse : nullptr;
+    dp.lse_ld = wts ? wts->lse_ld : 0;
+    dp.scores = nullptr;
+    dp.fp8_rule = DA_FP8_SCALE_DIVIDE;
+    return dp;
+}
+
 int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
               const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens, const float *sinks,
               int window, float scale, void *out, const da_shape &s, int T, int page_size, int max_pages,
@@ -2785,40 +2851,8 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         k_new = k_rot;
     }
     if (m.dec) {  // the decode kernel's several-token form, on this workspace
-        Params dp;
-        dp.q = static_cast<const __nv_bfloat16 *>(q);
-        dp.k_new = static_cast<const __nv_bfloat16 *>(k_new);
-        dp.v_new = static_cast<const __nv_bfloat16 *>(v_new);
-        dp.k_cache = static_cast<__nv_bfloat16 *>(k_cache);
-        dp.v_cache = static_cast<__nv_bfloat16 *>(v_cache);
-        dp.block_table = block_table;
-        dp.seq_lens = seq_lens;
-        dp.sinks = sinks;
-        dp.out = static_cast<__nv_bfloat16 *>(out);
-        dp.counters = static_cast<int *>(ws);
-        dp.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
-        dp.B = s.batch;
-        dp.Hq = s.num_q_heads;
-        dp.Hkv = s.num_kv_heads;
-        dp.G = s.num_q_heads / s.num_kv_heads;
-        dp.window = window;
-        dp.max_pages = max_pages;
-        dp.num_pages = num_pages;
-        dp.max_seq_len = max_seq_len;
-        dp.scale_log2 = scale * kLog2e;
-        dp.rope_cos = nullptr;
-        dp.rope_sin = nullptr;
-        dp.max_position = 0;
-        dp.T = T;
-        dp.q_lens = q_lens;
-        dp.ngrp = m.row_blocks;
-        dp.expire_at = -1;
-        dp.head_scratch = m.rows == 32 ? dp.part + static_cast<size_t>(sm_count(dev)) * 2 * slot_floats(m.rows) : nullptr;
-        dp.early = g_early_inputs.load();
-        dp.nlse = wts ? wts->nlse : nullptr;
-        dp.lse_ld = wts ? wts->lse_ld : 0;
-        dp.scores = nullptr;
-        dp.fp8_rule = DA_FP8_SCALE_DIVIDE;
+        const Params dp = multi_decode_params(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, q_lens, sinks, window,
+                                              scale, out, s, T, max_pages, num_pages, max_seq_len, m, ws, dev, wts);
         CUtensorMap mk, mv;
         const uint64_t slices = static_cast<uint64_t>(num_pages) * s.num_kv_heads;
         if (!make_kv_map(&mk, k_cache, kPage, slices) || !make_kv_map(&mv, v_cache, kPage, slices)) {
@@ -2908,7 +2942,7 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         cc.stream = stream;
         cc.attrs = attr;
         cc.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cc, multi_combine_kernel, prm, m.rows, ring ? 1 : 0);
+        e = cudaLaunchKernelEx(&cc, multi_combine_kernel<false>, prm, m.rows, ring ? 1 : 0);
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return set_cuda_error(e);
     }
@@ -2925,6 +2959,248 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
                            prm.max_seq_len);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+}
+
+// ------------------------------------------------------------------ fp8 steps of new tokens: host side
+// Launched as a programmatic dependent of the kernel before it in the stream.
+template <typename Kernel, typename... Args>
+int launch_pdl(Kernel kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? DA_OK : set_cuda_error(e);
+}
+
+int run_rotate(const da_rows *q, const da_rows *k, const da_rows *v, int tokens, int Hq, int Hkv, int head_dim,
+               const int32_t *positions, int axes, const unsigned char *pair_axis, const float *rope_cos,
+               const float *rope_sin, int max_position, const float *q_weight, const float *k_weight, float eps,
+               void *stream) {
+    if (!q || !k || tokens < 0 || Hq <= 0 || Hkv <= 0 || head_dim <= 0) return DA_ERR_INVALID_ARG;
+    if (head_dim != kD || Hq > kMaxQHeads || Hkv > kMaxQHeads) return DA_ERR_UNSUPPORTED;
+    if (!positions || !rope_cos || !rope_sin || max_position <= 0 || !aligned16(rope_cos) || !aligned16(rope_sin))
+        return DA_ERR_INVALID_ARG;
+    if (axes < 1 || axes > 3 || (axes > 1 && !pair_axis)) return DA_ERR_INVALID_ARG;
+    if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !(eps >= 0.f) || eps == INFINITY)
+        return DA_ERR_INVALID_ARG;
+    auto rows_ok = [&](const da_rows *r, int heads) {
+        const long long least = static_cast<long long>(heads) * kD;
+        return r->in && r->out && aligned16(r->in) && aligned16(r->out) && r->in_stride % 8 == 0 && r->out_stride % 8 == 0 &&
+               (tokens <= 1 || (r->in_stride >= least && r->out_stride >= least));
+    };
+    if (!rows_ok(q, Hq) || !rows_ok(k, Hkv) || (v && !rows_ok(v, Hkv))) return DA_ERR_INVALID_ARG;
+    RotateParams p = {};
+    for (int i = 0; i < kD / 2; ++i) {
+        p.axis[i] = axes > 1 ? pair_axis[i] : 0;
+        if (p.axis[i] >= axes) return DA_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < kD / 8; ++i)
+        if (p.axis[4 * i] == p.axis[4 * i + 1] && p.axis[4 * i] == p.axis[4 * i + 2] && p.axis[4 * i] == p.axis[4 * i + 3])
+            p.quads = static_cast<unsigned char>(p.quads | 1u << i);
+    if (tokens == 0) return DA_OK;
+    int dev;
+    int rc = current_device(&dev);
+    if (rc != DA_OK) return rc;
+    auto in = [](const da_rows *r) { return r ? static_cast<const __nv_bfloat16 *>(r->in) : nullptr; };
+    auto out = [](const da_rows *r) { return r ? static_cast<__nv_bfloat16 *>(r->out) : nullptr; };
+    p.q = in(q), p.k = in(k), p.v = in(v);
+    p.q_out = out(q), p.k_out = out(k), p.v_out = out(v);
+    p.q_ld = q->in_stride, p.k_ld = k->in_stride, p.v_ld = v ? v->in_stride : 0;
+    p.qo_ld = q->out_stride, p.ko_ld = k->out_stride, p.vo_ld = v ? v->out_stride : 0;
+    p.positions = positions;
+    p.rope_cos = rope_cos, p.rope_sin = rope_sin;
+    p.q_weight = q_weight, p.k_weight = k_weight;
+    p.eps = eps;
+    p.N = tokens, p.Hq = Hq, p.Hkv = Hkv, p.max_position = max_position;
+    p.rows = Hq + Hkv + (v ? Hkv : 0);
+    p.chunk = kRotRows;
+    const long long items = static_cast<long long>(tokens) * ((p.rows + p.chunk - 1) / p.chunk);
+    const long long blocks = (items + kRotThreads / 32 - 1) / (kRotThreads / 32);
+    if (blocks > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+    return launch_pdl(qk_norm_rope_kernel, dim3(static_cast<unsigned>(blocks)), kRotThreads, 0, static_cast<cudaStream_t>(stream), p);
+}
+
+// The arguments of fp8 blocks that every call over many of their tokens checks alike.
+int check_blocks(const void *kv_cache, const int32_t *block_table, const int32_t *seq_lens, int window, const da_shape &s,
+                 int page_size, int max_pages, int num_pages, int max_seq_len) {
+    if (s.batch < 0 || s.num_kv_heads <= 0 || s.head_dim <= 0) return DA_ERR_INVALID_ARG;
+    if (s.head_dim != kD || s.batch > kMaxBatch || static_cast<long long>(s.batch) * s.num_kv_heads > kMaxSegments)
+        return DA_ERR_UNSUPPORTED;
+    if (!kv_cache || !seq_lens || !aligned16(kv_cache)) return DA_ERR_INVALID_ARG;
+    if (block_table) {
+        if (max_pages <= 0 || num_pages <= 0 || max_seq_len < 0) return DA_ERR_INVALID_ARG;
+        if (page_size != kPage) return DA_ERR_UNSUPPORTED;
+        if (static_cast<long long>(max_pages) * kPage < max_seq_len) return DA_ERR_INVALID_ARG;
+        if (static_cast<long long>(num_pages) * s.num_kv_heads > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+    } else {
+        if (window <= 0) return DA_ERR_INVALID_ARG;
+        if (window % kPage != 0) return DA_ERR_UNSUPPORTED;
+    }
+    return DA_OK;
+}
+
+// One warp per block that `positions` consecutive positions can touch, and KV head.
+int launch_blocks_grid(long long positions, long long most, int Hkv, int batch, dim3 *grid) {
+    const long long blocks = std::min((std::min(positions, most) + 2 * kPage - 2) / kPage, most / kPage + 1);
+    const long long x = (blocks * Hkv + kStoreWarps - 1) / kStoreWarps;
+    if (x > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+    *grid = dim3(static_cast<unsigned>(std::max<long long>(x, 1)), static_cast<unsigned>(batch));
+    return DA_OK;
+}
+
+int run_append_fp8(const void *k_new, const void *v_new, void *kv_cache, const int32_t *block_table,
+                   const int32_t *seq_lens, const int32_t *q_lens, int window, int scale_rule, const da_shape &s, int T,
+                   int page_size, int max_pages, int num_pages, int max_seq_len, void *stream) {
+    int rc = check_blocks(kv_cache, block_table, seq_lens, window, s, page_size, max_pages, num_pages, max_seq_len);
+    if (rc != DA_OK) return rc;
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || T <= 0) return DA_ERR_INVALID_ARG;
+    if (scale_rule != DA_FP8_SCALE_RECIPROCAL && scale_rule != DA_FP8_SCALE_DIVIDE) return DA_ERR_INVALID_ARG;
+    if (s.batch == 0) return DA_OK;
+    dim3 grid;
+    rc = launch_blocks_grid(T, block_table ? max_seq_len : window, s.num_kv_heads, s.batch, &grid);
+    if (rc != DA_OK) return rc;
+    const BlockParams p = {static_cast<uint8_t *>(kv_cache), block_table, seq_lens, s.num_kv_heads,
+                           block_table ? 0 : window, block_table ? max_pages : 0, block_table ? num_pages : 0, max_seq_len};
+    return launch_pdl(kv_append_fp8_kernel, grid, kStoreWarps * 32, 0, static_cast<cudaStream_t>(stream), p,
+                      static_cast<const __nv_bfloat16 *>(k_new), static_cast<const __nv_bfloat16 *>(v_new), q_lens, T, scale_rule);
+}
+
+int run_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,
+                 int window, void *k_out, void *v_out, int rows, const da_shape &s, int page_size, int max_pages,
+                 int num_pages, int max_seq_len, void *stream) {
+    int rc = check_blocks(kv_cache, block_table, seq_lens, window, s, page_size, max_pages, num_pages, max_seq_len);
+    if (rc != DA_OK) return rc;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || rows < 0) return DA_ERR_INVALID_ARG;
+    if (s.batch == 0 || rows == 0) return DA_OK;
+    dim3 grid;
+    rc = launch_blocks_grid(rows, block_table ? max_seq_len : window, s.num_kv_heads, s.batch, &grid);
+    if (rc != DA_OK) return rc;
+    const BlockParams p = {static_cast<uint8_t *>(const_cast<void *>(kv_cache)), block_table, seq_lens, s.num_kv_heads,
+                           block_table ? 0 : window, block_table ? max_pages : 0, block_table ? num_pages : 0, max_seq_len};
+    return launch_pdl(kv_read_fp8_kernel, grid, kStoreWarps * 32, 0, static_cast<cudaStream_t>(stream), p, starts, rows,
+                      static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out),
+                      ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0 ? 1 : 0);
+}
+
+// How a several-token call over fp8 pages is cut: the decode kernel's several-token form as
+// multi_plan has it, else multi_tc8_kernel. Of shapes only, like multi_plan.
+MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, int sms) {
+    MultiPlan m = multi_plan(s, T, false, window, max_seq_len, sms);
+    if (m.dec) return m;
+    const int G = s.num_q_heads / s.num_kv_heads;
+    const long long TG = static_cast<long long>(T) * G;
+    m.tc = true;
+    m.nw = kT8Warps;
+    m.rows = kT8Rows;
+    m.row_blocks = static_cast<int>((TG + kT8Rows - 1) / kT8Rows);
+    // the most tiles that a row block's keys touch: under a window, those of its rows' windows
+    long long max_tiles = (static_cast<long long>(max_seq_len) + kPage - 1) / kPage;
+    if (window > 0) {
+        const long long tokens = std::min<long long>(T, (kT8Rows - 1) / G + 2);
+        max_tiles = std::min(max_tiles, (static_cast<long long>(window) + tokens + kPage - 2) / kPage + 1);
+    }
+    max_tiles = std::max(max_tiles, 1ll);
+    m.groups = static_cast<long long>(s.batch) * s.num_kv_heads * m.row_blocks;
+    const long long target = static_cast<long long>(DA_MULTI_TC_CTAS_PER_SM) * sms;
+    long long sp = std::max<long long>(1, (target + m.groups - 1) / std::max<long long>(1, m.groups));
+    sp = std::min(sp, std::max<long long>(1, max_tiles / DA_MULTI_MIN_CHUNK));
+    sp = std::max(sp, (max_tiles + kMMaxChunk - 1) / kMMaxChunk);  // a CTA's pages fit its smem
+    m.chunk = static_cast<int>((max_tiles + sp - 1) / sp);
+    m.splits = static_cast<int>((max_tiles + m.chunk - 1) / m.chunk);
+    m.defer = m.splits >= DA_MULTI_DEFER_SPLITS;
+    m.counter_bytes = static_cast<size_t>(kMMaxGroups) * sizeof(int);
+    m.part_bytes = m.splits > 1 ? static_cast<size_t>(m.groups) * m.splits * m.rows * kMSlotFloats * sizeof(float) : 0;
+    return m;
+}
+
+int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_cache, const int32_t *block_table,
+                  const int32_t *seq_lens, const int32_t *q_lens, const float *sinks, int window, float scale,
+                  int scale_rule, void *out, const da_shape &s, int T, int page_size, int max_pages, int num_pages,
+                  int max_seq_len, void *stream_v) {
+    int rc = check_shape(s);
+    if (rc != DA_OK) return rc;
+    if (!block_table || !q || !k_new || !v_new || !out || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))
+        return DA_ERR_INVALID_ARG;
+    rc = check_blocks(kv_cache, block_table, seq_lens, window, s, page_size, max_pages, num_pages, max_seq_len);
+    if (rc != DA_OK) return rc;
+    if (!(scale > 0.f) || scale == INFINITY || T <= 0 || window < 0) return DA_ERR_INVALID_ARG;
+    if (scale_rule != DA_FP8_SCALE_RECIPROCAL && scale_rule != DA_FP8_SCALE_DIVIDE) return DA_ERR_INVALID_ARG;
+    if (T > kMMaxTokens) return DA_ERR_UNSUPPORTED;
+    if (s.batch == 0) return DA_OK;
+    int dev;
+    rc = current_device(&dev);
+    if (rc != DA_OK) return rc;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    const MultiPlan m = multi_fp8_plan(s, T, window, max_seq_len, sm_count(dev));
+    if (static_cast<long long>(m.splits) * m.row_blocks > 0x7fffffffLL || m.groups > kMMaxGroups) return DA_ERR_UNSUPPORTED;
+    void *ws = nullptr;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        rc = workspace_locked(dev, stream, kWsMulti, m.counter_bytes + m.part_bytes, &ws);
+        if (rc != DA_OK) return rc;
+    }
+    if (m.dec) {
+        Params dp = multi_decode_params(q, k_new, v_new, kv_cache, nullptr, block_table, seq_lens, q_lens, sinks, window,
+                                        scale, out, s, T, max_pages, num_pages, max_seq_len, m, ws, dev, nullptr);
+        dp.fp8_rule = scale_rule;
+        CUtensorMap none;
+        memset(&none, 0, sizeof none);
+        return m.rows == 8    ? launch_attn<1, false, false, true, 1, true>(none, none, dp, dev, stream)
+               : m.rows == 16 ? launch_attn<2, false, false, true, 1, true>(none, none, dp, dev, stream)
+                              : launch_attn<4, false, false, true, 1, true>(none, none, dp, dev, stream);
+    }
+    if (!g_dev[dev].fp8_multi_attr_set.load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(multi_tc8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kT8Smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(multi_tc8_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return set_cuda_error(e);
+        g_dev[dev].fp8_multi_attr_set.store(true, std::memory_order_release);
+    }
+    // the new tokens first: the attention reads every key from the cache
+    rc = run_append_fp8(k_new, v_new, kv_cache, block_table, seq_lens, q_lens, 0, scale_rule, s, T, page_size, max_pages,
+                        num_pages, max_seq_len, stream_v);
+    if (rc != DA_OK) return rc;
+    MultiParams prm = {};
+    prm.q = static_cast<const __nv_bfloat16 *>(q);
+    prm.out = static_cast<__nv_bfloat16 *>(out);
+    prm.block_table = block_table;
+    prm.seq_lens = seq_lens;
+    prm.q_lens = q_lens;
+    prm.sinks = sinks;
+    prm.scale_log2 = scale * kLog2e;
+    prm.B = s.batch;
+    prm.Hq = s.num_q_heads;
+    prm.Hkv = s.num_kv_heads;
+    prm.G = s.num_q_heads / s.num_kv_heads;
+    prm.T = T;
+    prm.window = window;
+    prm.max_pages = max_pages;
+    prm.num_pages = num_pages;
+    prm.max_seq_len = max_seq_len;
+    prm.row_blocks = m.row_blocks;
+    prm.splits = m.splits;
+    prm.chunk = m.chunk;
+    prm.counters = static_cast<int *>(ws);
+    prm.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
+    prm.defer = m.defer ? 1 : 0;
+    rc = launch_pdl(multi_tc8_kernel,
+                    dim3(static_cast<unsigned>(m.splits * m.row_blocks), static_cast<unsigned>(s.num_kv_heads),
+                         static_cast<unsigned>(s.batch)),
+                    kT8Threads, kT8Smem, stream, prm, static_cast<const uint8_t *>(kv_cache));
+    if (rc != DA_OK || !m.defer) return rc;
+    return launch_pdl(multi_combine_kernel<true>,
+                      dim3(static_cast<unsigned>(m.row_blocks * ((m.rows + kCombWarps - 1) / kCombWarps)),
+                           static_cast<unsigned>(s.num_kv_heads), static_cast<unsigned>(s.batch)),
+                      kCombWarps * 32, 0, stream, prm, m.rows, 0);
 }
 
 // ------------------------------------------------------------------ accumulated weights: host side
@@ -3561,6 +3837,46 @@ int decode_attn_paged_noalloc(const void *q, const void *k_new, const void *v_ne
                               int num_pages, int max_seq_len, void *stream) {
     return run_paged_noalloc(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, sinks, window, scale, out,
                              s, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+int qk_norm_rope(const da_rows *q, const da_rows *k, const da_rows *v, int tokens, int num_q_heads, int num_kv_heads,
+                 int head_dim, const int32_t *positions, int axes, const unsigned char *pair_axis, const float *rope_cos,
+                 const float *rope_sin, int max_position, const float *q_weight, const float *k_weight, float eps,
+                 void *stream) {
+    return run_rotate(q, k, v, tokens, num_q_heads, num_kv_heads, head_dim, positions, axes, pair_axis, rope_cos, rope_sin,
+                      max_position, q_weight, k_weight, eps, stream);
+}
+
+int kv_append_fp8(const void *k_new, const void *v_new, void *kv_cache, const int32_t *block_table,
+                  const int32_t *seq_lens, const int32_t *q_lens, int window, int scale_rule, da_shape s, int q_tokens,
+                  int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void *stream) {
+    return run_append_fp8(k_new, v_new, kv_cache, block_table, seq_lens, q_lens, window, scale_rule, s, q_tokens, page_size,
+                          max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+int kv_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,
+                int window, void *k_out, void *v_out, int rows, da_shape s, int page_size, int max_pages_per_seq,
+                int num_pages, int max_seq_len, void *stream) {
+    return run_read_fp8(kv_cache, block_table, seq_lens, starts, window, k_out, v_out, rows, s, page_size, max_pages_per_seq,
+                        num_pages, max_seq_len, stream);
+}
+
+int decode_attn_paged_fp8_multi(const void *q, const void *k_new, const void *v_new, void *kv_cache,
+                                const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                                const float *sinks, int window, float scale, int scale_rule, void *out, da_shape s,
+                                int q_tokens, int page_size, int max_pages_per_seq, int num_pages, int max_seq_len,
+                                void *stream) {
+    return run_multi_fp8(q, k_new, v_new, kv_cache, block_table, seq_lens, q_lens, sinks, window, scale, scale_rule, out, s,
+                         q_tokens, page_size, max_pages_per_seq, num_pages, max_seq_len, stream);
+}
+
+size_t decode_attn_paged_fp8_multi_workspace_bytes(da_shape s, int q_tokens, int window, int max_seq_len) {
+    int dev;
+    if (check_shape(s) != DA_OK || q_tokens <= 0 || q_tokens > kMMaxTokens || window < 0 || max_seq_len < 0 ||
+        current_device(&dev) != DA_OK)
+        return 0;
+    const MultiPlan m = multi_fp8_plan(s, q_tokens, window, max_seq_len, sm_count(dev));
+    return m.groups > kMMaxGroups ? 0 : m.counter_bytes + m.part_bytes;
 }
 
 int decode_attn_paged_multi(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
