@@ -2357,7 +2357,9 @@ int grow_locked(Workspace &w, size_t bytes) {
     void *p = nullptr;
     cudaError_t e = cudaMalloc(&p, bytes);
     if (e != cudaSuccess) return set_cuda_error(e);
+    // the zeros are written on the legacy stream, which a non-blocking stream's call does not wait for
     e = cudaMemset(p, 0, bytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         cudaFree(p);
         return set_cuda_error(e);
