@@ -2944,7 +2944,7 @@ int run_multi(bool ring, const void *q, const void *k_new, const void *v_new, vo
         cc.stream = stream;
         cc.attrs = attr;
         cc.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cc, multi_combine_kernel<false>, prm, m.rows, ring ? 1 : 0);
+        e = cudaLaunchKernelEx(&cc, multi_combine_kernel, prm, m.rows, ring ? 1 : 0);
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return set_cuda_error(e);
     }
@@ -3092,6 +3092,9 @@ int run_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t
                       ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0 ? 1 : 0);
 }
 
+#ifndef DA_T8_DEFER
+#define DA_T8_DEFER 4
+#endif
 // How a several-token call over fp8 pages is cut: the decode kernel's several-token form as
 // multi_plan has it, else multi_tc8_kernel. Of shapes only, like multi_plan.
 MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, int sms) {
@@ -3103,23 +3106,13 @@ MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, 
     m.nw = kT8Warps;
     m.rows = kT8Rows;
     m.row_blocks = static_cast<int>((TG + kT8Rows - 1) / kT8Rows);
-    // the most tiles that a row block's keys touch: under a window, those of its rows' windows
-    long long max_tiles = (static_cast<long long>(max_seq_len) + kPage - 1) / kPage;
-    if (window > 0) {
-        const long long tokens = std::min<long long>(T, (kT8Rows - 1) / G + 2);
-        max_tiles = std::min(max_tiles, (static_cast<long long>(window) + tokens + kPage - 2) / kPage + 1);
-    }
-    max_tiles = std::max(max_tiles, 1ll);
     m.groups = static_cast<long long>(s.batch) * s.num_kv_heads * m.row_blocks;
-    const long long target = static_cast<long long>(DA_MULTI_TC_CTAS_PER_SM) * sms;
-    long long sp = std::max<long long>(1, (target + m.groups - 1) / std::max<long long>(1, m.groups));
-    sp = std::min(sp, std::max<long long>(1, max_tiles / DA_MULTI_MIN_CHUNK));
-    sp = std::max(sp, (max_tiles + kMMaxChunk - 1) / kMMaxChunk);  // a CTA's pages fit its smem
-    m.chunk = static_cast<int>((max_tiles + sp - 1) / sp);
-    m.splits = static_cast<int>((max_tiles + m.chunk - 1) / m.chunk);
-    m.defer = m.splits >= DA_MULTI_DEFER_SPLITS;
+    m.splits = 1;
+    m.chunk = 0;
+    // segments so few that each is spread over four CTAs or more, if they are about equally long
+    m.defer = m.groups * DA_T8_DEFER <= static_cast<long long>(kT8CtasPerSm) * sms;
     m.counter_bytes = static_cast<size_t>(kMMaxGroups) * sizeof(int);
-    m.part_bytes = m.splits > 1 ? static_cast<size_t>(m.groups) * m.splits * m.rows * kMSlotFloats * sizeof(float) : 0;
+    m.part_bytes = static_cast<size_t>(kT8CtasPerSm) * sms * 2 * kT8SlotFloats * sizeof(float);
     return m;
 }
 
@@ -3142,7 +3135,7 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
     if (rc != DA_OK) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     const MultiPlan m = multi_fp8_plan(s, T, window, max_seq_len, sm_count(dev));
-    if (static_cast<long long>(m.splits) * m.row_blocks > 0x7fffffffLL || m.groups > kMMaxGroups) return DA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(s.batch) * m.row_blocks > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
     void *ws = nullptr;
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -3189,20 +3182,16 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
     prm.num_pages = num_pages;
     prm.max_seq_len = max_seq_len;
     prm.row_blocks = m.row_blocks;
-    prm.splits = m.splits;
-    prm.chunk = m.chunk;
     prm.counters = static_cast<int *>(ws);
     prm.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
     prm.defer = m.defer ? 1 : 0;
-    rc = launch_pdl(multi_tc8_kernel,
-                    dim3(static_cast<unsigned>(m.splits * m.row_blocks), static_cast<unsigned>(s.num_kv_heads),
-                         static_cast<unsigned>(s.batch)),
-                    kT8Threads, kT8Smem, stream, prm, static_cast<const uint8_t *>(kv_cache));
+    const unsigned grid = static_cast<unsigned>(kT8CtasPerSm * sm_count(dev));
+    rc = launch_pdl(multi_tc8_kernel, dim3(grid), kT8Threads, kT8Smem, stream, prm, static_cast<const uint8_t *>(kv_cache));
     if (rc != DA_OK || !m.defer) return rc;
-    return launch_pdl(multi_combine_kernel<true>,
-                      dim3(static_cast<unsigned>(m.row_blocks * ((m.rows + kCombWarps - 1) / kCombWarps)),
-                           static_cast<unsigned>(s.num_kv_heads), static_cast<unsigned>(s.batch)),
-                      kCombWarps * 32, 0, stream, prm, m.rows, 0);
+    return launch_pdl(t8_combine_kernel,
+                      dim3(static_cast<unsigned>(m.row_blocks * (kT8Rows / kT8FoldWarps)), static_cast<unsigned>(s.num_kv_heads),
+                           static_cast<unsigned>(s.batch)),
+                      kT8FoldWarps * 32, 0, stream, prm, static_cast<int>(grid));
 }
 
 // ------------------------------------------------------------------ accumulated weights: host side
@@ -3878,7 +3867,7 @@ size_t decode_attn_paged_fp8_multi_workspace_bytes(da_shape s, int q_tokens, int
         current_device(&dev) != DA_OK)
         return 0;
     const MultiPlan m = multi_fp8_plan(s, q_tokens, window, max_seq_len, sm_count(dev));
-    return m.groups > kMMaxGroups ? 0 : m.counter_bytes + m.part_bytes;
+    return m.counter_bytes + m.part_bytes;
 }
 
 int decode_attn_paged_multi(const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,

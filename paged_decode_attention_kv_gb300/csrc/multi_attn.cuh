@@ -120,29 +120,6 @@ __device__ __forceinline__ MultiKeys multi_keys(const MultiParams &p, bool ring,
     return k;
 }
 
-// multi_keys for calls whose new tokens are in the cache: the tiles pt_lo .. pt_lo + ntiles - 1, of
-// which positions below the first row's window start and past the last row's are not keys.
-__device__ __forceinline__ MultiKeys multi_keys_cached(const MultiParams &p, int b, int r0, int r_end, int &lo, int &end) {
-    MultiKeys k;
-    k.L = __ldg(p.seq_lens + b);
-    k.n = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
-    k.bad = k.L < 0 || k.n < 0 || k.n > p.T || (k.L > 0 && k.n > k.L) || k.L > p.max_seq_len ||
-            k.L > static_cast<long long>(p.max_pages) * kPage;
-    if (k.bad) k.L = 0;
-    if (k.L == 0) k.n = 0;
-    k.base = k.L - k.n;
-    k.ncache = k.pt_lo = k.nvalid = k.nt_base = k.ntiles = k.ring_off = 0;
-    lo = end = 0;
-    const int t0 = r0 / p.G, t1 = min(k.n - 1, (r_end - 1) / p.G);
-    if (t1 >= t0) {
-        lo = p.window > 0 ? max(0, k.base + t0 - p.window + 1) : 0;
-        end = k.base + t1 + 1;
-        k.pt_lo = lo / kPage;
-        k.ncache = k.ntiles = (end - 1) / kPage - k.pt_lo + 1;
-    }
-    return k;
-}
-
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
                                             int c3, uint32_t bar, uint64_t policy) {
     asm volatile(
@@ -612,9 +589,7 @@ __global__ void __launch_bounds__(NW * 32, MultiShape<NW>::kMinBlocks)
 // lanes' maxima and sums, then each lane adds up its splits' weighted accumulators (64
 // values) and the warp sums them over the lanes through shared memory (a padded 32 x 64
 // transpose), so a row costs about three dependent L2 round trips however many splits.
-// CACHED: the new tokens are keys in the cache (multi_keys_cached).
 constexpr int kCombWarps = 4;  // query rows per CTA
-template <bool CACHED>
 __global__ void __launch_bounds__(kCombWarps * 32) multi_combine_kernel(const MultiParams p, int RB, int ring) {
     __shared__ float s_sum[kCombWarps][32][kD + 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the attention kernel
@@ -624,8 +599,7 @@ __global__ void __launch_bounds__(kCombWarps * 32) multi_combine_kernel(const Mu
     const int g = blockIdx.y, b = blockIdx.z;
     const int r0 = rb * RB, r_end = min(r0 + RB, p.T * p.G);
     if (r0 + sl * kCombWarps >= r_end) return;
-    int lo, end;
-    const MultiKeys k = CACHED ? multi_keys_cached(p, b, r0, r_end, lo, end) : multi_keys(p, ring != 0, b, r0, r_end);
+    const MultiKeys k = multi_keys(p, ring != 0, b, r0, r_end);
     const int nsplit = (k.ntiles + p.chunk - 1) / p.chunk;
     if (nsplit <= 1) return;  // the attention kernel wrote these rows (or their zeros)
     const int rl = sl * kCombWarps + warp;  // this warp's row of the block

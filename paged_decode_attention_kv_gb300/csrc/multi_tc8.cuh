@@ -5,9 +5,10 @@
 //
 // The codes are turned into fp16 operands in shared memory, their token's scale with them. A page
 // (16 tokens) has a power of two 2^E at least as large as its K scales, 2^F for its V scales, and
-//     K'_j = fp16(code_j ks_j 2^-E),   V'_j = fp16(code_j vs_j 2^-F):
-// code times a factor in (0, 1], rounded once (2^-12 of the element, or of 2^-13 of the page's largest
-// factor), nothing to overflow. 2^E goes into the page's score multiplier; 2^F into the exponent of
+//     K'_j = fp16(code_j ks_j 2^-E),   V'_j = fp16(code_j fp16(vs_j 2^-F)):
+// code times a factor in (0, 1], nothing to overflow. K' is rounded once (its factor is carried as two
+// fp16 values: an error of the factor would move all of a token's score), V' twice, each time by at most
+// fp16's half step 2^-11. 2^E goes into the page's score multiplier; 2^F into the exponent of
 // its probabilities, so that the output accumulates in one unit:
 //     s_j + F = (q K'_j) (scale log2(e) 2^E) + F,   P_j = fp16(2^(s_j + F - R + 7)),
 //     O = sum P_j V'_j = 2^(7-R) sum 2^(s_j) v_j,   l = sum over pages 2^-F sum P_j = 2^(7-R) sum 2^(s_j)
@@ -18,32 +19,55 @@
 // lane and key, more than the whole softmax takes. Scales beyond 2^100 (K) or outside 2^-60 ..
 // 2^60 (V) lose bits.
 //
-// One CTA per (sequence, KV head, block of 128 query rows, key split); 9 warps:
-//   warps 0-3  one query row per thread (TMEM lane = row): the softmax and the finish
-//   warps 4-7  warp 4 + u copies tile u of every 64-key block (one 2176-byte block, a bulk copy
-//              into its own ring of raw blocks) and writes its K' and V' into the stage
-//   warp 8     issues the MMAs: S_j = Q K'_j^T and O += P_j V'_j (V' as it is stored, transposed:
-//              tokens contiguous, so both operands are K-major)
+// The work is cut on the device: a unit is a block of 64 keys of a segment (sequence, KV head, block of
+// 128 query rows), and every CTA of the grid (two per SM) takes the same number of consecutive units,
+// whatever the lengths. A segment that lies in one CTA is finished there; one that is shared leaves fp32
+// partials (m, l, O per row; two slots per CTA), folded by the CTA that comes last, or, where the host
+// sees that a few segments fill the whole grid, by t8_combine_kernel. With a grid of (segment, key split)
+// CTAs cut for the longest sequence instead, 64 sequences of 1024 to 8192 tokens took 248 us.
+//
+// 16 warps stream through the CTA's units without a break between segments:
+//   warps 0-3   one query row per thread (TMEM lane = row): the softmax and the finish, and the next
+//               segment's query rows as fp16 into the other of two Q buffers
+//   warps 4-11  two teams of four that take turns: warp u of a team turns tile u of its unit into K' and V'
+//   warp 12     issues the MMAs: S_i = Q K'_i^T and O += P_i V'_i (V' as it is stored, transposed:
+//               tokens contiguous, so both operands are K-major)
+//   warp 13     copies the units' fp8 blocks (2176 bytes each, one bulk copy), lane u tile u
+// Two teams because one is a chain of latencies (copy landed, scales' maximum, factors, operands) of about
+// 2400 cycles a unit. Registers go where they are needed (setmaxnreg): 64 a thread at launch, then 104 for
+// the rows, 56 for the teams, 40 for the last four warps, 4 x 64 in all.
+// The softmax takes the probabilities with the reference it has, and looks for a larger one only if a
+// tile's sum shows that one may have left fp16's range (or the row has no reference yet): the scores then
+// still stand in TMEM (P has its own columns) and are taken again. The maxima of every unit cost 40 of
+// 230 instructions, and holding 64 scores in registers for them 84 bytes of spills.
 constexpr int kT8Rows = 128, kT8Keys = 64, kT8Tiles = kT8Keys / kPage;
 #ifndef DA_T8_STAGES
 #define DA_T8_STAGES 3
 #endif
 #ifndef DA_T8_RAW
-#define DA_T8_RAW 4
+#define DA_T8_RAW 2
 #endif
 constexpr int kT8Stages = DA_T8_STAGES;  // blocks of K' and V'
-constexpr int kT8Raw = DA_T8_RAW;        // fp8 blocks in flight per copying warp
-constexpr int kT8SBufs = 2;
+constexpr int kT8Raw = DA_T8_RAW;        // units of fp8 blocks in flight
+// An even number: every raw block is always the same team's. With three, a team could wait for its unit's
+// parity on a barrier whose last unit, the other team's, had not landed yet, and take the phase before for its own.
+// (The stages are safe with any number: a team's unit i - 2 has seen PV_{i-5} done, so that the phase before the one
+// it waits for, PV_{i-6}'s, is over.)
+static_assert(kT8Raw % 2 == 0, "a raw block belongs to one team");
 constexpr int kT8HalfBytes = kT8Keys * kD * 2;  // 8 KiB of K' (or V')
 constexpr int kT8StageBytes = 2 * kT8HalfBytes;
 constexpr int kT8QBytes = kT8Rows * kD * 2;
 constexpr int kT8RawBytes = kT8Tiles * kT8Raw * kBlk8Bytes;
-constexpr int kT8Bars = kT8Tiles * kT8Raw + 2 * kT8Stages + 3 * kT8SBufs + 1;
-constexpr int kT8Smem = 1024 + kT8QBytes + kT8Stages * kT8StageBytes + kT8RawBytes + kT8Stages * kT8Tiles * 16 + kT8Bars * 8;
-constexpr int kT8Warps = 9, kT8Threads = kT8Warps * 32;
-constexpr uint32_t kT8TmemCols = 256, kT8ColS = 0, kT8ColO = 64 * kT8SBufs;
-constexpr float kT8Rescale = 8.f, kT8Shift = 7.f;  // log2: a row's reference may be exceeded by; the probabilities' unit
+constexpr int kT8Bars = 2 * kT8Raw + 2 * kT8Stages + 4 * 2 + 1;
+constexpr int kT8Smem = 1024 + 2 * kT8QBytes + kT8Stages * kT8StageBytes + kT8RawBytes + kT8Stages * kT8Tiles * 16 + kT8Bars * 8;
+constexpr int kT8Warps = 16, kT8Threads = kT8Warps * 32, kT8CtasPerSm = 2;
+static_assert(kT8CtasPerSm * (kT8Smem + 1024 + 1024) <= 233472, "two CTAs' shared memory on one SM");
+static_assert((kMaxBatch + 1) * 8 <= kT8Stages * kT8StageBytes, "the prefix of units fits the stages");
+constexpr uint32_t kT8TmemCols = 256, kT8ColS = 0, kT8ColO = 128, kT8ColP = 192;  // S and P: two buffers each
+constexpr float kT8Shift = 7.f, kT8TileMax = 32768.f;  // log2 of the probabilities' unit; the most a tile's may add up to
 constexpr int kT8MaxE = 100, kT8MaxF = 60;
+constexpr int kT8MinUnits = 4;                         // units per CTA at least, where there are so few
+constexpr size_t kT8SlotFloats = static_cast<size_t>(kT8Rows) * kMSlotFloats;
 
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -60,184 +84,366 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 
-__global__ void __launch_bounds__(kT8Threads, 2)
+// A sequence's counts (n = 0: nothing to do), and its row blocks with queries: the first `blocks`.
+struct T8Seq {
+    int L, n, blocks;
+    bool bad;
+};
+__device__ __forceinline__ T8Seq t8_seq(const MultiParams &p, int b) {
+    T8Seq s;
+    s.L = __ldg(p.seq_lens + b);
+    s.n = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
+    s.bad = s.L < 0 || s.n < 0 || s.n > p.T || (s.L > 0 && s.n > s.L) || s.L > p.max_seq_len ||
+            s.L > static_cast<long long>(p.max_pages) * kPage;
+    if (s.bad || s.L == 0) s.L = s.n = 0;
+    s.blocks = (s.n * p.G + kT8Rows - 1) / kT8Rows;
+    return s;
+}
+// The keys [lo, end) of row block rb of a sequence, its first tile and its units.
+struct T8Keys {
+    int lo, end, pt_lo, ntiles, units;
+};
+__device__ __forceinline__ T8Keys t8_keys(const MultiParams &p, const T8Seq &s, int rb) {
+    T8Keys k;
+    const int base = s.L - s.n;
+    const int t0 = rb * kT8Rows / p.G, t1 = min(s.n - 1, (rb * kT8Rows + kT8Rows - 1) / p.G);
+    k.lo = p.window > 0 ? max(0, base + t0 - p.window + 1) : 0;
+    k.end = base + t1 + 1;
+    k.pt_lo = k.lo / kPage;
+    k.ntiles = (k.end - 1) / kPage - k.pt_lo + 1;
+    k.units = (k.ntiles + kT8Tiles - 1) / kT8Tiles;
+    return k;
+}
+// The units of one KV head of sequence b, added up by a warp.
+__device__ __forceinline__ long long t8_units(const MultiParams &p, int b, int lane) {
+    const T8Seq s = t8_seq(p, b);
+    long long sum = 0;
+    for (int rb = lane; rb < s.blocks; rb += 32) sum += t8_keys(p, s, rb).units;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    return sum;
+}
+
+// Exclusive prefix over the sequences of their units (all KV heads) into pre[0 .. B], by all threads of the CTA.
+__device__ __forceinline__ void t8_prefix(const MultiParams &p, long long *pre, int warp, int nwarps, int lane) {
+    const int tid = warp * 32 + lane;
+    if (p.row_blocks <= 4) {  // a thread per sequence
+        for (int b = tid; b < p.B; b += nwarps * 32) {
+            const T8Seq s = t8_seq(p, b);
+            long long sum = 0;
+            for (int rb = 0; rb < s.blocks; ++rb) sum += t8_keys(p, s, rb).units;
+            pre[b + 1] = sum * p.Hkv;
+        }
+    } else {
+        for (int b = warp; b < p.B; b += nwarps) {
+            const long long sum = t8_units(p, b, lane);
+            if (lane == 0) pre[b + 1] = sum * p.Hkv;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long run = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            long long x = b < p.B ? pre[b + 1] : 0;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off) x += y;
+            }
+            if (b < p.B) pre[b + 1] = run + x;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) pre[0] = 0;
+    }
+    __syncthreads();
+}
+
+// CTA c of nc takes the units [c U / nc, (c + 1) U / nc); the CTA that holds unit x.
+__device__ __forceinline__ long long t8_first(long long U, int nc, int c) { return c * U / nc; }
+__device__ __forceinline__ int t8_owner(long long U, int nc, long long x) { return static_cast<int>(((x + 1) * nc - 1) / U); }
+__device__ __forceinline__ int t8_ctas(long long U, int grid) {
+    return static_cast<int>(max(1ll, min(static_cast<long long>(grid), (U + kT8MinUnits - 1) / kT8MinUnits)));
+}
+
+// A walk over a CTA's units, segment by segment: the segment's place and keys, and the units [u0, u1)
+// of it that are the CTA's.
+struct T8Walk {
+    int b, g, rb, u0, u1;
+    long long left;  // the CTA's units after this segment
+    T8Seq seq;
+    T8Keys keys;
+    __device__ __forceinline__ void cut() {
+        u1 = static_cast<int>(min(static_cast<long long>(keys.units), u0 + left));
+        left -= u1 - u0;
+    }
+    __device__ __forceinline__ void start(const MultiParams &p, const int4 &at, long long units) {
+        b = at.x, g = at.y, rb = at.z, u0 = at.w, left = units;
+        seq = t8_seq(p, b);
+        keys = t8_keys(p, seq, rb);
+        cut();
+    }
+    __device__ __forceinline__ bool next(const MultiParams &p) {  // false: that was the last one
+        if (left <= 0) return false;
+        if (++rb >= seq.blocks) {
+            rb = 0;
+            if (++g >= p.Hkv) {
+                g = 0;
+                do seq = t8_seq(p, ++b);
+                while (seq.blocks == 0);
+            }
+        }
+        keys = t8_keys(p, seq, rb);
+        u0 = 0;
+        cut();
+        return true;
+    }
+};
+
+// Row rl of a segment's partials: contributor i of `count`, the first one in its CTA's slot k0, the others in slot 0.
+__device__ __forceinline__ const float *t8_slot(const MultiParams &p, int c0, int k0, int i, int rl) {
+    return p.part + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? k0 : 0)) * kT8SlotFloats + static_cast<size_t>(rl) * kMSlotFloats;
+}
+
+// One row's partials folded with the sink by a warp; every lane returns output elements 2 lane, 2 lane + 1.
+__device__ __forceinline__ uint32_t t8_fold_row(const MultiParams &p, int c0, int k0, int count, int rl, int head, int lane) {
+    float M = -INFINITY, den = 0.f;
+    for (int i = lane; i < count; i += 32) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(t8_slot(p, c0, k0, i, rl)));
+        if (ml.x == -INFINITY) continue;  // no key of the row there
+        const float Mn = fmaxf(M, ml.x);
+        den = den * exp2f(M - Mn) + ml.y * exp2f(ml.x - Mn);
+        M = Mn;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float Mo = __shfl_xor_sync(0xffffffffu, M, off), Do = __shfl_xor_sync(0xffffffffu, den, off);
+        const float Mn = fmaxf(M, Mo);
+        den = Mn == -INFINITY ? 0.f : den * exp2f(M - Mn) + Do * exp2f(Mo - Mn);
+        M = Mn;
+    }
+    const float sg = p.sinks != nullptr ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
+    const float Mf = fmaxf(M, sg);  // the same on every lane: an exact maximum
+    if (Mf == -INFINITY) return 0u;
+    const float d = den * exp2f(M - Mf) + (sg == -INFINITY ? 0.f : exp2f(sg - Mf));
+    const float inv = d > 0.f ? 1.f / d : d == d ? 0.f : d;
+    float x0 = 0.f, x1 = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {  // independent loads: several in flight
+        const float *s = t8_slot(p, c0, k0, i, rl);
+        const float m = __ldcg(s);
+        const float2 a = __ldcg(reinterpret_cast<const float2 *>(s + kMAccOff) + lane);
+        const float w = m == -INFINITY ? 0.f : exp2f(m - Mf);
+        x0 += a.x * w;
+        x1 += a.y * w;
+    }
+    return pack_bf16(x0 * inv, x1 * inv);
+}
+
+// The same by one thread, 16 bytes at a time: for the CTA that folds 128 rows of a few partials at once (a warp a row
+// leaves a chain of dependent loads for each of a warp's 32 rows).
+__device__ __noinline__ void t8_fold_thread(const MultiParams &p, int c0, int k0, int count, int rl, int head, bool query, uint4 *out) {
+    float M = -INFINITY;
+    if (query)
+        for (int i = 0; i < count; ++i) M = fmaxf(M, __ldcg(t8_slot(p, c0, k0, i, rl)));
+    const float sg = query && p.sinks != nullptr ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
+    const float Mf = fmaxf(M, sg);
+    float d = sg == -INFINITY ? 0.f : exp2f(sg - Mf);
+    if (Mf != -INFINITY)
+        for (int i = 0; i < count; ++i) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(t8_slot(p, c0, k0, i, rl)));
+            if (ml.x != -INFINITY) d += ml.y * exp2f(ml.x - Mf);
+        }
+    const float inv = d > 0.f ? 1.f / d : d == d ? 0.f : d;
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+        float4 o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (Mf != -INFINITY)
+            for (int i = 0; i < count; ++i) {
+                const float *s = t8_slot(p, c0, k0, i, rl);
+                const float m = __ldcg(s);
+                const float4 *acc = reinterpret_cast<const float4 *>(s + kMAccOff) + 4 * h;
+                const float w = m == -INFINITY ? 0.f : exp2f(m - Mf);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 x = __ldcg(acc + c);
+                    o[c].x += x.x * w, o[c].y += x.y * w, o[c].z += x.z * w, o[c].w += x.w * w;
+                }
+            }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            out[2 * h + c] = make_uint4(pack_bf16(o[2 * c].x * inv, o[2 * c].y * inv), pack_bf16(o[2 * c].z * inv, o[2 * c].w * inv),
+                                        pack_bf16(o[2 * c + 1].x * inv, o[2 * c + 1].y * inv), pack_bf16(o[2 * c + 1].z * inv, o[2 * c + 1].w * inv));
+    }
+}
+
+__global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
     multi_tc8_kernel(const MultiParams p, const uint8_t *__restrict__ kv) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sQ = smem;                    // [128 rows][128 B], 128-byte swizzle
-    uint8_t *sKV = smem + kT8QBytes;       // [stage][K' block [64 tokens][128 B] | V' block [64 d][128 B]]
-    uint8_t *sRaw = sKV + kT8Stages * kT8StageBytes;  // [tile][kT8Raw][2176]
-    float4 *s_fac = reinterpret_cast<float4 *>(sRaw + kT8RawBytes);  // [stage][tile]: multiplier, F, 2^-F
+    uint8_t *sQ = smem;                        // [2][128 rows][128 B], 128-byte swizzle
+    uint8_t *sKV = smem + 2 * kT8QBytes;       // [stage][K' block [64 tokens][128 B] | V' block [64 d][128 B]]
+    uint8_t *sRaw = sKV + kT8Stages * kT8StageBytes;  // [kT8Raw][tile][2176]
+    float4 *s_fac = reinterpret_cast<float4 *>(sRaw + kT8RawBytes);  // [stage][tile]: multiplier, F, 2^-F, bits: the unit is a segment's first
     uint64_t *bars = reinterpret_cast<uint64_t *>(s_fac + kT8Stages * kT8Tiles);
-    const uint32_t raw_full = smem_addr(bars);  // [tile][kT8Raw]
-    const uint32_t kv_full = raw_full + 8 * kT8Tiles * kT8Raw, kv_empty = kv_full + 8 * kT8Stages;
-    const uint32_t s_full = kv_empty + 8 * kT8Stages, p_full = s_full + 8 * kT8SBufs;
-    const uint32_t o_done = p_full + 8 * kT8SBufs, drain = o_done + 8 * kT8SBufs;
-    __shared__ int s_page[kMMaxChunk];
-    __shared__ __align__(16) uint32_t s_vfac[kT8Tiles][kPage];  // V factors: 16 high halves, then 16 low ones
+    const uint32_t raw_full = smem_addr(bars), raw_empty = raw_full + 8 * kT8Raw;
+    const uint32_t kv_full = raw_empty + 8 * kT8Raw, kv_empty = kv_full + 8 * kT8Stages;
+    const uint32_t s_full = kv_empty + 8 * kT8Stages, p_full = s_full + 16, o_done = p_full + 16;
+    const uint32_t q_full = o_done + 16, drain = q_full + 16;
+    __shared__ __align__(16) uint32_t s_vfac[2 * kT8Tiles][kPage / 2];  // V factors of a tile: 16 fp16 values
+    // a raw tile's tokens that are keys: [x & 255, x >> 8 & 255), none where there is no page; bit 16: its unit is the
+    // segment's first here
+    __shared__ int s_keys[kT8Raw][kT8Tiles];
+    __shared__ T8Walk s_walk[4][2];  // a row warp's segment and its next one, out of the registers' way
+    __shared__ long long s_begin[4];
+    __shared__ int4 s_start;
+    __shared__ long long s_range[3];  // the CTA's first unit, its units, all units
     __shared__ uint32_t s_tmem;
-    __shared__ int s_ticket;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-    const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits;
-    const int g = blockIdx.y, b = blockIdx.z;
-
     if (tid == 0) {
-        for (int s = 0; s < kT8Tiles * kT8Raw; ++s) mbar_init(raw_full + 8 * s, 1);
+        for (int s = 0; s < kT8Raw; ++s) {
+            mbar_init(raw_full + 8 * s, 1);
+            mbar_init(raw_empty + 8 * s, kT8Tiles);
+        }
         for (int s = 0; s < kT8Stages; ++s) {
             mbar_init(kv_full + 8 * s, kT8Tiles);
             mbar_init(kv_empty + 8 * s, 1);
         }
-        for (int s = 0; s < kT8SBufs; ++s) {
-            mbar_init(s_full + 8 * s, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(s_full + 8 * s, 2);  // the products, and the issuing thread
             mbar_init(p_full + 8 * s, 4);  // the four row warps
             mbar_init(o_done + 8 * s, 1);
+            mbar_init(q_full + 8 * s, 4);
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    const int W = p.window;
-    const int r0 = rb * kT8Rows;
-    const int r_end = min(r0 + kT8Rows, p.T * p.G);
-    int key_lo, key_end;
-    const MultiKeys keys = multi_keys_cached(p, b, r0, r_end, key_lo, key_end);
-    if (keys.bad && tid == 0 && g == 0 && blockIdx.x == 0) flag_status(DA_STATUS_BAD_SEQ_LEN);
-    const int n = keys.n, base = keys.base, pt_lo = keys.pt_lo, ntiles = keys.ntiles;
-    const int kb = split * p.chunk;
-    const int ke = min(kb + p.chunk, ntiles);
-    const int nsplit = (ntiles + p.chunk - 1) / p.chunk;
-    const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
-    auto row_off = [&](int r) {
-        const int t = r / p.G, hl = r - t * p.G;
-        return ((static_cast<size_t>(b) * p.T + t) * p.Hq + g * p.G + hl) * kD;
-    };
-    if (kb >= ke) {
-        if (ntiles == 0 && split == 0)
-            for (int i = tid; i < (r_end - r0) * (kD / 8); i += blockDim.x)
-                *reinterpret_cast<uint4 *>(p.out + row_off(r0 + i / (kD / 8)) + (i % (kD / 8)) * 8) =
-                    make_uint4(0, 0, 0, 0);
-        return;
-    }
-    const int cnt = ke - kb;
-    const int nblk = (cnt + kT8Tiles - 1) / kT8Tiles;
-    const int r_valid = min(r_end, r0 + max(0, n * p.G - r0));  // rows r0 .. r_valid-1 are queries
-
-    // ---- page indices, query rows as fp16 (zero past the valid ones), TMEM
-    for (int i = tid; i < cnt; i += blockDim.x) {
-        int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + pt_lo + kb + i);
-        if (page < 0 || page >= p.num_pages) {
-            flag_status(DA_STATUS_BAD_PAGE);
-            page = -1;  // its tokens read as zeros
-        }
-        s_page[i] = page;
-    }
-    if (warp < 4) {
-        const int r = r0 + tid;
-        const bool ok = r < r_valid;
-        const uint4 *src = ok ? reinterpret_cast<const uint4 *>(p.q + row_off(r)) : nullptr;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            uint4 v = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
-            *reinterpret_cast<uint4 *>(sQ + tid * 128 + ((c ^ (tid & 7)) << 4)) = v;
-        }
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q is read by the tensor cores
-    if (warp == 0) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
                      "r"(kT8TmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- the CTA's units; the output rows that have no query: zeros
+    long long *pre = reinterpret_cast<long long *>(sKV);
+    t8_prefix(p, pre, warp, kT8Warps, lane);
+    const long long U = pre[p.B];
+    const int nc = t8_ctas(U, gridDim.x), cta = blockIdx.x;
+    if (warp == 0) {
+        const long long first = cta < nc ? t8_first(U, nc, cta) : U, units = (cta < nc ? t8_first(U, nc, cta + 1) : U) - first;
+        if (units > 0) {
+            int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before it
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] <= first) lo = mid;
+                else hi = mid - 1;
+            }
+            const T8Seq s = t8_seq(p, lo);
+            const long long per = (pre[lo + 1] - pre[lo]) / p.Hkv;
+            const int g = static_cast<int>((first - pre[lo]) / per);
+            long long x = first - pre[lo] - g * per;
+            int rb = 0;
+            for (int r0 = 0; r0 < s.blocks; r0 += 32) {  // 32 row blocks at a time
+                const int u = r0 + lane < s.blocks ? t8_keys(p, s, r0 + lane).units : 0;
+                int sum = u;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, sum, off);
+                    if (lane >= off) sum += y;
+                }
+                const uint32_t in = __ballot_sync(0xffffffffu, x < sum);
+                if (in != 0) {
+                    const int at = __ffs(static_cast<int>(in)) - 1;
+                    x -= __shfl_sync(0xffffffffu, sum - u, at);
+                    rb = r0 + at;
+                    break;
+                }
+                x -= __shfl_sync(0xffffffffu, sum, 31);
+            }
+            if (lane == 0) s_start = make_int4(lo, g, rb, static_cast<int>(x));
+        }
+        if (lane == 0) {
+            s_range[0] = first;
+            s_range[1] = units;
+            s_range[2] = U;
+        }
+    }
+    for (int i = cta; i < p.B * p.row_blocks; i += gridDim.x) {
+        const int b = i / p.row_blocks, rb = i - b * p.row_blocks;
+        const T8Seq s = t8_seq(p, b);
+        if (s.bad && rb == 0 && tid == 0) flag_status(DA_STATUS_BAD_SEQ_LEN);
+        if (rb < s.blocks) continue;
+        const int r0 = rb * kT8Rows, rows = min(kT8Rows, p.T * p.G - r0);
+        for (int j = tid; j < rows * p.Hkv * (kD / 8); j += kT8Threads) {
+            const int c = j & 7, r = r0 + (j >> 3) % rows, g = (j >> 3) / rows, t = r / p.G;
+            reinterpret_cast<uint4 *>(p.out + ((static_cast<size_t>(b) * p.T + t) * p.Hq + g * p.G + (r - t * p.G)) * kD)[c] =
+                make_uint4(0, 0, 0, 0);
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the stages held the prefix
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tmem;
+    const int units = static_cast<int>(s_range[1]);
 
     bool failed = false;
-    if (warp >= 4 && warp < 8) {
-        // ---- copies and operands: tile u of every block
-        const int u = warp - 4;
-        uint8_t *raw = sRaw + u * kT8Raw * kBlk8Bytes;
-        const uint32_t full0 = raw_full + 8 * u * kT8Raw;
-        const uint64_t policy = evict_first_policy();
-        const int mine = cnt > u ? (cnt - u + kT8Tiles - 1) / kT8Tiles : 0;  // blocks whose tile u exists
-        auto issue = [&](int j) {  // (lane 0)
-            const int page = s_page[j * kT8Tiles + u], s = j % kT8Raw;
-            const uint32_t bar = full0 + 8 * s;
-            if (page < 0) {  // nothing to copy: the phase completes by itself
-                mbar_arrive(bar);
-                return;
+    if (warp >= 4 && warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // ---- operands: tile u of every other unit
+        const int u = warp & 3, team = (warp - 4) >> 2;
+        unsigned short *const vfac = reinterpret_cast<unsigned short *>(s_vfac[warp - 4]);
+        int st = team % kT8Stages, rs = team % kT8Raw;
+        uint32_t st_ph = 1, rs_ph = 0;  // (the first round of stages is free)
+        for (int i = team; i < units; i += 2) {
+            if (__any_sync(0xffffffffu, !mbar_wait_bounded(raw_full + 8 * rs, rs_ph))) {
+                failed = true;
+                break;
             }
-            mbar_expect_tx(bar, kBlk8Bytes);
-            const uint8_t *src = kv + (static_cast<size_t>(page) * p.Hkv + g) * kBlk8Bytes;
-            if (p.row_blocks == 1)
-                bulk_load_hint(smem_addr(raw + s * kBlk8Bytes), src, kBlk8Bytes, bar, policy);
-            else  // other row blocks read it too
-                bulk_load(smem_addr(raw + s * kBlk8Bytes), src, kBlk8Bytes, bar);
-        };
-        int issued = 0;
-        if (lane == 0)
-            for (; issued < mine && issued < kT8Raw; ++issued) issue(issued);
-        for (int j = 0; j < nblk; ++j) {
-            const int st = j % kT8Stages;
+            const uint8_t *blk = sRaw + (rs * kT8Tiles + u) * kBlk8Bytes;
+            const int keys = s_keys[rs][u], key_a = keys & 255, key_e = keys >> 8 & 255;
+            float sc = reinterpret_cast<const float *>(blk + kBlk8S)[lane];
             uint4 kc[2], vc[2];
-            float sc = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-            if (j < mine) {
-                if (__any_sync(0xffffffffu, !mbar_wait_bounded(full0 + 8 * (j % kT8Raw), (j / kT8Raw) & 1))) {
-                    failed = true;
-                    break;
-                }
-                const int k = j * kT8Tiles + u;
-                if (s_page[k] >= 0) {
-                    const uint8_t *blk = raw + (j % kT8Raw) * kBlk8Bytes;
-                    const int pos0 = (pt_lo + kb + k) * kPage;
-                    // a token outside the rows' keys may hold anything: its codes and scales are zeros
-                    auto key = [&](int t) { return pos0 + t >= key_lo && pos0 + t < key_end; };
-                    if (key(lane & 15)) sc = reinterpret_cast<const float *>(blk + kBlk8S)[lane];
+            for (int h = 0; h < 2; ++h) {
+                kc[h] = reinterpret_cast<const uint4 *>(blk)[lane + 32 * h];
+                vc[h] = reinterpret_cast<const uint4 *>(blk + kBlk8V)[lane + 32 * h];
+            }
+            if ((keys & 0xffff) != kPage << 8) {
+                // a token outside the rows' keys may hold anything: its codes and scales are zeros
+                auto key = [&](int t) { return t >= key_a && t < key_e; };
+                if (!key(lane & 15)) sc = 0.f;
+                uint32_t m[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (key((lane >> 2) + 8 * i)) kc[i] = reinterpret_cast<const uint4 *>(blk)[lane + 32 * i];
-                        vc[i] = reinterpret_cast<const uint4 *>(blk + kBlk8V)[lane + 32 * i];
-                    }
-                    if (pos0 < key_lo || pos0 + kPage > key_end) {  // (V rows hold the 16 tokens' bytes)
-                        uint32_t m[4];
+                for (int e = 0; e < 4; ++e)
+                    m[e] = (key(4 * e) ? 0xffu : 0u) | (key(4 * e + 1) ? 0xff00u : 0u) |
+                           (key(4 * e + 2) ? 0xff0000u : 0u) | (key(4 * e + 3) ? 0xff000000u : 0u);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            m[e] = (key(4 * e) ? 0xffu : 0u) | (key(4 * e + 1) ? 0xff00u : 0u) |
-                                   (key(4 * e + 2) ? 0xff0000u : 0u) | (key(4 * e + 3) ? 0xff000000u : 0u);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            vc[i] = make_uint4(vc[i].x & m[0], vc[i].y & m[1], vc[i].z & m[2], vc[i].w & m[3]);
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    if (!key((lane >> 2) + 8 * h)) kc[h] = make_uint4(0, 0, 0, 0);
+                    vc[h] = make_uint4(vc[h].x & m[0], vc[h].y & m[1], vc[h].z & m[2], vc[h].w & m[3]);
                 }
             }
-            // the page's powers of two, and each token's factor as two fp16 values (K: lanes 0-15, V: 16-31)
+            // the page's powers of two, and each token's factor (K: lanes 0-15, V: 16-31)
             float top = fabsf(sc);
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             const int lim = lane < 16 ? kT8MaxE : kT8MaxF;
             const int ex = max(-lim, min(lim, static_cast<int>(__float_as_uint(top) >> 23) - 126));
-            const float fac = sc * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            const float fac = sc * down;
             const __half hi = __float2half_rn(fac), lo = __float2half_rn(fac - __half2float(hi));
-            uint32_t packed = static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
-            __syncwarp();  // the raw block and the previous block's V factors have been read
-            if (lane >= 16) {
-                unsigned short *f = reinterpret_cast<unsigned short *>(s_vfac[u]);
-                f[lane - 16] = __half_as_ushort(hi);
-                f[lane] = __half_as_ushort(lo);
-            }
-            if (lane == 0 && issued < mine) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                issue(issued);
-                ++issued;
-            }
+            const uint32_t packed = static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
+            if (lane >= 16) vfac[lane - 16] = __half_as_ushort(hi);
             __syncwarp();
-            if (j >= kT8Stages && __any_sync(0xffffffffu, !mbar_wait_bounded(kv_empty + 8 * st, ((j / kT8Stages) - 1) & 1))) {
+            if (lane == 0) mbar_arrive(raw_empty + 8 * rs);  // the raw block has been read
+            const uint4 f0 = reinterpret_cast<const uint4 *>(vfac)[0], f1 = reinterpret_cast<const uint4 *>(vfac)[1];
+            const uint32_t vf[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+            if (__any_sync(0xffffffffu, !mbar_wait_bounded(kv_empty + 8 * st, st_ph))) {
                 failed = true;
                 break;
             }
@@ -245,257 +451,417 @@ __global__ void __launch_bounds__(kT8Threads, 2)
             if (lane == 0) fo[0] = fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23), 1.1754944e-38f);
             if (lane == 16) {
                 fo[1] = static_cast<float>(ex);
-                fo[2] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+                fo[2] = down;
+                fo[3] = __int_as_float(keys >> 16);
             }
             uint8_t *sK = sKV + st * kT8StageBytes, *sV = sK + kT8HalfBytes;
-            const uint4 *vf = reinterpret_cast<const uint4 *>(s_vfac[u]);
-            const uint4 f0 = vf[0], f1 = vf[1], f2 = vf[2], f3 = vf[3];
-            const uint32_t vh[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-            const uint32_t vl[8] = {f2.x, f2.y, f2.z, f2.w, f3.x, f3.y, f3.z, f3.w};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                {  // K: token (lane / 4) + 8 i, elements 16 (lane % 4) .. + 15
-                    const int t = (lane >> 2) + 8 * i, row = u * kPage + t;
+            for (int h = 0; h < 2; ++h) {
+                {  // K: token (lane / 4) + 8 h, elements 16 (lane % 4) .. + 15
+                    const int t = (lane >> 2) + 8 * h, row = u * kPage + t;
                     const uint32_t f = __shfl_sync(0xffffffffu, packed, t);
                     const uint32_t fh = __byte_perm(f, f, 0x1010), fl = __byte_perm(f, f, 0x3232);
-                    const uint32_t w[4] = {kc[i].x, kc[i].y, kc[i].z, kc[i].w};
-                    uint32_t o[8];
+                    const uint32_t x[4] = {kc[h].x, kc[h].y, kc[h].z, kc[h].w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t a, c;
-                        e4m3x4_to_f16x2x2(w[e], a, c);
-                        o[2 * e] = hfma2(a, fh, hmul2(a, fl));
-                        o[2 * e + 1] = hfma2(c, fh, hmul2(c, fl));
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t y, z;
+                            e4m3x4_to_f16x2x2(x[2 * e + k], y, z);
+                            o[2 * k] = hfma2(y, fh, hmul2(y, fl));
+                            o[2 * k + 1] = hfma2(z, fh, hmul2(z, fl));
+                        }
+                        *reinterpret_cast<uint4 *>(sK + row * 128 + (((2 * (lane & 3) + e) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<uint4 *>(sK + row * 128 + (((2 * (lane & 3) + h) ^ (row & 7)) << 4)) =
-                            make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
                 }
-                {  // V: element d = lane + 32 i, the tile's 16 tokens
-                    const int d = lane + 32 * i;
-                    const uint32_t w[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w};
-                    uint32_t o[8];
+                {  // V: element d = lane + 32 h, the tile's 16 tokens
+                    const int d = lane + 32 * h;
+                    const uint32_t x[4] = {vc[h].x, vc[h].y, vc[h].z, vc[h].w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t a, c;
-                        e4m3x4_to_f16x2x2(w[e], a, c);
-                        o[2 * e] = hfma2(a, vh[2 * e], hmul2(a, vl[2 * e]));
-                        o[2 * e + 1] = hfma2(c, vh[2 * e + 1], hmul2(c, vl[2 * e + 1]));
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t y, z;
+                            e4m3x4_to_f16x2x2(x[2 * e + k], y, z);
+                            o[2 * k] = hmul2(y, vf[4 * e + 2 * k]);
+                            o[2 * k + 1] = hmul2(z, vf[4 * e + 2 * k + 1]);
+                        }
+                        *reinterpret_cast<uint4 *>(sV + d * 128 + (((2 * u + e) ^ (d & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<uint4 *>(sV + d * 128 + (((2 * u + h) ^ (d & 7)) << 4)) =
-                            make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(kv_full + 8 * st);
+            if ((st += 2) >= kT8Stages) {
+                st -= kT8Stages;
+                st_ph ^= 1u;
+            }
+            if ((rs += 2) >= kT8Raw) {
+                rs -= kT8Raw;
+                rs_ph ^= 1u;
+            }
         }
-        if (lane == 0 && failed)  // nothing may still be landing when the CTA leaves
-            for (int j = max(0, issued - kT8Raw); j < issued; ++j) mbar_wait_idle(full0 + 8 * (j % kT8Raw), (j / kT8Raw) & 1);
-        __syncwarp();
-    } else if (warp == 8) {
-        // ---- MMA issuer: S_j = Q K'_j^T, then O += P_{j-1} V'_{j-1}
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 13 && units > 0) {
+            // ---- copies: lane u < 4 the block of tile u of every unit
+            const uint64_t policy = evict_first_policy();
+            T8Walk w;
+            w.start(p, s_start, units);
+            int wu = w.u0;
+            // the block-table entry of the next copy is read one copy early; -2: past the segment's tiles
+            auto page_of = [&]() {
+                const int k = wu * kT8Tiles + lane;
+                return lane < kT8Tiles && k < w.keys.ntiles ? __ldg(p.block_table + static_cast<size_t>(w.b) * p.max_pages + w.keys.pt_lo + k) : -2;
+            };
+            int page = page_of(), rs = 0;
+            uint32_t rs_ph = 1;  // (the first round is free)
+            int i = 0;
+            for (; i < units; ++i) {
+                if (__any_sync(0xffffffffu, !mbar_wait_idle(raw_empty + 8 * rs, rs_ph))) {
+                    failed = true;
+                    break;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the teams have read what was there
+                const bool there = page >= 0 && page < p.num_pages;
+                if (page != -2 && !there) flag_status(DA_STATUS_BAD_PAGE);  // its tokens read as zeros
+                if (lane < kT8Tiles) {
+                    const int pos0 = (w.keys.pt_lo + wu * kT8Tiles + lane) * kPage;
+                    s_keys[rs][lane] = (there ? max(0, w.keys.lo - pos0) | min(kPage, w.keys.end - pos0) << 8 : 0) | (wu == w.u0 ? 1 << 16 : 0);
+                }
+                const int copies = __popc(__ballot_sync(0xffffffffu, there));
+                __syncwarp();
+                const uint32_t bar = raw_full + 8 * rs;
+                if (lane == 0) mbar_expect_tx(bar, copies * kBlk8Bytes);
+                __syncwarp();
+                if (there) {
+                    const uint8_t *src = kv + (static_cast<size_t>(page) * p.Hkv + w.g) * kBlk8Bytes;
+                    const uint32_t dst = smem_addr(sRaw + (rs * kT8Tiles + lane) * kBlk8Bytes);
+                    if (p.row_blocks == 1)
+                        bulk_load_hint(dst, src, kBlk8Bytes, bar, policy);
+                    else  // other row blocks read it too
+                        bulk_load(dst, src, kBlk8Bytes, bar);
+                }
+                if (++wu >= w.u1 && i + 1 < units) {
+                    w.next(p);
+                    wu = w.u0;
+                }
+                page = page_of();
+                if (++rs == kT8Raw) {
+                    rs = 0;
+                    rs_ph ^= 1u;
+                }
+            }
+            // nothing may still be landing when the CTA leaves: the last copy of every raw block
+            for (int k = max(0, i - kT8Raw); k < i; ++k) mbar_wait_idle(raw_full + 8 * (k % kT8Raw), (k / kT8Raw) & 1);
+            __syncwarp();
+        } else if (warp == 12 && units > 0) {
+        // ---- MMA issuer: S_i = Q K'_i^T, then O += P_{i-1} V'_{i-1}
         const bool leader = elect_one();
         const uint32_t id_qk = umma_idesc_f16(kT8Rows, kT8Keys), id_pv = umma_idesc_f16(kT8Rows, kD);
         const uint64_t dq = umma_sdesc(smem_addr(sQ), 16, 1024), dk = umma_sdesc(smem_addr(sKV), 16, 1024);
         const uint64_t dv = umma_sdesc(smem_addr(sKV) + kT8HalfBytes, 16, 1024);
         auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity)); };
-        auto scores = [&](int j) {
-            const int s = j % kT8Stages, sb = j % kT8SBufs;
-            if (!wait_all(kv_full + 8 * s, (j / kT8Stages) & 1) ||
-                (j >= kT8SBufs && !wait_all(o_done + 8 * sb, ((j / kT8SBufs) - 1) & 1)))
-                return false;
-            tc_fence_after();
-            const uint64_t dks = dk + s * (kT8StageBytes / 16);
-            if (leader) {
+        int seg = -1;
+        bool fresh = false, fresh_before = false;  // unit i, i - 1 is its segment's first
+        for (int i = 0; i <= units && !failed; ++i) {
+            if (i < units) {
+                // (S_i's buffer was read before P_{i-2} arrived, which PV_{i-2} below waited for)
+                const int s = i % kT8Stages, sb = i & 1;
+                if (!wait_all(kv_full + 8 * s, (i / kT8Stages) & 1)) {
+                    failed = true;
+                    break;
+                }
+                fresh = __float_as_int(s_fac[s * kT8Tiles].w) != 0;
+                if (fresh) {
+                    ++seg;
+                    if (!wait_all(q_full + 8 * (seg & 1), (seg >> 1) & 1)) {
+                        failed = true;
+                        break;
+                    }
+                }
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t dqs = dq + (seg & 1) * (kT8QBytes / 16), dks = dk + s * (kT8StageBytes / 16);
 #pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk)
-                    umma_bf16_ss(tm + kT8ColS + 64 * sb, dq + 2 * kk, dks + 2 * kk, id_qk, kk > 0);
-                umma_commit(s_full + 8 * sb);
+                    for (int kk = 0; kk < kD / 16; ++kk)
+                        umma_bf16_ss(tm + kT8ColS + 64 * sb, dqs + 2 * kk, dks + 2 * kk, id_qk, kk > 0);
+                    umma_commit(s_full + 8 * sb);
+                    mbar_arrive(s_full + 8 * sb);  // the rows see what kv_full told this thread: the pages' factors
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        auto values = [&](int jj) {
-            const int s = jj % kT8Stages, pb = jj % kT8SBufs;
-            if (!wait_all(p_full + 8 * pb, (jj / kT8SBufs) & 1)) return false;
-            tc_fence_after();
-            const uint64_t dvs = dv + s * (kT8StageBytes / 16);
-            if (leader) {
+            if (i >= 1) {
+                const int j = i - 1, s = j % kT8Stages, pb = j & 1;
+                if (!wait_all(p_full + 8 * pb, (j >> 1) & 1)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t dvs = dv + s * (kT8StageBytes / 16);
 #pragma unroll
-                for (int kk = 0; kk < kT8Keys / 16; ++kk)
-                    umma_bf16_ts(tm + kT8ColO, tm + kT8ColS + 64 * pb + 8 * kk, dvs + 2 * kk, id_pv, kk > 0 || jj > 0 ? 1u : 0u);
-                umma_commit(o_done + 8 * pb);
-                umma_commit(kv_empty + 8 * s);
+                    for (int kk = 0; kk < kT8Keys / 16; ++kk)
+                        umma_bf16_ts(tm + kT8ColO, tm + kT8ColP + 32 * pb + 8 * kk, dvs + 2 * kk, id_pv, kk > 0 || !fresh_before ? 1u : 0u);
+                    umma_commit(o_done + 8 * pb);
+                    umma_commit(kv_empty + 8 * s);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        for (int j = 0; j <= nblk && !failed; ++j)
-            if ((j < nblk && !scores(j)) || (j >= 1 && !values(j - 1))) failed = true;
+            fresh_before = fresh;
+        }
         if (leader) {
             umma_commit(drain);  // completes when every MMA issued above has
             mbar_wait_bounded(drain, 0);
         }
         __syncwarp();
+        }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // ---- query rows: one per thread
-        const int r = r0 + tid;
-        const bool valid = r < r_valid;
-        const bool warp_active = r0 + 32 * warp < r_valid;
-        const int t = r / p.G;
-        const int pr = valid ? base + t : -1;
-        const int lor = valid && W > 0 ? max(0, base + t - W + 1) : 0;
+        if (units > 0) {
         const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-        float m_ref = -INFINITY, l = 0.f;
-        for (int j = 0; j < nblk; ++j) {
-            const int k0 = kb + j * kT8Tiles;
-            // every row warp waits for S_j, rows or not, so that no warp's arrival on p_full can run ahead
-            // into a later phase (a give-up is taken by the whole warp: the TMEM accesses are warp-wide)
-            const int sb = j % kT8SBufs, st = j % kT8Stages;
-            if (__any_sync(0xffffffffu, !mbar_wait_bounded(s_full + 8 * sb, (j / kT8SBufs) & 1))) {
-                failed = true;
-                break;
+        auto row_off = [&](const T8Walk &x, int r) {
+            const int t = r / p.G, hl = r - t * p.G;
+            return ((static_cast<size_t>(x.b) * p.T + t) * p.Hq + x.g * p.G + hl) * kD;
+        };
+        // a segment's query rows as fp16, zeros past its valid ones, into buffer buf
+        auto load_q = [&](const T8Walk &x, int buf) {
+            const int r = x.rb * kT8Rows + tid;
+            const bool ok = r < x.seq.n * p.G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (ok ? row_off(x, r) : 0));
+            uint8_t *dst = sQ + buf * kT8QBytes + tid * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint4 v = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+                *reinterpret_cast<uint4 *>(dst + ((c ^ (tid & 7)) << 4)) = v;
             }
-            if (warp_active) {
-                // the pages' factors: complete since S_j is, waited for to see them (the stage is not
-                // filled again before this block's P)
-                if (__any_sync(0xffffffffu, !mbar_wait_bounded(kv_full + 8 * st, (j / kT8Stages) & 1))) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the tensor cores
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + 8 * buf);
+        };
+        {
+            T8Walk w;
+            w.start(p, s_start, units);
+            load_q(w, 0);
+            if (lane == 0) {
+                s_walk[warp][1] = w;
+                s_begin[warp] = s_range[0] - w.u0;  // the segment's first unit among all
+            }
+            __syncwarp();
+        }
+        int i = 0, seg = 0, st = 0;
+        bool more = true;
+        while (more) {  // (a warp that gave up still counts itself at its shared segments, whose counters return to zero)
+            int pr, lor, jf, count;  // the row's keys [lor, pr], the unit's first position, the segment's units here
+            bool valid, warp_active;
+            {
+                T8Walk w = s_walk[warp][1];
+                const int r = w.rb * kT8Rows + tid, r_valid = min(p.T, w.seq.n) * p.G;
+                valid = r < r_valid;
+                warp_active = w.rb * kT8Rows + 32 * warp < r_valid;
+                const int pos = w.seq.L - w.seq.n + r / p.G;
+                pr = valid ? pos : -1;
+                lor = valid && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+                jf = (w.keys.pt_lo + w.u0 * kT8Tiles) * kPage;
+                count = w.u1 - w.u0;
+                T8Walk ahead = w;
+                more = ahead.next(p);
+                if (more && !failed) load_q(ahead, (seg + 1) & 1);  // (its buffer's last segment is finished)
+                __syncwarp();
+                if (lane == 0) {
+                    s_walk[warp][0] = w;
+                    s_walk[warp][1] = ahead;
+                }
+                __syncwarp();
+            }
+            float R = -INFINITY, l = 0.f;
+            for (int k = 0; k < count && !failed; ++k, ++i, jf += kT8Keys) {
+                const int sb = i & 1;
+                // every row warp waits for S_i, rows or not, so that no warp's arrival on p_full can run ahead
+                // into a later phase (a give-up is taken by the whole warp: the TMEM accesses are warp-wide)
+                if (__any_sync(0xffffffffu, !mbar_wait_bounded(s_full + 8 * sb, (i >> 1) & 1))) {
                     failed = true;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t sc = tm + lanes + kT8ColS + 64 * sb;
-                uint32_t raw[2][32];
-                tmem_ld32(sc, raw[0]);
-                tmem_ld32(sc + 32, raw[1]);
-                tmem_wait_ld();
-                float x[64];
-#pragma unroll
-                for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
-                const int jf = (pt_lo + k0) * kPage;
-                if (!(valid && k0 + kT8Tiles <= ke && jf >= lor && jf + kT8Keys - 1 <= pr)) {
-                    // keys [a, e) of the block are this row's
-                    const int a = lor - jf, e = min(pr + 1 - jf, (ke - k0) * kPage);
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c < a || c >= e) x[c] = -INFINITY;
-                }
-                float4 fac[kT8Tiles];
-                float mb = -INFINITY;
-#pragma unroll
-                for (int u = 0; u < kT8Tiles; ++u) {
-                    fac[u] = s_fac[st * kT8Tiles + u];
-                    const float *y = x + 16 * u;
-                    const float m1 = max3(y[0], y[1], y[2]), m2 = max3(y[3], y[4], y[5]), m3 = max3(y[6], y[7], y[8]);
-                    const float m4 = max3(y[9], y[10], y[11]), m5 = max3(y[12], y[13], y[14]);
-                    const float mt = max3(max3(m1, m2, m3), max3(m4, m5, y[15]), -INFINITY);
-                    mb = fmaxf(mb, fmaf(mt, fac[u].x, fac[u].y));  // the multiplier is positive
-                }
-                const bool need = valid && mb > m_ref + kT8Rescale;
-                const float m_new = need ? ceilf(mb) : m_ref;  // an integer: F - R and the rescaling are exact
-                if (j > 0 && __any_sync(0xffffffffu, need)) {
-                    const int jb = (j - 1) % kT8SBufs;  // (see multi_tc_kernel on this wait)
-                    if (__any_sync(0xffffffffu, !mbar_wait_bounded(o_done + 8 * jb, ((j - 1) / kT8SBufs) & 1))) {
-                        failed = true;
-                        break;
-                    }
+                if (warp_active) {
+                    // (S_i complete: so is PV_{i-2}, which read the P buffer)
                     tc_fence_after();
-                    const float f = need ? exp2f(m_ref - m_new) : 1.f;  // m_ref = -inf: 0 (O and l are 0)
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {  // (16 columns at a time: the 64 scores hold most registers)
-                        uint32_t o[16];
-                        tmem_ld16(tm + lanes + kT8ColO + 16 * h, o);
+                    const uint32_t sc = tm + lanes + kT8ColS + 64 * sb, pc = tm + lanes + kT8ColP + 32 * sb;
+                    const float4 *fac = s_fac + st * kT8Tiles;
+                    const bool interior = __all_sync(0xffffffffu, jf >= lor && jf + kT8Keys - 1 <= pr);
+                    const int a = lor - jf, e = pr + 1 - jf;  // keys [a, e) of the unit are this row's
+                    auto scores = [&](int h, uint32_t(&x)[32]) {
+                        tmem_ld32(sc + 32 * h, x);
                         tmem_wait_ld();
+                        if (!interior) {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                        tmem_st16(tm + lanes + kT8ColO + 16 * h, o);
-                        tmem_wait_st();
-                    }
-                }
-                if (need) {
-                    l *= exp2f(m_ref - m_new);
-                    m_ref = m_new;
-                }
-                const float mr = kT8Shift - (m_ref == -INFINITY ? 0.f : m_ref);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int u = 2 * h + v;
-                        const float2 mul = make_float2(fac[u].x, fac[u].x), add = make_float2(fac[u].y + mr, fac[u].y + mr);
-                        float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float2 a = fma2(make_float2(x[16 * u + 2 * c], x[16 * u + 2 * c + 1]), mul, add);
-                            const float a0 = fast_exp2(a.x), a1 = fast_exp2(a.y);
-                            ls[c & 1] = add2(ls[c & 1], make_float2(a0, a1));
-                            pk[8 * v + c] = pack_f16(a0, a1);
+                            for (int c = 0; c < 32; ++c)
+                                if (32 * h + c < a || 32 * h + c >= e) x[c] = 0xff800000u;
                         }
-                        l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) * fac[u].z;
+                    };
+                    float l_unit;
+                    // the probabilities with the reference R; true: one may be too large
+                    auto probabilities = [&]() {
+                        const float mr = kT8Shift - (R == -INFINITY ? 0.f : R);
+                        bool over = false;
+                        l_unit = 0.f;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t x[32], pk[16];
+                            scores(h, x);
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) {
+                                const float4 f = fac[2 * h + v];
+                                const float2 mul = make_float2(f.x, f.x), add = make_float2(f.y + mr, f.y + mr);
+                                float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const float2 y = fma2(make_float2(__uint_as_float(x[16 * v + 2 * c]), __uint_as_float(x[16 * v + 2 * c + 1])), mul, add);
+                                    const float a0 = fast_exp2(y.x), a1 = fast_exp2(y.y);
+                                    ls[c & 1] = add2(ls[c & 1], make_float2(a0, a1));
+                                    pk[8 * v + c] = pack_f16(a0, a1);
+                                }
+                                const float2 s2 = add2(ls[0], ls[1]);
+                                const float sum = s2.x + s2.y;
+                                over = over || sum > kT8TileMax;
+                                l_unit = fmaf(sum, f.z, l_unit);
+                            }
+                            tmem_st16(pc + 16 * h, pk);
+                        }
+                        return over;
+                    };
+                    bool need = R == -INFINITY && valid;
+                    if (!__any_sync(0xffffffffu, need)) need = probabilities();
+                    if (__any_sync(0xffffffffu, need)) {
+                        float mb = -INFINITY;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t x[32];
+                            scores(h, x);
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) {
+                                const float4 f = fac[2 * h + v];
+                                float mt = -INFINITY;
+#pragma unroll
+                                for (int c = 0; c < 16; c += 2) mt = max3(mt, __uint_as_float(x[16 * v + c]), __uint_as_float(x[16 * v + c + 1]));
+                                mb = fmaxf(mb, fmaf(mt, f.x, f.y));  // the multiplier is positive
+                            }
+                        }
+                        const float Rn = need ? fmaxf(R, ceilf(mb)) : R;  // an integer: F - R and the rescaling are exact
+                        const float f = Rn == R ? 1.f : exp2f(R - Rn);    // R = -inf: 0 (O and l are 0)
+                        if (k > 0) {
+                            // O holds the segment's PVs up to PV_{i-1}, whose barrier cannot be a phase further:
+                            // PV_{i+1} waits for P_{i+1}
+                            if (__any_sync(0xffffffffu, !mbar_wait_bounded(o_done + 8 * (sb ^ 1), ((i - 1) >> 1) & 1))) {
+                                failed = true;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                uint32_t o[16];
+                                tmem_ld16(tm + lanes + kT8ColO + 16 * h, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                                tmem_st16(tm + lanes + kT8ColO + 16 * h, o);
+                                tmem_wait_st();
+                            }
+                        }
+                        l *= f;
+                        R = Rn;
+                        tmem_wait_st();
+                        probabilities();
                     }
-                    tmem_st16(tm + lanes + kT8ColS + 64 * sb + 16 * h, pk);
+                    l += l_unit;
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * sb);
+                if (++st == kT8Stages) st = 0;
             }
-            tc_fence_before();
+            // ---- finish this thread's row: O (after the segment's last PV) -> output or partial
+            const int last = i - 1;
+            if (!failed && warp_active && __any_sync(0xffffffffu, !mbar_wait_bounded(o_done + 8 * (last & 1), (last >> 1) & 1)))
+                failed = true;
+            const T8Walk w = s_walk[warp][0];
+            const int r0 = w.rb * kT8Rows, r = r0 + tid, r_end = min(r0 + kT8Rows, p.T * p.G);
+            const bool whole = w.u0 == 0 && w.u1 == w.keys.units;
+            const int slot_k = seg == 0 ? 0 : 1;
+            const float m_row = R - kT8Shift;
+            float f = 0.f;  // rows that are not queries: zeros
+            if (whole && valid) {
+                const float sg = p.sinks != nullptr ? __ldg(p.sinks + w.g * p.G + r % p.G) * kLog2e : -INFINITY;
+                const float M = fmaxf(m_row, sg);
+                if (M != -INFINITY) {
+                    const float den = l * exp2f(m_row - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
+                    f = den > 0.f ? exp2f(m_row - M) / den : den == den ? 0.f : den;
+                }
+            }
+            float *slot = p.part + (static_cast<size_t>(cta) * 2 + slot_k) * kT8SlotFloats + static_cast<size_t>(tid) * kMSlotFloats;
+            if (!whole && valid && !failed) {
+                slot[0] = m_row;
+                slot[1] = l;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 4 && !failed; ++h) {
+                uint32_t x[16];
+                if (warp_active) {
+                    tmem_ld16(tm + lanes + kT8ColO + 16 * h, x);
+                    tmem_wait_ld();
+                }
+                float o[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) o[c] = valid ? __uint_as_float(x[c]) : 0.f;
+                if (whole) {
+                    if (r < r_end) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row_off(w, r)) + 2 * h;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint4 y;
+                            y.x = pack_bf16(o[8 * c] * f, o[8 * c + 1] * f);
+                            y.y = pack_bf16(o[8 * c + 2] * f, o[8 * c + 3] * f);
+                            y.z = pack_bf16(o[8 * c + 4] * f, o[8 * c + 5] * f);
+                            y.w = pack_bf16(o[8 * c + 6] * f, o[8 * c + 7] * f);
+                            dst[c] = y;
+                        }
+                    }
+                } else if (valid) {
+                    float4 *acc = reinterpret_cast<float4 *>(slot + kMAccOff) + 4 * h;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                }
+            }
+            tc_fence_before();  // (the next segment's first PV writes O after this warp's next P)
+            if (!whole && !p.defer && r0 + 32 * warp < r_end) {
+                // the last of the CTAs that share the segment folds its partials, every warp its own 32 rows: a
+                // counter per warp, at the segment's first CTA (which has no other segment that goes on)
+                const long long begin = s_begin[warp], U = s_range[2];
+                const int c0 = t8_owner(U, nc, begin), c1 = t8_owner(U, nc, begin + w.keys.units - 1);
+                __threadfence();
+                __syncwarp();
+                int *ctr = p.counters + 4 * c0 + warp;
+                int ticket = 0;
+                if (lane == 0) ticket = atomicAdd(ctr, 1);
+                if (__shfl_sync(0xffffffffu, ticket, 0) == c1 - c0) {
+                    __threadfence();
+                    const int k0 = t8_first(U, nc, c0) < begin ? 1 : 0;
+                    if (r < r_end)
+                        t8_fold_thread(p, c0, k0, c1 - c0 + 1, tid, w.g * p.G + r % p.G, valid, reinterpret_cast<uint4 *>(p.out + row_off(w, r)));
+                    if (lane == 0) *ctr = 0;  // ready for the next call
+                }
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full + 8 * sb);
+            if (lane == 0) s_begin[warp] += w.keys.units;
+            ++seg;
         }
-        // ---- finish this thread's row: O (after the last PV) -> output or partial
-        const int lb = (nblk - 1) % kT8SBufs;
-        if (warp_active && !failed && __any_sync(0xffffffffu, !mbar_wait_bounded(o_done + 8 * lb, ((nblk - 1) / kT8SBufs) & 1)))
-            failed = true;
-        const bool have = warp_active && !failed;
-        const float m_row = m_ref - kT8Shift;
-        float f = 0.f;  // rows that are not queries: zeros
-        if (nsplit == 1 && valid && have) {
-            const int h = g * p.G + (r - t * p.G);
-            const float sg = p.sinks != nullptr ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
-            const float M = fmaxf(m_row, sg);
-            if (M != -INFINITY) {
-                const float den = l * exp2f(m_row - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
-                f = den > 0.f ? exp2f(m_row - M) / den : 0.f;
-            }
-        }
-        float *slot = p.part + ((((bg * p.row_blocks + rb) * p.splits + split) * kT8Rows) + tid) * kMSlotFloats;
-        if (nsplit > 1 && r < r_valid) {
-            slot[0] = m_row;
-            slot[1] = l;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            uint32_t raw[16];
-            if (have) {  // (the whole warp)
-                tmem_ld16(tm + lanes + kT8ColO + 16 * h, raw);
-                tmem_wait_ld();
-            }
-            float o[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = have && valid ? __uint_as_float(raw[c]) : 0.f;
-            if (nsplit == 1) {
-                if (r < r_end) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + row_off(r)) + 2 * h;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint4 w;
-                        w.x = pack_bf16(o[8 * c] * f, o[8 * c + 1] * f);
-                        w.y = pack_bf16(o[8 * c + 2] * f, o[8 * c + 3] * f);
-                        w.z = pack_bf16(o[8 * c + 4] * f, o[8 * c + 5] * f);
-                        w.w = pack_bf16(o[8 * c + 6] * f, o[8 * c + 7] * f);
-                        dst[c] = w;
-                    }
-                }
-            } else if (r < r_valid) {
-                float4 *acc = reinterpret_cast<float4 *>(slot + kMAccOff) + 4 * h;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            }
         }
     }
     if (failed) flag_status(DA_STATUS_TIMEOUT);
@@ -503,21 +869,32 @@ __global__ void __launch_bounds__(kT8Threads, 2)
     // ---- teardown: every MMA done (the issuer has waited) before TMEM is released
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 12) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kT8TmemCols));
     }
-    if (nsplit == 1 || p.defer) return;  // p.defer: multi_combine_kernel follows
-    __threadfence();
-    __syncthreads();
-    int *ctr = p.counters + bg * p.row_blocks + rb;
-    if (tid == 0) s_ticket = atomicAdd(ctr, 1);
-    __syncthreads();
-    if (s_ticket != nsplit - 1) return;
-    __threadfence();
-    const size_t slot0 = ((bg * p.row_blocks + rb) * p.splits) * static_cast<size_t>(kT8Rows);
-    multi_combine_rows(p, p.part + slot0 * kMSlotFloats, kT8Rows, r0, r_end, n, b, g, nsplit, 0, kT8Rows, warp,
-                       kT8Warps, lane);
-    __syncthreads();
-    if (tid == 0) *ctr = 0;  // ready for the next call
+}
+
+// The partials of the segments that several CTAs share, folded after the attention, one warp per query row:
+// where few segments are spread over the whole grid the CTA that comes last would fold dozens alone.
+// One CTA per four rows of a segment; the split is worked out again from the lengths.
+constexpr int kT8FoldWarps = 4;
+__global__ void __launch_bounds__(kT8FoldWarps * 32) t8_combine_kernel(const MultiParams p, int grid) {
+    __shared__ long long pre[kMaxBatch + 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rb = blockIdx.x / (kT8Rows / kT8FoldWarps), rl = blockIdx.x % (kT8Rows / kT8FoldWarps) * kT8FoldWarps + warp;
+    const int g = blockIdx.y, b = blockIdx.z;
+    const T8Seq s = t8_seq(p, b);
+    if (rb >= s.blocks) return;  // zeros, written by the attention
+    t8_prefix(p, pre, warp, kT8FoldWarps, lane);
+    const long long U = pre[p.B];
+    const int nc = t8_ctas(U, grid);
+    long long begin = pre[b] + (pre[b + 1] - pre[b]) / p.Hkv * g;
+    for (int i = 0; i < rb; ++i) begin += t8_keys(p, s, i).units;
+    const int c0 = t8_owner(U, nc, begin), c1 = t8_owner(U, nc, begin + t8_keys(p, s, rb).units - 1);
+    const int r = rb * kT8Rows + rl, t = r / p.G, hl = r - t * p.G;
+    if (c0 == c1 || r >= p.T * p.G) return;
+    const uint32_t y = t < s.n ? t8_fold_row(p, c0, t8_first(U, nc, c0) < begin ? 1 : 0, c1 - c0 + 1, rl, g * p.G + hl, lane) : 0u;
+    reinterpret_cast<uint32_t *>(p.out + ((static_cast<size_t>(b) * p.T + t) * p.Hq + g * p.G + hl) * kD)[lane] = y;
 }
