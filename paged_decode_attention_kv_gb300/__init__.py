@@ -19,7 +19,9 @@ Tensor layouts (all contiguous, bf16 unless noted):
   weights           [num_pages, Hkv, page_size] float32, accumulated attention weights
 """
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -155,8 +157,7 @@ def load_library():
     lib.kv_evict_workspace_bytes.argtypes = [da_shape, c_int]
     lib.kv_evict_workspace_bytes.restype = ctypes.c_size_t
     lib.decode_attn_weights_reserve.argtypes = [vp, ctypes.c_size_t]
-    rows_p = ctypes.POINTER(da_rows)
-    lib.qk_norm_rope.argtypes = [rows_p, rows_p, rows_p, c_int, c_int, c_int, c_int, i32p, c_int, ctypes.c_char_p, f32p, f32p,
+    lib.qk_norm_rope.argtypes = [vp, vp, vp, c_int, c_int, c_int, c_int, i32p, c_int, ctypes.c_char_p, f32p, f32p,
                                  c_int, f32p, f32p, c_float, vp]
     lib.kv_append_fp8.argtypes = [vp, vp, vp, i32p, i32p, i32p, c_int, c_int, da_shape, c_int, c_int, c_int, c_int, c_int, vp]
     lib.kv_read_fp8.argtypes = [vp, i32p, i32p, i32p, c_int, vp, vp, c_int, da_shape, c_int, c_int, c_int, c_int, vp]
@@ -619,31 +620,34 @@ def decode_attn_weights_reserve(nbytes: int, stream=None):
     _check(load_library().decode_attn_weights_reserve(_raw_stream(stream, torch.cuda.current_device()), int(nbytes)))
 
 
+_ROWS = struct.Struct("@PPqq")  # da_rows
+
+
 def _token_rows(name, x, heads, dev):
-    """The shape [..., heads, 64] of bf16 rows whose tokens are evenly spaced, their count and the elements from
-    one token to the next."""
-    if x.dim() < 3 or x.shape[-1] != 64 or x.shape[-2] != heads or x.dtype is not torch.bfloat16 or not x.is_cuda \
-            or x.get_device() != dev or x.stride(-1) != 1 or (heads > 1 and x.stride(-2) != 64):
-        _refuse_rows(name, x, heads)
-    tokens, step = 1, None
-    for n, st in zip(reversed(x.shape[:-2]), reversed(x.stride()[:-2])):
-        if n == 1:
-            continue
-        if step is None:
-            step = st
-        elif st != step * tokens:
-            _refuse_rows(name, x, heads)
-        tokens *= n
-    return tokens, heads * 64 if step is None else step
-
-
-def _refuse_rows(name, x, heads):
+    """The count of bf16 rows [..., heads, 64] whose tokens are evenly spaced, and the elements from one to the next."""
+    if x.dtype is torch.bfloat16 and x.get_device() == dev:  # (-1: not on a GPU)
+        shape, step = x.shape, x.stride()
+        if len(shape) == 3 and shape[2] == 64 and shape[1] == heads and step[2] == 1 and (step[1] == 64 or heads == 1):
+            return shape[0], step[0]
+        if len(shape) > 3 and shape[-1] == 64 and shape[-2] == heads and step[-1] == 1 and (step[-2] == 64 or heads == 1):
+            tokens, token = 1, None
+            for n, st in zip(reversed(shape[:-2]), reversed(step[:-2])):
+                if n == 1:
+                    continue
+                if token is None:
+                    token = st
+                elif st != token * tokens:
+                    break
+                tokens *= n
+            else:
+                return tokens if 0 not in shape else 0, heads * 64 if token is None else token
     if x.is_cuda and x.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
     raise ValueError(f"{name} must be CUDA bf16 rows [..., {heads}, 64], contiguous within a token and evenly spaced, "
                      f"got {x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
 
 
+@functools.lru_cache(maxsize=64)
 def _pair_axes(axes, sections, interleaved):
     """The axis of each of the 32 pairs: the sections one after the other, or the axes taking turns until theirs is
     used up."""
@@ -653,7 +657,7 @@ def _pair_axes(axes, sections, interleaved):
         return None
     left = [int(n) for n in sections]
     if len(left) != axes or min(left) < 0 or sum(left) != 32:
-        raise ValueError(f"sections {tuple(sections)} must be {axes} counts of pairs that add up to 32")
+        raise ValueError(f"sections {sections} must be {axes} counts of pairs that add up to 32")
     if not interleaved:
         return bytes(a for a, n in enumerate(left) for _ in range(n))
     turn = []
@@ -670,37 +674,38 @@ def qk_norm_rope(q, k, positions, rope_cos, rope_sin, q_out, k_out, q_weight=Non
     """The RMS norm of every query and key head (q_weight, k_weight fp32 [64]; None: no norm) and the rotary embedding
     at the given positions, in one pass; value rows (v, v_out) are copied along. q, k, v: bf16 [..., heads, 64], any
     views whose tokens are evenly spaced (slices of one packed projection); the outputs likewise, or the inputs
-    themselves. positions int32 [tokens], or [axes, tokens] with sections (pairs per axis, 32 in all, in blocks or
-    interleaved: the axes taking turns); rope_cos / rope_sin fp32 [max_position, 32]. Returns q_out, k_out."""
+    themselves. positions int32, one per token, or [axes, tokens] with sections (pairs per axis, 32 in all, in blocks
+    or interleaved: the axes taking turns); rope_cos / rope_sin fp32 [max_position, 32]. Returns q_out, k_out."""
     dev = torch.cuda.current_device()
+    lead = q.shape[:-2]
+    if len(lead) == 0 or len(k.shape) < 3:
+        raise ValueError(f"q and k are [..., heads, 64], got {tuple(q.shape)} and {tuple(k.shape)}")
     if (v is None) != (v_out is None):
         raise ValueError("v and v_out are given together")
-    if q.dim() < 3 or k.dim() < 3:
-        raise ValueError(f"q and k are [..., heads, 64], got {tuple(q.shape)} and {tuple(k.shape)}")
     Hq, Hkv = q.shape[-2], k.shape[-2]
-    if rope_cos.dim() != 2:
-        raise ValueError(f"rope_cos is [max_position, 32], got {tuple(rope_cos.shape)}")
-    lead, tables = q.shape[:-2], (rope_cos.shape[0], 32)
-    rows, tokens = [], None
-    for name, x, y, heads in (("q", q, q_out, Hq), ("k", k, k_out, Hkv), ("v", v, v_out, Hkv)):
-        if x is None:
-            rows.append(None)
-            continue
-        if x.shape[:-2] != lead or y.shape[:-2] != lead:
-            raise ValueError(f"{name} is {tuple(x.shape)} and {name}_out {tuple(y.shape)}, q is {tuple(q.shape)}")
-        tokens, step = _token_rows(name, x, heads, dev)
-        rows.append(da_rows(x.data_ptr(), y.data_ptr(), step, _token_rows(name + "_out", y, heads, dev)[1]))
-    axes = 1
-    if positions.dim() == 2 and sections is not None:
-        axes = positions.shape[0]
-        pp = _tensor("positions", positions, torch.int32, (axes, tokens), dev)
+    if k.shape[:-2] != lead or q_out.shape[:-2] != lead or k_out.shape[:-2] != lead or \
+            (v is not None and (v.shape[:-2] != lead or v_out.shape[:-2] != lead)):
+        raise ValueError(f"q is {tuple(q.shape)}: k, v and the outputs have its leading dimensions, got k {tuple(k.shape)}, "
+                         f"q_out {tuple(q_out.shape)}, k_out {tuple(k_out.shape)}"
+                         + ("" if v is None else f", v {tuple(v.shape)}, v_out {tuple(v_out.shape)}"))
+    tokens, step = _token_rows("q", q, Hq, dev)
+    q_rows = _ROWS.pack(q.data_ptr(), q_out.data_ptr(), step, _token_rows("q_out", q_out, Hq, dev)[1])
+    k_rows = _ROWS.pack(k.data_ptr(), k_out.data_ptr(), _token_rows("k", k, Hkv, dev)[1], _token_rows("k_out", k_out, Hkv, dev)[1])
+    v_rows = None if v is None else _ROWS.pack(v.data_ptr(), v_out.data_ptr(), _token_rows("v", v, Hkv, dev)[1],
+                                               _token_rows("v_out", v_out, Hkv, dev)[1])
+    if sections is None:
+        axes = 1
+        pp = _tensor("positions", positions, torch.int32, lead if len(lead) == positions.dim() else (tokens,), dev)
     else:
-        pp = _tensor("positions", positions, torch.int32, lead if positions.dim() == len(lead) else (tokens,), dev)
-    weights = [None if w is None else _tensor(n, w, torch.float32, (64,), dev) for n, w in (("q_weight", q_weight), ("k_weight", k_weight))]
-    _check(load_library().qk_norm_rope(
-        ctypes.byref(rows[0]), ctypes.byref(rows[1]), None if rows[2] is None else ctypes.byref(rows[2]), tokens, Hq, Hkv, 64, pp, axes,
-        _pair_axes(axes, sections, interleaved), _tensor("rope_cos", rope_cos, torch.float32, tables, dev),
-        _tensor("rope_sin", rope_sin, torch.float32, tables, dev), rope_cos.shape[0], *weights, float(eps), _raw_stream(stream, dev)))
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        pp = _tensor("positions", positions, torch.int32, (axes, tokens) if positions.dim() == 2 else (tokens,), dev)
+        sections = tuple(sections)
+    most = rope_cos.shape[0] if rope_cos.dim() else 0
+    _check((_lib or load_library()).qk_norm_rope(
+        q_rows, k_rows, v_rows, tokens, Hq, Hkv, 64, pp, axes, _pair_axes(axes, sections, bool(interleaved)),
+        _tensor("rope_cos", rope_cos, torch.float32, (most, 32), dev), _tensor("rope_sin", rope_sin, torch.float32, (most, 32), dev), most,
+        None if q_weight is None else _tensor("q_weight", q_weight, torch.float32, (64,), dev),
+        None if k_weight is None else _tensor("k_weight", k_weight, torch.float32, (64,), dev), eps, _raw_stream(stream, dev)))
     return q_out, k_out
 
 
