@@ -3023,7 +3023,10 @@ int run_rotate(const da_rows *q, const da_rows *k, const da_rows *v, int tokens,
     p.eps = eps;
     p.N = tokens, p.Hq = Hq, p.Hkv = Hkv, p.max_position = max_position;
     p.rows = Hq + Hkv + (v ? Hkv : 0);
-    p.chunk = kRotRows;
+    // a warp takes a whole token's rows where the tokens fill the GPU (its angles are then read once), or eight rows
+    const long long fill = static_cast<long long>(sm_count(dev)) * kRotWarps;
+    const int pieces = static_cast<int>(std::min<long long>((p.rows + 7) / 8, std::max<long long>(1, fill / tokens)));
+    p.chunk = ((p.rows + pieces - 1) / pieces + 7) / 8 * 8;
     const long long items = static_cast<long long>(tokens) * ((p.rows + p.chunk - 1) / p.chunk);
     const long long blocks = (items + kRotThreads / 32 - 1) / (kRotThreads / 32);
     if (blocks > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
@@ -3088,8 +3091,7 @@ int run_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t
     const BlockParams p = {static_cast<uint8_t *>(const_cast<void *>(kv_cache)), block_table, seq_lens, s.num_kv_heads,
                            block_table ? 0 : window, block_table ? max_pages : 0, block_table ? num_pages : 0, max_seq_len};
     return launch_pdl(kv_read_fp8_kernel, grid, kStoreWarps * 32, 0, static_cast<cudaStream_t>(stream), p, starts, rows,
-                      static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out),
-                      ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0 ? 1 : 0);
+                      static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out));
 }
 
 #ifndef DA_T8_DEFER

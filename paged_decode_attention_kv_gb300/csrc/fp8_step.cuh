@@ -6,13 +6,6 @@
 // Included into decode_attn.cu (inside its anonymous namespace): one translation unit, sharing
 // the fp8 helpers and the status word.
 
-// 32 bytes to global memory at a 32-byte aligned address.
-__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 // ------------------------------------------------------------------ norms and rotation
 // Row x of 64 values of one head: y = x w / sqrt(sum(x^2) / 64 + eps) (no norm: y = x), then the
 // pairs (i, i + 32) rotated by row pos[axis(i)] of the tables. All in fp32, rounded once to bf16;
@@ -36,8 +29,14 @@ struct RotateParams {
     unsigned char axis[kD / 2];              // the axis of each pair
     unsigned char quads;                     // bit i: the pairs 4 i .. 4 i + 3 are of one axis
 };
-constexpr int kRotThreads = 128;
-constexpr int kRotRows = 16;
+#ifndef DA_ROT_BATCH
+#define DA_ROT_BATCH 2
+#endif
+#ifndef DA_ROT_WARPS
+#define DA_ROT_WARPS 32
+#endif
+constexpr int kRotThreads = 128, kRotBatch = DA_ROT_BATCH;
+constexpr int kRotWarps = DA_ROT_WARPS;  // warps per SM that a token's rows are spread over where there are few tokens
 
 __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_constant__ RotateParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -78,55 +77,65 @@ __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_
         }
         if (bad) flag_status(DA_STATUS_BAD_POSITION);
     }
-    for (int r = r_begin + (lane >> 2); r - (lane >> 2) < r_end; r += 8) {  // (all lanes stay for the shuffles)
-        const bool live = r < r_end;
-        const int kind = r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2;  // q, k, v
-        const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.Hkv;
-        const __nv_bfloat16 *src = (kind == 0 ? p.q + tok * p.q_ld : kind == 1 ? p.k + tok * p.k_ld : p.v + tok * p.v_ld) + h * kD + 8 * j;
-        __nv_bfloat16 *dst = (kind == 0 ? p.q_out + tok * p.qo_ld : kind == 1 ? p.k_out + tok * p.ko_ld : p.v_out + tok * p.vo_ld) + h * kD + 8 * j;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (live) {
-            a = *reinterpret_cast<const uint4 *>(src);
-            b = *reinterpret_cast<const uint4 *>(src + kD / 2);
-        }
-        const float *w = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-        uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-        float x[8], y[8], ss = 0.f;
+    // two rows at a time: their loads are in flight together
+    for (int r0 = r_begin + (lane >> 2); r0 - (lane >> 2) < r_end; r0 += 8 * kRotBatch) {  // (all lanes stay for the shuffles)
+        uint4 a[kRotBatch], b[kRotBatch];
+        __nv_bfloat16 *dst[kRotBatch];
+        int kind[kRotBatch];  // q, k, v, or no row
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 u = unpack_bf16(aw[e]), v = unpack_bf16(bw[e]);
-            x[2 * e] = u.x, x[2 * e + 1] = u.y, y[2 * e] = v.x, y[2 * e + 1] = v.y;
-            ss += u.x * u.x + u.y * u.y + v.x * v.x + v.y * v.y;
-        }
-        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-        ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-        if (!live) continue;
-        if (w != nullptr) {
-            const float rms = 1.f / sqrtf(ss * (1.f / kD) + p.eps);
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const float4 wa = __ldg(reinterpret_cast<const float4 *>(w + 8 * j + e));
-                const float4 wb = __ldg(reinterpret_cast<const float4 *>(w + kD / 2 + 8 * j + e));
-                x[e] *= rms * wa.x, x[e + 1] *= rms * wa.y, x[e + 2] *= rms * wa.z, x[e + 3] *= rms * wa.w;
-                y[e] *= rms * wb.x, y[e + 1] *= rms * wb.y, y[e + 2] *= rms * wb.z, y[e + 3] *= rms * wb.w;
+        for (int i = 0; i < kRotBatch; ++i) {
+            const int r = r0 + 8 * i;
+            kind[i] = r >= r_end ? 3 : r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2;
+            const int h = (kind[i] == 0 ? r : kind[i] == 1 ? r - p.Hq : r - p.Hq - p.Hkv) * kD + 8 * j;
+            const __nv_bfloat16 *src = (kind[i] == 0 ? p.q + tok * p.q_ld : kind[i] == 1 ? p.k + tok * p.k_ld : p.v + tok * p.v_ld) + h;
+            dst[i] = (kind[i] == 0 ? p.q_out + tok * p.qo_ld : kind[i] == 1 ? p.k_out + tok * p.ko_ld : p.v_out + tok * p.vo_ld) + h;
+            a[i] = b[i] = make_uint4(0, 0, 0, 0);
+            if (kind[i] < 3) {
+                a[i] = *reinterpret_cast<const uint4 *>(src);
+                b[i] = *reinterpret_cast<const uint4 *>(src + kD / 2);
             }
         }
-        if (kind < 2) {
+#pragma unroll
+        for (int i = 0; i < kRotBatch; ++i) {
+            const float *w = kind[i] == 0 ? p.q_weight : kind[i] == 1 ? p.k_weight : nullptr;
+            uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+            float x[8], y[8], ss = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float o[2], u[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int n = 2 * e + i;
-                    o[i] = __fsub_rn(__fmul_rn(x[n], c[n]), __fmul_rn(y[n], s[n]));
-                    u[i] = __fadd_rn(__fmul_rn(y[n], c[n]), __fmul_rn(x[n], s[n]));
-                }
-                aw[e] = pack_bf16(o[0], o[1]);
-                bw[e] = pack_bf16(u[0], u[1]);
+                const float2 u = unpack_bf16(aw[e]), v = unpack_bf16(bw[e]);
+                x[2 * e] = u.x, x[2 * e + 1] = u.y, y[2 * e] = v.x, y[2 * e + 1] = v.y;
+                ss += u.x * u.x + u.y * u.y + v.x * v.x + v.y * v.y;
             }
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+            if (kind[i] == 3) continue;
+            if (w != nullptr) {
+                const float rms = 1.f / sqrtf(ss * (1.f / kD) + p.eps);
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 wa = __ldg(reinterpret_cast<const float4 *>(w + 8 * j + e));
+                    const float4 wb = __ldg(reinterpret_cast<const float4 *>(w + kD / 2 + 8 * j + e));
+                    x[e] *= rms * wa.x, x[e + 1] *= rms * wa.y, x[e + 2] *= rms * wa.z, x[e + 3] *= rms * wa.w;
+                    y[e] *= rms * wb.x, y[e + 1] *= rms * wb.y, y[e + 2] *= rms * wb.z, y[e + 3] *= rms * wb.w;
+                }
+            }
+            if (kind[i] < 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float o[2], u[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int n = 2 * e + k;
+                        o[k] = __fsub_rn(__fmul_rn(x[n], c[n]), __fmul_rn(y[n], s[n]));
+                        u[k] = __fadd_rn(__fmul_rn(y[n], c[n]), __fmul_rn(x[n], s[n]));
+                    }
+                    aw[e] = pack_bf16(o[0], o[1]);
+                    bw[e] = pack_bf16(u[0], u[1]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst[i]) = make_uint4(aw[0], aw[1], aw[2], aw[3]);
+            *reinterpret_cast<uint4 *>(dst[i] + kD / 2) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
         }
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(aw[0], aw[1], aw[2], aw[3]);
-        *reinterpret_cast<uint4 *>(dst + kD / 2) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
     }
 }
 
@@ -159,16 +168,73 @@ __device__ __forceinline__ float fp8_scale(float top, int rule) {
     return rule == DA_FP8_SCALE_RECIPROCAL ? __fmul_rn(top, 1.f / 448.f) : __fdiv_rn(top, 448.f);
 }
 
+// x / scale of a row, correctly rounded: the quotient's first guess x r, r = RN(1 / scale), corrected by its exact
+// remainder, is the rounded quotient (Markstein's theorem, IBM J. Res. Dev. 34, 1990), as long as nothing under- or
+// overflows on the way. Rows whose largest magnitude lies far from both ends of fp32's range qualify: their scale and
+// its reciprocal are normal, and a remainder can only be inexact where the quotient is far below half of e4m3's
+// smallest step, 2^-10. The others divide. Three operations instead of a division's ten or so (those, and the
+// divisions' branches, made the kernel take 51 us for 42000 tokens of 8 heads, 32 of them at the memory's rate).
+struct RowScale {
+    float scale, r;
+    bool fast;
+    __device__ __forceinline__ RowScale(float top, int rule) {
+        scale = fp8_scale(top, rule);
+        fast = top >= 1e-20f && top <= 1e30f;
+        r = fast ? __frcp_rn(scale) : 0.f;
+    }
+    __device__ __forceinline__ float quotient(float x) const {
+        const float q = __fmul_rn(x, r);
+        const float y = __fmaf_rn(__fmaf_rn(-q, scale, x), r, q);
+        return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // (-0 stays -0)
+    }
+};
+// Eight bf16 values of a row (16 bytes) to their codes.
+__device__ __forceinline__ uint2 fp8_codes8(const uint4 &v, const RowScale &s) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+    if (s.fast) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16(w[e]);
+            c[e] = f32x2_to_e4m3x2(s.quotient(f.x), s.quotient(f.y));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16(w[e]);
+            c[e] = f32x2_to_e4m3x2(__fdiv_rn(f.x, s.scale), __fdiv_rn(f.y, s.scale));
+        }
+    }
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+// The larger magnitudes of two pairs of bf16 values (a NaN loses against a number, as in fmaxf).
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7fff7fffu));
+    return d;
+}
+// Four words of four bytes, turned around: word i of the result holds byte i of each.
+__device__ __forceinline__ void transpose4x4(uint32_t (&w)[4]) {
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[0], w[1], 0x7362);
+    const uint32_t c = __byte_perm(w[2], w[3], 0x5140), d = __byte_perm(w[2], w[3], 0x7362);
+    w[0] = __byte_perm(a, c, 0x5410);
+    w[1] = __byte_perm(a, c, 0x7632);
+    w[2] = __byte_perm(b, d, 0x5410);
+    w[3] = __byte_perm(b, d, 0x7632);
+}
+
 // The new tokens t < n of every sequence quantised into positions L - n + t (a ring keeps the last
-// `window` of them). One warp per block that they touch and KV head: lanes 2 t and 2 t + 1 take
-// token t of the block, 32 elements of its K row and of its V row each; the V codes are turned
-// around through the warp's 1 KiB of shared memory, so that a block that is filled by this call is
-// written in whole 16-byte rows. A block that is shared with earlier tokens gets its new bytes only.
+// `window` of them). One warp per block that they touch and KV head: lane 4 t' + j takes elements
+// 8 j .. + 7 and 32 + 8 j .. + 7 of tokens t' and t' + 8 of the block, so that every load and every store of codes is
+// made of whole sectors. The V codes are turned around, four by four bytes, on their way through the warp's shared
+// memory; a block that is filled by this call is written in whole words, one that is shared with earlier tokens
+// gets its new bytes only.
 constexpr int kStoreWarps = 4;
+constexpr int kCodePitch = 72;  // bytes from one token's codes to the next: the turning reads meet no bank twice
 __global__ void __launch_bounds__(kStoreWarps * 32)
     kv_append_fp8_kernel(const __grid_constant__ BlockParams p, const __nv_bfloat16 *__restrict__ k_new,
                          const __nv_bfloat16 *__restrict__ v_new, const int32_t *__restrict__ q_lens, int T, int rule) {
-    __shared__ __align__(16) uint8_t s_v[kStoreWarps][kPage * kD];
+    __shared__ __align__(16) uint8_t s_v[kStoreWarps][kPage * kCodePitch];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -183,90 +249,97 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
     }
     if (L == 0 || n == 0) return;
     const int base = L - n;
-    const int lo = p.block_table == nullptr ? max(base, L - p.window) : base;  // the first position stored
+    const int first = p.block_table == nullptr ? max(base, L - p.window) : base;  // the first position stored
     const int unit = blockIdx.x * kStoreWarps + warp;
-    const int blk_i = lo / kPage + unit / p.Hkv, g = unit % p.Hkv;
+    const int blk_i = first / kPage + unit / p.Hkv, g = unit % p.Hkv;
     if (blk_i > (L - 1) / kPage) return;
     uint8_t *blk = block_of(p, b, blk_i, g);
     if (blk == nullptr) return;
-    const int t = lane >> 1, half = lane & 1;
-    const int pos = blk_i * kPage + t;
-    const bool live = pos >= lo && pos < L;
-    const uint32_t mask = __ballot_sync(0xffffffffu, live);  // two bits per token
-    uint4 raw[2][4];
-    if (live) {
-        const size_t src = ((static_cast<size_t>(b) * T + (pos - base)) * p.Hkv + g) * kD + 32 * half;
+    const int pos0 = blk_i * kPage, t_lo = max(0, first - pos0), t_hi = min(kPage, L - pos0);  // tokens [t_lo, t_hi)
+    const int t = lane >> 2, j = lane & 3;
+    uint4 raw[2][2][2];  // K, V; token t, t + 8; elements 8 j, 32 + 8 j
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            raw[0][i] = __ldg(reinterpret_cast<const uint4 *>(k_new + src) + i);
-            raw[1][i] = __ldg(reinterpret_cast<const uint4 *>(v_new + src) + i);
+    for (int h = 0; h < 2; ++h) {
+        const int tt = t + 8 * h;
+        const bool live = tt >= t_lo && tt < t_hi;
+        const size_t src = ((static_cast<size_t>(b) * T + (pos0 + tt - base)) * p.Hkv + g) * kD + 8 * j;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            raw[0][h][i] = live ? __ldg(reinterpret_cast<const uint4 *>(k_new + src + 32 * i)) : make_uint4(0, 0, 0, 0);
+            raw[1][h][i] = live ? __ldg(reinterpret_cast<const uint4 *>(v_new + src + 32 * i)) : make_uint4(0, 0, 0, 0);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw[0][i] = raw[1][i] = make_uint4(0, 0, 0, 0);
     }
+    uint8_t *sv = s_v[warp];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        float x[32], top = 0.f;
+    for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {raw[kv][i].x, raw[kv][i].y, raw[kv][i].z, raw[kv][i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 u = unpack_bf16(w[e]);
-                x[8 * i + 2 * e] = u.x;
-                x[8 * i + 2 * e + 1] = u.y;
-                top = fmaxf(top, fmaxf(fabsf(u.x), fabsf(u.y)));
+        for (int h = 0; h < 2; ++h) {
+            const int tt = t + 8 * h;
+            const bool live = tt >= t_lo && tt < t_hi;
+            const uint4 &a = raw[kv][h][0], &c = raw[kv][h][1];
+            uint32_t m = abs_max2(abs_max2(a.x & 0x7fff7fffu, a.y), abs_max2(a.z & 0x7fff7fffu, a.w));
+            m = abs_max2(m, abs_max2(abs_max2(c.x & 0x7fff7fffu, c.y), abs_max2(c.z & 0x7fff7fffu, c.w)));
+            m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const float2 top = unpack_bf16(m);
+            const RowScale rs(fmaxf(top.x, top.y), rule);
+            const uint2 ca = fp8_codes8(a, rs), cc = fp8_codes8(c, rs);
+            if (kv == 0) {
+                if (live) {
+                    *reinterpret_cast<uint2 *>(blk + tt * kD + 8 * j) = ca;
+                    *reinterpret_cast<uint2 *>(blk + tt * kD + 32 + 8 * j) = cc;
+                }
+            } else {
+                *reinterpret_cast<uint2 *>(sv + tt * kCodePitch + 8 * j) = ca;
+                *reinterpret_cast<uint2 *>(sv + tt * kCodePitch + 32 + 8 * j) = cc;
             }
+            if (live && j == 0) reinterpret_cast<float *>(blk + kBlk8S)[kv * kPage + tt] = rs.scale;
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        const float scale = fp8_scale(top, rule);
-        uint32_t code[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t lo2 = f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
-            const uint32_t hi2 = f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
-            code[i] = lo2 | hi2 << 16;
-        }
-        uint4 *dst = reinterpret_cast<uint4 *>((kv == 0 ? blk : s_v[warp]) + t * kD + 32 * half);
-        if (live || kv == 1) {
-            dst[0] = make_uint4(code[0], code[1], code[2], code[3]);
-            dst[1] = make_uint4(code[4], code[5], code[6], code[7]);
-        }
-        if (live && half == kv) reinterpret_cast<float *>(blk + kBlk8S)[kv * kPage + t] = scale;
-    }
     __syncwarp();
-    const uint8_t *sv = s_v[warp];
+    if (t_lo == 0 && t_hi == kPage) {  // elements 4 (lane % 16) .. + 3 of tokens 8 (lane / 16) .. + 7
+        const int dq = lane & 15, th = lane >> 4;
+        uint32_t w[2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int d = lane + 32 * i;
-        uint8_t *dst = blk + kBlk8V + d * kPage;
-        if (mask == 0xffffffffu) {
-            uint32_t w[4];
+        for (int i = 0; i < 8; ++i) w[i >> 2][i & 3] = *reinterpret_cast<const uint32_t *>(sv + (8 * th + i) * kCodePitch + 4 * dq);
+        transpose4x4(w[0]);
+        transpose4x4(w[1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = sv[(4 * e) * kD + d] | sv[(4 * e + 1) * kD + d] << 8 | sv[(4 * e + 2) * kD + d] << 16 |
-                       static_cast<uint32_t>(sv[(4 * e + 3) * kD + d]) << 24;
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            for (uint32_t m = mask & 0x55555555u; m != 0; m &= m - 1) {
-                const int tt = (__ffs(static_cast<int>(m)) - 1) >> 1;
-                dst[tt] = sv[tt * kD + d];
-            }
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint2 *>(blk + kBlk8V + (4 * dq + e) * kPage + 8 * th) = make_uint2(w[0][e], w[1][e]);
+    } else {
+        for (int tt = t_lo; tt < t_hi; ++tt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) blk[kBlk8V + (lane + 32 * i) * kPage + tt] = sv[tt * kCodePitch + lane + 32 * i];
+    }
+}
+
+// Eight codes times their token's scale as bf16.
+__device__ __forceinline__ uint4 fp8_values8(uint2 c, float s) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint32_t h[2];
+        e4m3x4_to_f16x2x2(w[e], h[0], h[1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[u]));
+            o[2 * e + u] = pack_bf16(f.x * s, f.y * s);
         }
     }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Positions first .. L - 1 (first = starts[b], or 0; at most N of them) of every sequence as bf16
 // rows i = position - first of k_out / v_out [B][N][Hkv][64]: e4m3(code) times the token's scale in
-// fp32, rounded to bf16. Rows past them are not written. One warp per block and KV head, the V
-// codes turned around through shared memory. Positions that a ring has dropped are not there to
-// be read: DA_STATUS_BAD_SEQ_LEN. wide: both outputs start at 32-byte addresses (then one store takes
-// a lane's 16 elements).
+// fp32, rounded to bf16. Rows past them are not written. One warp per block and KV head; eight lanes
+// write a row. The V codes pass through shared memory as they are (a row's 16 tokens every 16 bytes, and 16 bytes more
+// every eight rows, so that the reads of eight rows' words meet no bank twice) and are turned around four by four.
+// Positions that a ring has dropped are not there to be read: DA_STATUS_BAD_SEQ_LEN.
 __global__ void __launch_bounds__(kStoreWarps * 32)
     kv_read_fp8_kernel(const __grid_constant__ BlockParams p, const int32_t *__restrict__ starts, int N,
-                       __nv_bfloat16 *__restrict__ k_out, __nv_bfloat16 *__restrict__ v_out, int wide) {
-    __shared__ __align__(16) uint8_t s_v[kStoreWarps][kPage * kD];
+                       __nv_bfloat16 *__restrict__ k_out, __nv_bfloat16 *__restrict__ v_out) {
+    __shared__ __align__(16) uint8_t s_v[kStoreWarps][(kD + kD / 8) * kPage];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -288,51 +361,39 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
     if (first >= end || blk_i > (end - 1) / kPage) return;
     const uint8_t *blk = block_of(p, b, blk_i, g);
     if (blk == nullptr) return;
-    uint4 kc[2], vc[2];
+    const int pos0 = blk_i * kPage, o = lane & 7;  // elements 8 o .. + 7
+    uint2 kc[4];
+    uint4 vc[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        kc[i] = *(reinterpret_cast<const uint4 *>(blk) + lane + 32 * i);
-        vc[i] = *(reinterpret_cast<const uint4 *>(blk + kBlk8V) + lane + 32 * i);
-    }
+    for (int i = 0; i < 4; ++i) kc[i] = *(reinterpret_cast<const uint2 *>(blk) + lane + 32 * i);  // token lane / 8 + 4 i
+#pragma unroll
+    for (int i = 0; i < 2; ++i) vc[i] = *(reinterpret_cast<const uint4 *>(blk + kBlk8V) + lane + 32 * i);
     const float sc = *(reinterpret_cast<const float *>(blk + kBlk8S) + lane);  // K scales, then V scales
+    uint8_t *sv = s_v[warp];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t w[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w};
+        const int d = lane + 32 * i;
+        *reinterpret_cast<uint4 *>(sv + (d + (d >> 3)) * kPage) = vc[i];
+    }
+    auto row = [&](int t) { return ((static_cast<size_t>(b) * N + (pos0 + t - first)) * p.Hkv + g) * kD + 8 * o; };
+    auto there = [&](int t) { return pos0 + t >= first && pos0 + t < end; };
 #pragma unroll
-        for (int t = 0; t < kPage; ++t) s_v[warp][t * kD + lane + 32 * i] = static_cast<uint8_t>(w[t >> 2] >> (8 * (t & 3)));
+    for (int i = 0; i < 4; ++i) {
+        const int t = (lane >> 3) + 4 * i;
+        const float s = __shfl_sync(0xffffffffu, sc, t);
+        if (there(t)) *reinterpret_cast<uint4 *>(k_out + row(t)) = fp8_values8(kc[i], s);
     }
     __syncwarp();
+    const int t4 = lane >> 3;  // tokens 4 t4 .. + 3
+    uint32_t w[2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) vc[i] = reinterpret_cast<const uint4 *>(s_v[warp])[lane + 32 * i];
+    for (int e = 0; e < 8; ++e) w[e >> 2][e & 3] = *reinterpret_cast<const uint32_t *>(sv + (8 * o + e + o) * kPage + 4 * t4);
+    transpose4x4(w[0]);
+    transpose4x4(w[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // token t, elements 16 (lane % 4) .. + 15
-        const int t = (lane >> 2) + 8 * i, pos = blk_i * kPage + t;
-        const float ks = __shfl_sync(0xffffffffu, sc, t), vs = __shfl_sync(0xffffffffu, sc, kPage + t);
-        if (pos < first || pos >= end) continue;
-        const size_t row = ((static_cast<size_t>(b) * N + (pos - first)) * p.Hkv + g) * kD + 16 * (lane & 3);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const uint4 c = kv == 0 ? kc[i] : vc[i];
-            const float s = kv == 0 ? ks : vs;
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t h[2];
-                e4m3x4_to_f16x2x2(w[e], h[0], h[1]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[u]));
-                    o[2 * e + u] = pack_bf16(f.x * s, f.y * s);
-                }
-            }
-            __nv_bfloat16 *dst = (kv == 0 ? k_out : v_out) + row;
-            if (wide) {
-                st_global_v8(dst, o);
-            } else {
-                reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int t = 4 * t4 + i;
+        const float s = __shfl_sync(0xffffffffu, sc, kPage + t);
+        if (there(t)) *reinterpret_cast<uint4 *>(v_out + row(t)) = fp8_values8(make_uint2(w[0][i], w[1][i]), s);
     }
 }
