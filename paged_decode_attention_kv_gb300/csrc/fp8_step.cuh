@@ -12,10 +12,14 @@
 // the rotation's products and its sum or difference are rounded one by one, as in the other
 // calls with a rotary embedding (without a norm the bits are theirs).
 //
-// Bound by memory: every row is read and written once. Four lanes hold a row, lane j its
-// elements 8 j .. + 7 and 32 + 8 j .. + 7, so that a lane has both halves of its pairs (two
-// 16-byte loads and stores, no exchange for the rotation; two shuffles for the norm). A lane
-// keeps its pairs' cosines and sines over all the rows of a token that its warp takes.
+// Every row is read and written once. Four lanes hold a row, lane j its elements 8 j .. + 7 and
+// 32 + 8 j .. + 7, so that a lane has both halves of its pairs (two 16-byte loads and stores, no exchange for the
+// rotation; two shuffles for the norm). A warp takes eight rows of a token at a time; a lane keeps its pairs' cosines
+// and sines over all of them, with a norm multiplied by the head's weights once: the pair is then
+//     r (x (c w_x) - y (s w_y)),  r (y (c w_y) + x (s w_x)),   r = 1 / sqrt(..),
+// two values per instruction (240 instructions per eight rows had bound the kernel, not memory: 8191 tokens of 80 rows
+// took 36.6 us). The rows come through shared memory, four eights ahead: registers had limited the loads in flight
+// (37.7 us). 31.3 us back to back, 5.4 TB/s of the 6.7 of a plain copy.
 struct RotateParams {
     const __nv_bfloat16 *q, *k, *v;          // token strides below, heads contiguous; v may be null
     __nv_bfloat16 *q_out, *k_out, *v_out;
@@ -29,16 +33,105 @@ struct RotateParams {
     unsigned char axis[kD / 2];              // the axis of each pair
     unsigned char quads;                     // bit i: the pairs 4 i .. 4 i + 3 are of one axis
 };
-#ifndef DA_ROT_BATCH
-#define DA_ROT_BATCH 2
+constexpr int kRotThreads = 128;
+#ifndef DA_ROT_AHEAD
+#define DA_ROT_AHEAD 4
 #endif
+constexpr int kRotAhead = DA_ROT_AHEAD;  // eights of rows on their way
 #ifndef DA_ROT_WARPS
-#define DA_ROT_WARPS 32
+#define DA_ROT_WARPS 16
 #endif
-constexpr int kRotThreads = 128, kRotBatch = DA_ROT_BATCH;
 constexpr int kRotWarps = DA_ROT_WARPS;  // warps per SM that a token's rows are spread over where there are few tokens
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Rows h0 + lane / 4, + 8, .. below h1 of one token's query or key heads (in and out at head 0, this lane's first
+// element). c, s: the lane's pairs' angles, two pairs each; w: the heads' norm weights from this lane's first element on.
+template <bool NORM>
+__device__ __forceinline__ void rotate_rows(const __nv_bfloat16 *in, __nv_bfloat16 *out, int h0, int h1, const float2 (&c)[4],
+                                            const float2 (&s)[4], const float *w, float eps, int lane, uint8_t *stage) {
+    // coefficients of x and y in both results
+    float2 xc[4], ys[4], yc[4], xs[4];
+    if (NORM)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 wx = __ldg(reinterpret_cast<const float2 *>(w) + e), wy = __ldg(reinterpret_cast<const float2 *>(w + kD / 2) + e);
+            xc[e] = mul2(c[e], wx);
+            xs[e] = mul2(s[e], wx);
+            yc[e] = mul2(c[e], wy);
+            ys[e] = mul2(make_float2(-s[e].x, -s[e].y), wy);
+        }
+    const float2 one = make_float2(1.f, 1.f);
+    in += (h0 + (lane >> 2)) * kD;
+    out += (h0 + (lane >> 2)) * kD;
+    // this lane's 32 bytes of the rows kRotAhead eights ahead, copied into its own places of shared memory
+    const uint32_t mine = smem_addr(stage) + 16 * lane;
+    auto fetch = [&](int k) {
+        if (h0 + 8 * k + (lane >> 2) < h1) {
+            const uint32_t dst = mine + k % kRotAhead * 1024;
+            const __nv_bfloat16 *src = in + 8 * k * kD;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(src + kD / 2) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kRotAhead - 1; ++k) fetch(k);
+    for (int k = 0; h0 + 8 * k < h1; ++k, out += 8 * kD) {  // (all lanes stay for the shuffles)
+        const bool live = h0 + 8 * k + (lane >> 2) < h1;
+        fetch(k + kRotAhead - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRotAhead - 1) : "memory");
+        const uint4 a = *reinterpret_cast<const uint4 *>(stage + k % kRotAhead * 1024 + 16 * lane);
+        const uint4 b = *reinterpret_cast<const uint4 *>(stage + k % kRotAhead * 1024 + 512 + 16 * lane);
+        uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        float2 x[4], y[4], r = one;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[e] = unpack_bf16(aw[e]);
+            y[e] = unpack_bf16(bw[e]);
+        }
+        if (NORM) {
+            float2 q = mul2(x[0], x[0]);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) q = fma2(x[e], x[e], q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q = fma2(y[e], y[e], q);
+            float ss = q.x + q.y;
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+            r.x = r.y = rsqrtf(ss * (1.f / kD) + eps);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 o, u;
+            if (NORM) {
+                o = mul2(r, fma2(x[e], xc[e], mul2(y[e], ys[e])));
+                u = mul2(r, fma2(y[e], yc[e], mul2(x[e], xs[e])));
+            } else {  // every product and sum rounded by itself
+                o = make_float2(__fsub_rn(__fmul_rn(x[e].x, c[e].x), __fmul_rn(y[e].x, s[e].x)),
+                                __fsub_rn(__fmul_rn(x[e].y, c[e].y), __fmul_rn(y[e].y, s[e].y)));
+                u = make_float2(__fadd_rn(__fmul_rn(y[e].x, c[e].x), __fmul_rn(x[e].x, s[e].x)),
+                                __fadd_rn(__fmul_rn(y[e].y, c[e].y), __fmul_rn(x[e].y, s[e].y)));
+            }
+            aw[e] = pack_bf16(o.x, o.y);
+            bw[e] = pack_bf16(u.x, u.y);
+        }
+        if (live) {
+            *reinterpret_cast<uint4 *>(out) = make_uint4(aw[0], aw[1], aw[2], aw[3]);
+            *reinterpret_cast<uint4 *>(out + kD / 2) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_constant__ RotateParams p) {
+    __shared__ __align__(16) uint8_t s_rows[kRotThreads / 32][kRotAhead * 1024];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -46,10 +139,10 @@ __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_
     const long long item = static_cast<long long>(blockIdx.x) * (kRotThreads / 32) + warp;
     const long long tok = item / chunks;
     if (tok >= p.N) return;
-    const int r_begin = static_cast<int>(item - tok * chunks) * p.chunk, r_end = min(r_begin + p.chunk, p.rows);
-    const int j = lane & 3;
-    float c[8], s[8];
-    if (r_begin < p.Hq + p.Hkv) {
+    const int r0 = static_cast<int>(item - tok * chunks) * p.chunk, r1 = min(r0 + p.chunk, p.rows);
+    const int j = lane & 3, Hqk = p.Hq + p.Hkv;
+    if (r0 < Hqk) {
+        float2 c[4], s[4];
         bool bad = false;
         auto row_of = [&](int a) {
             const int pos = __ldg(p.positions + static_cast<long long>(a) * p.N + tok);
@@ -60,83 +153,40 @@ __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i0 = 8 * j + 4 * h;
+            float cv[4], sv[4];
             if (p.quads >> (i0 >> 2) & 1) {
                 const size_t at = row_of(p.axis[i0]) + i0;
-                const float4 cv = __ldg(reinterpret_cast<const float4 *>(p.rope_cos + at));
-                const float4 sv = __ldg(reinterpret_cast<const float4 *>(p.rope_sin + at));
-                c[4 * h] = cv.x, c[4 * h + 1] = cv.y, c[4 * h + 2] = cv.z, c[4 * h + 3] = cv.w;
-                s[4 * h] = sv.x, s[4 * h + 1] = sv.y, s[4 * h + 2] = sv.z, s[4 * h + 3] = sv.w;
+                const float4 c4 = __ldg(reinterpret_cast<const float4 *>(p.rope_cos + at));
+                const float4 s4 = __ldg(reinterpret_cast<const float4 *>(p.rope_sin + at));
+                cv[0] = c4.x, cv[1] = c4.y, cv[2] = c4.z, cv[3] = c4.w;
+                sv[0] = s4.x, sv[1] = s4.y, sv[2] = s4.z, sv[3] = s4.w;
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const size_t at = row_of(p.axis[i0 + e]) + i0 + e;
-                    c[4 * h + e] = __ldg(p.rope_cos + at);
-                    s[4 * h + e] = __ldg(p.rope_sin + at);
+                    cv[e] = __ldg(p.rope_cos + at);
+                    sv[e] = __ldg(p.rope_sin + at);
                 }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                c[2 * h + e] = make_float2(cv[2 * e], cv[2 * e + 1]);
+                s[2 * h + e] = make_float2(sv[2 * e], sv[2 * e + 1]);
             }
         }
         if (bad) flag_status(DA_STATUS_BAD_POSITION);
+        auto rows = [&](const __nv_bfloat16 *in, __nv_bfloat16 *out, int h0, int h1, const float *w) {
+            if (h0 >= h1) return;
+            if (w != nullptr)
+                rotate_rows<true>(in + 8 * j, out + 8 * j, h0, h1, c, s, w + 8 * j, p.eps, lane, s_rows[warp]);
+            else
+                rotate_rows<false>(in + 8 * j, out + 8 * j, h0, h1, c, s, nullptr, 0.f, lane, s_rows[warp]);
+        };
+        rows(p.q + tok * p.q_ld, p.q_out + tok * p.qo_ld, r0, min(r1, p.Hq), p.q_weight);
+        rows(p.k + tok * p.k_ld, p.k_out + tok * p.ko_ld, max(r0 - p.Hq, 0), min(r1 - p.Hq, p.Hkv), p.k_weight);
     }
-    // two rows at a time: their loads are in flight together
-    for (int r0 = r_begin + (lane >> 2); r0 - (lane >> 2) < r_end; r0 += 8 * kRotBatch) {  // (all lanes stay for the shuffles)
-        uint4 a[kRotBatch], b[kRotBatch];
-        __nv_bfloat16 *dst[kRotBatch];
-        int kind[kRotBatch];  // q, k, v, or no row
-#pragma unroll
-        for (int i = 0; i < kRotBatch; ++i) {
-            const int r = r0 + 8 * i;
-            kind[i] = r >= r_end ? 3 : r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2;
-            const int h = (kind[i] == 0 ? r : kind[i] == 1 ? r - p.Hq : r - p.Hq - p.Hkv) * kD + 8 * j;
-            const __nv_bfloat16 *src = (kind[i] == 0 ? p.q + tok * p.q_ld : kind[i] == 1 ? p.k + tok * p.k_ld : p.v + tok * p.v_ld) + h;
-            dst[i] = (kind[i] == 0 ? p.q_out + tok * p.qo_ld : kind[i] == 1 ? p.k_out + tok * p.ko_ld : p.v_out + tok * p.vo_ld) + h;
-            a[i] = b[i] = make_uint4(0, 0, 0, 0);
-            if (kind[i] < 3) {
-                a[i] = *reinterpret_cast<const uint4 *>(src);
-                b[i] = *reinterpret_cast<const uint4 *>(src + kD / 2);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRotBatch; ++i) {
-            const float *w = kind[i] == 0 ? p.q_weight : kind[i] == 1 ? p.k_weight : nullptr;
-            uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-            float x[8], y[8], ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 u = unpack_bf16(aw[e]), v = unpack_bf16(bw[e]);
-                x[2 * e] = u.x, x[2 * e + 1] = u.y, y[2 * e] = v.x, y[2 * e + 1] = v.y;
-                ss += u.x * u.x + u.y * u.y + v.x * v.x + v.y * v.y;
-            }
-            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-            if (kind[i] == 3) continue;
-            if (w != nullptr) {
-                const float rms = 1.f / sqrtf(ss * (1.f / kD) + p.eps);
-#pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 wa = __ldg(reinterpret_cast<const float4 *>(w + 8 * j + e));
-                    const float4 wb = __ldg(reinterpret_cast<const float4 *>(w + kD / 2 + 8 * j + e));
-                    x[e] *= rms * wa.x, x[e + 1] *= rms * wa.y, x[e + 2] *= rms * wa.z, x[e + 3] *= rms * wa.w;
-                    y[e] *= rms * wb.x, y[e + 1] *= rms * wb.y, y[e + 2] *= rms * wb.z, y[e + 3] *= rms * wb.w;
-                }
-            }
-            if (kind[i] < 2) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float o[2], u[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int n = 2 * e + k;
-                        o[k] = __fsub_rn(__fmul_rn(x[n], c[n]), __fmul_rn(y[n], s[n]));
-                        u[k] = __fadd_rn(__fmul_rn(y[n], c[n]), __fmul_rn(x[n], s[n]));
-                    }
-                    aw[e] = pack_bf16(o[0], o[1]);
-                    bw[e] = pack_bf16(u[0], u[1]);
-                }
-            }
-            *reinterpret_cast<uint4 *>(dst[i]) = make_uint4(aw[0], aw[1], aw[2], aw[3]);
-            *reinterpret_cast<uint4 *>(dst[i] + kD / 2) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
-        }
-    }
+    for (int h = max(r0 - Hqk, 0) + (lane >> 3); h < r1 - Hqk; h += 4)  // value rows, eight lanes each
+        reinterpret_cast<uint4 *>(p.v_out + tok * p.vo_ld + h * kD)[lane & 7] = reinterpret_cast<const uint4 *>(p.v + tok * p.v_ld + h * kD)[lane & 7];
 }
 
 // ------------------------------------------------------------------ fp8 blocks written and read back
@@ -184,8 +234,7 @@ struct RowScale {
     }
     __device__ __forceinline__ float quotient(float x) const {
         const float q = __fmul_rn(x, r);
-        const float y = __fmaf_rn(__fmaf_rn(-q, scale, x), r, q);
-        return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // (-0 stays -0)
+        return __fmaf_rn(-__fmaf_rn(q, scale, -x), r, q);  // (the remainder's negative: so that -0 stays -0)
     }
 };
 // Eight bf16 values of a row (16 bytes) to their codes.
@@ -207,10 +256,10 @@ __device__ __forceinline__ uint2 fp8_codes8(const uint4 &v, const RowScale &s) {
     }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
-// The larger magnitudes of two pairs of bf16 values (a NaN loses against a number, as in fmaxf).
+// The larger magnitudes of two pairs of bf16 values, of whatever sign (a NaN loses against a number, as in fmaxf).
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
     uint32_t d;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7fff7fffu));
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w));
     return d;
 }
 // Four words of four bytes, turned around: word i of the result holds byte i of each.
@@ -277,12 +326,12 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
             const int tt = t + 8 * h;
             const bool live = tt >= t_lo && tt < t_hi;
             const uint4 &a = raw[kv][h][0], &c = raw[kv][h][1];
-            uint32_t m = abs_max2(abs_max2(a.x & 0x7fff7fffu, a.y), abs_max2(a.z & 0x7fff7fffu, a.w));
-            m = abs_max2(m, abs_max2(abs_max2(c.x & 0x7fff7fffu, c.y), abs_max2(c.z & 0x7fff7fffu, c.w)));
+            uint32_t m = abs_max2(abs_max2(a.x, a.y), abs_max2(a.z, a.w));
+            m = abs_max2(m, abs_max2(abs_max2(c.x, c.y), abs_max2(c.z, c.w)));
             m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const float2 top = unpack_bf16(m);
-            const RowScale rs(fmaxf(top.x, top.y), rule);
+            const RowScale rs(fmaxf(fabsf(top.x), fabsf(top.y)), rule);
             const uint2 ca = fp8_codes8(a, rs), cc = fp8_codes8(c, rs);
             if (kv == 0) {
                 if (live) {
