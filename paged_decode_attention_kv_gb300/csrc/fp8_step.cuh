@@ -6,6 +6,15 @@
 // Included into decode_attn.cu (inside its anonymous namespace): one translation unit, sharing
 // the fp8 helpers and the status word.
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // ------------------------------------------------------------------ norms and rotation
 // Row x of 64 values of one head: y = x w / sqrt(sum(x^2) / 64 + eps) (no norm: y = x), then the
 // pairs (i, i + 32) rotated by row pos[axis(i)] of the tables. All in fp32, rounded once to bf16;
@@ -42,15 +51,6 @@ constexpr int kRotAhead = DA_ROT_AHEAD;  // eights of rows on their way
 #define DA_ROT_WARPS 16
 #endif
 constexpr int kRotWarps = DA_ROT_WARPS;  // warps per SM that a token's rows are spread over where there are few tokens
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
 
 // Rows h0 + lane / 4, + 8, .. below h1 of one token's query or key heads (in and out at head 0, this lane's first
 // element). c, s: the lane's pairs' angles, two pairs each; w: the heads' norm weights from this lane's first element on.
@@ -232,29 +232,35 @@ struct RowScale {
         fast = top >= 1e-20f && top <= 1e30f;
         r = fast ? __frcp_rn(scale) : 0.f;
     }
-    __device__ __forceinline__ float quotient(float x) const {
-        const float q = __fmul_rn(x, r);
-        return __fmaf_rn(-__fmaf_rn(q, scale, -x), r, q);  // (the remainder's negative: so that -0 stays -0)
+    __device__ __forceinline__ float2 quotients(float2 x) const {
+        const float2 q = mul2(x, make_float2(r, r)), d = fma2(q, make_float2(scale, scale), make_float2(-x.x, -x.y));
+        return fma2(make_float2(-d.x, -d.y), make_float2(r, r), q);  // (the remainder's negative: so that -0 stays -0)
     }
 };
+// Four values to e4m3 codes (nearest, ties to even, saturating at +-448; NaN: 0x7f), low byte first.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float2 a, float2 b) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(d)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 // Eight bf16 values of a row (16 bytes) to their codes.
 __device__ __forceinline__ uint2 fp8_codes8(const uint4 &v, const RowScale &s) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[4];
+    float2 q[4];
     if (s.fast) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16(w[e]);
-            c[e] = f32x2_to_e4m3x2(s.quotient(f.x), s.quotient(f.y));
-        }
+        for (int e = 0; e < 4; ++e) q[e] = s.quotients(unpack_bf16(w[e]));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 f = unpack_bf16(w[e]);
-            c[e] = f32x2_to_e4m3x2(__fdiv_rn(f.x, s.scale), __fdiv_rn(f.y, s.scale));
+            q[e] = make_float2(__fdiv_rn(f.x, s.scale), __fdiv_rn(f.y, s.scale));
         }
     }
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    return make_uint2(f32x4_to_e4m3x4(q[0], q[1]), f32x4_to_e4m3x4(q[2], q[3]));
 }
 // The larger magnitudes of two pairs of bf16 values, of whatever sign (a NaN loses against a number, as in fmaxf).
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
@@ -302,8 +308,6 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
     const int unit = blockIdx.x * kStoreWarps + warp;
     const int blk_i = first / kPage + unit / p.Hkv, g = unit % p.Hkv;
     if (blk_i > (L - 1) / kPage) return;
-    uint8_t *blk = block_of(p, b, blk_i, g);
-    if (blk == nullptr) return;
     const int pos0 = blk_i * kPage, t_lo = max(0, first - pos0), t_hi = min(kPage, L - pos0);  // tokens [t_lo, t_hi)
     const int t = lane >> 2, j = lane & 3;
     uint4 raw[2][2][2];  // K, V; token t, t + 8; elements 8 j, 32 + 8 j
@@ -318,6 +322,8 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
             raw[1][h][i] = live ? __ldg(reinterpret_cast<const uint4 *>(v_new + src + 32 * i)) : make_uint4(0, 0, 0, 0);
         }
     }
+    uint8_t *blk = block_of(p, b, blk_i, g);  // (read while the rows are on their way)
+    if (blk == nullptr) return;
     uint8_t *sv = s_v[warp];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
