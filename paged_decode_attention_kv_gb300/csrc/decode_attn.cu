@@ -3063,7 +3063,8 @@ int launch_blocks_grid(long long positions, long long most, int Hkv, int batch, 
 
 int run_append_fp8(const void *k_new, const void *v_new, void *kv_cache, const int32_t *block_table,
                    const int32_t *seq_lens, const int32_t *q_lens, int window, int scale_rule, const da_shape &s, int T,
-                   int page_size, int max_pages, int num_pages, int max_seq_len, void *stream) {
+                   int page_size, int max_pages, int num_pages, int max_seq_len, void *stream, int *clear = nullptr,
+                   int n_clear = 0) {
     int rc = check_blocks(kv_cache, block_table, seq_lens, window, s, page_size, max_pages, num_pages, max_seq_len);
     if (rc != DA_OK) return rc;
     if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || T <= 0) return DA_ERR_INVALID_ARG;
@@ -3075,7 +3076,8 @@ int run_append_fp8(const void *k_new, const void *v_new, void *kv_cache, const i
     const BlockParams p = {static_cast<uint8_t *>(kv_cache), block_table, seq_lens, s.num_kv_heads,
                            block_table ? 0 : window, block_table ? max_pages : 0, block_table ? num_pages : 0, max_seq_len};
     return launch_pdl(kv_append_fp8_kernel, grid, kStoreWarps * 32, 0, static_cast<cudaStream_t>(stream), p,
-                      static_cast<const __nv_bfloat16 *>(k_new), static_cast<const __nv_bfloat16 *>(v_new), q_lens, T, scale_rule);
+                      static_cast<const __nv_bfloat16 *>(k_new), static_cast<const __nv_bfloat16 *>(v_new), q_lens, T, scale_rule,
+                      clear, n_clear);
 }
 
 int run_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,
@@ -3114,7 +3116,8 @@ MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, 
     // segments so few that each is spread over four CTAs or more, if they are about equally long
     m.defer = m.groups * DA_T8_DEFER <= static_cast<long long>(kT8CtasPerSm) * sms;
     m.counter_bytes = static_cast<size_t>(kMMaxGroups) * sizeof(int);
-    m.part_bytes = static_cast<size_t>(kT8CtasPerSm) * sms * 2 * kT8SlotFloats * sizeof(float);
+    // two slots per CTA, then its counters (not among those that are zero at rest: every call clears them itself)
+    m.part_bytes = static_cast<size_t>(kT8CtasPerSm) * sms * 2 * kT8SlotFloats * sizeof(float) + kT8Counters * sizeof(int);
     return m;
 }
 
@@ -3135,6 +3138,7 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
     int dev;
     rc = current_device(&dev);
     if (rc != DA_OK) return rc;
+    if (kT8CtasPerSm * sm_count(dev) * 4 > kT8Counters) return DA_ERR_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     const MultiPlan m = multi_fp8_plan(s, T, window, max_seq_len, sm_count(dev));
     if (static_cast<long long>(s.batch) * m.row_blocks > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
@@ -3162,9 +3166,10 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
         if (e != cudaSuccess) return set_cuda_error(e);
         g_dev[dev].fp8_multi_attr_set.store(true, std::memory_order_release);
     }
-    // the new tokens first: the attention reads every key from the cache
+    // the new tokens first: the attention reads every key from the cache (and finds its counters at zero)
+    int *counters = reinterpret_cast<int *>(static_cast<char *>(ws) + m.counter_bytes + m.part_bytes) - kT8Counters;
     rc = run_append_fp8(k_new, v_new, kv_cache, block_table, seq_lens, q_lens, 0, scale_rule, s, T, page_size, max_pages,
-                        num_pages, max_seq_len, stream_v);
+                        num_pages, max_seq_len, stream_v, counters, 4 * kT8CtasPerSm * sm_count(dev));
     if (rc != DA_OK) return rc;
     MultiParams prm = {};
     prm.q = static_cast<const __nv_bfloat16 *>(q);
@@ -3184,14 +3189,14 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
     prm.num_pages = num_pages;
     prm.max_seq_len = max_seq_len;
     prm.row_blocks = m.row_blocks;
-    prm.counters = static_cast<int *>(ws);
+    prm.counters = counters;
     prm.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
     prm.defer = m.defer ? 1 : 0;
     const unsigned grid = static_cast<unsigned>(kT8CtasPerSm * sm_count(dev));
     rc = launch_pdl(multi_tc8_kernel, dim3(grid), kT8Threads, kT8Smem, stream, prm, static_cast<const uint8_t *>(kv_cache));
     if (rc != DA_OK || !m.defer) return rc;
     return launch_pdl(t8_combine_kernel,
-                      dim3(static_cast<unsigned>(m.row_blocks * (kT8Rows / kT8FoldWarps)), static_cast<unsigned>(s.num_kv_heads),
+                      dim3(static_cast<unsigned>(m.row_blocks * 4), static_cast<unsigned>(s.num_kv_heads),
                            static_cast<unsigned>(s.batch)),
                       kT8FoldWarps * 32, 0, stream, prm, static_cast<int>(grid));
 }

@@ -283,17 +283,20 @@ __device__ __forceinline__ void transpose4x4(uint32_t (&w)[4]) {
 // 8 j .. + 7 and 32 + 8 j .. + 7 of tokens t' and t' + 8 of the block, so that every load and every store of codes is
 // made of whole sectors. The V codes are turned around, four by four bytes, on their way through the warp's shared
 // memory; a block that is filled by this call is written in whole words, one that is shared with earlier tokens
-// gets its new bytes only.
+// gets its new bytes only. clear: counters of the attention that follows in the same call (multi_tc8_kernel).
 constexpr int kStoreWarps = 4;
 constexpr int kCodePitch = 72;  // bytes from one token's codes to the next: the turning reads meet no bank twice
 __global__ void __launch_bounds__(kStoreWarps * 32)
     kv_append_fp8_kernel(const __grid_constant__ BlockParams p, const __nv_bfloat16 *__restrict__ k_new,
-                         const __nv_bfloat16 *__restrict__ v_new, const int32_t *__restrict__ q_lens, int T, int rule) {
+                         const __nv_bfloat16 *__restrict__ v_new, const int32_t *__restrict__ q_lens, int T, int rule,
+                         int *clear, int n_clear) {
     __shared__ __align__(16) uint8_t s_v[kStoreWarps][kPage * kCodePitch];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
+    if (blockIdx.x == 0 && b == 0)
+        for (int i = threadIdx.x; i < n_clear; i += blockDim.x) clear[i] = 0;
     const int L = __ldg(p.seq_lens + b);
     const int n = q_lens != nullptr ? __ldg(q_lens + b) : T;
     bool bad = L < 0 || n < 0 || n > T || (L > 0 && n > L);

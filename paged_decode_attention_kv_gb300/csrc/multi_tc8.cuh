@@ -58,7 +58,7 @@ constexpr int kT8HalfBytes = kT8Keys * kD * 2;  // 8 KiB of K' (or V')
 constexpr int kT8StageBytes = 2 * kT8HalfBytes;
 constexpr int kT8QBytes = kT8Rows * kD * 2;
 constexpr int kT8RawBytes = kT8Tiles * kT8Raw * kBlk8Bytes;
-constexpr int kT8Bars = 2 * kT8Raw + 2 * kT8Stages + 4 * 2 + 1;
+constexpr int kT8Bars = 2 * kT8Raw + 2 * kT8Stages + 5 * 2 + 1;
 constexpr int kT8Smem = 1024 + 2 * kT8QBytes + kT8Stages * kT8StageBytes + kT8RawBytes + kT8Stages * kT8Tiles * 16 + kT8Bars * 8;
 constexpr int kT8Warps = 16, kT8Threads = kT8Warps * 32, kT8CtasPerSm = 2;
 static_assert(kT8CtasPerSm * (kT8Smem + 1024 + 1024) <= 233472, "two CTAs' shared memory on one SM");
@@ -66,8 +66,9 @@ static_assert((kMaxBatch + 1) * 8 <= kT8Stages * kT8StageBytes, "the prefix of u
 constexpr uint32_t kT8TmemCols = 256, kT8ColS = 0, kT8ColO = 128, kT8ColP = 192;  // S and P: two buffers each
 constexpr float kT8Shift = 7.f, kT8TileMax = 32768.f;  // log2 of the probabilities' unit; the most a tile's may add up to
 constexpr int kT8MaxE = 100, kT8MaxF = 60;
+constexpr int kT8Counters = 4 * kT8CtasPerSm * kMaxSms;  // arrivals at a shared segment: one per row warp, at its first CTA
 constexpr int kT8MinUnits = 4;                         // units per CTA at least, where there are so few
-constexpr size_t kT8SlotFloats = static_cast<size_t>(kT8Rows) * kMSlotFloats;
+constexpr size_t kT8SlotFloats = static_cast<size_t>(kT8Rows) * (2 + kD);
 
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -200,81 +201,60 @@ struct T8Walk {
     }
 };
 
-// Row rl of a segment's partials: contributor i of `count`, the first one in its CTA's slot k0, the others in slot 0.
-__device__ __forceinline__ const float *t8_slot(const MultiParams &p, int c0, int k0, int i, int rl) {
-    return p.part + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? k0 : 0)) * kT8SlotFloats + static_cast<size_t>(rl) * kMSlotFloats;
+// What the row warps need of a segment, from the warps that load its query rows.
+struct T8Seg {
+    int b, g, rb, n, base;        // base: position of the first new token
+    int pt_lo, u0, u1, units;     // first tile; the CTA's units [u0, u1) of all
+    int last;
+    long long begin;              // the segment's first unit among the call's
+};
+
+// Partials of a segment: m [128 rows], l [128 rows], O as [16][128 rows] float4 (so that 32 rows' loads and stores are
+// contiguous). Contributor i: the first one's in its CTA's slot k0, the others' in slot 0.
+__device__ __forceinline__ const float *t8_slot(const MultiParams &p, int c0, int k0, int i) {
+    return p.part + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? k0 : 0)) * kT8SlotFloats;
+}
+__device__ __forceinline__ const float4 *t8_acc(const float *slot, int c, int rl) {
+    return reinterpret_cast<const float4 *>(slot + 2 * kT8Rows) + c * kT8Rows + rl;
 }
 
-// One row's partials folded with the sink by a warp; every lane returns output elements 2 lane, 2 lane + 1.
-__device__ __forceinline__ uint32_t t8_fold_row(const MultiParams &p, int c0, int k0, int count, int rl, int head, int lane) {
-    float M = -INFINITY, den = 0.f;
-    for (int i = lane; i < count; i += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(t8_slot(p, c0, k0, i, rl)));
-        if (ml.x == -INFINITY) continue;  // no key of the row there
-        const float Mn = fmaxf(M, ml.x);
-        den = den * exp2f(M - Mn) + ml.y * exp2f(ml.x - Mn);
-        M = Mn;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float Mo = __shfl_xor_sync(0xffffffffu, M, off), Do = __shfl_xor_sync(0xffffffffu, den, off);
-        const float Mn = fmaxf(M, Mo);
-        den = Mn == -INFINITY ? 0.f : den * exp2f(M - Mn) + Do * exp2f(Mo - Mn);
-        M = Mn;
-    }
-    const float sg = p.sinks != nullptr ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
-    const float Mf = fmaxf(M, sg);  // the same on every lane: an exact maximum
-    if (Mf == -INFINITY) return 0u;
-    const float d = den * exp2f(M - Mf) + (sg == -INFINITY ? 0.f : exp2f(sg - Mf));
-    const float inv = d > 0.f ? 1.f / d : d == d ? 0.f : d;
-    float x0 = 0.f, x1 = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {  // independent loads: several in flight
-        const float *s = t8_slot(p, c0, k0, i, rl);
-        const float m = __ldcg(s);
-        const float2 a = __ldcg(reinterpret_cast<const float2 *>(s + kMAccOff) + lane);
-        const float w = m == -INFINITY ? 0.f : exp2f(m - Mf);
-        x0 += a.x * w;
-        x1 += a.y * w;
-    }
-    return pack_bf16(x0 * inv, x1 * inv);
-}
-
-// The same by one thread, 16 bytes at a time: for the CTA that folds 128 rows of a few partials at once (a warp a row
-// leaves a chain of dependent loads for each of a warp's 32 rows).
-__device__ __noinline__ void t8_fold_thread(const MultiParams &p, int c0, int k0, int count, int rl, int head, bool query, uint4 *out) {
+// A row's partials folded with the sink by one thread, for the CTA that folds a few of them.
+__device__ __noinline__ void t8_fold(const MultiParams &p, int c0, int k0, int count, int rl, int head, bool query, uint4 *out) {
     float M = -INFINITY;
-    if (query)
-        for (int i = 0; i < count; ++i) M = fmaxf(M, __ldcg(t8_slot(p, c0, k0, i, rl)));
+    if (query) {
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) M = fmaxf(M, __ldcg(t8_slot(p, c0, k0, i) + rl));
+    }
     const float sg = query && p.sinks != nullptr ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
     const float Mf = fmaxf(M, sg);
     float d = sg == -INFINITY ? 0.f : exp2f(sg - Mf);
-    if (Mf != -INFINITY)
+    if (Mf != -INFINITY) {
+#pragma unroll 4
         for (int i = 0; i < count; ++i) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(t8_slot(p, c0, k0, i, rl)));
-            if (ml.x != -INFINITY) d += ml.y * exp2f(ml.x - Mf);
+            const float m = __ldcg(t8_slot(p, c0, k0, i) + rl), l = __ldcg(t8_slot(p, c0, k0, i) + kT8Rows + rl);
+            d += m == -INFINITY ? 0.f : l * exp2f(m - Mf);
         }
+    }
     const float inv = d > 0.f ? 1.f / d : d == d ? 0.f : d;
 #pragma unroll 1
-    for (int h = 0; h < 4; ++h) {
-        float4 o[4];
+    for (int h = 0; h < 2; ++h) {
+        float4 o[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < 8; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (Mf != -INFINITY)
             for (int i = 0; i < count; ++i) {
-                const float *s = t8_slot(p, c0, k0, i, rl);
-                const float m = __ldcg(s);
-                const float4 *acc = reinterpret_cast<const float4 *>(s + kMAccOff) + 4 * h;
-                const float w = m == -INFINITY ? 0.f : exp2f(m - Mf);
+                const float *s = t8_slot(p, c0, k0, i);
+                const float m = __ldcg(s + rl), w = m == -INFINITY ? 0.f : exp2f(m - Mf);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 x = __ldcg(acc + c);
+                for (int c = 0; c < 8; ++c) {
+                    const float4 x = __ldcg(t8_acc(s, 8 * h + c, rl));
+                    if (w == 0.f) continue;  // (no key there: the accumulator was not written)
                     o[c].x += x.x * w, o[c].y += x.y * w, o[c].z += x.z * w, o[c].w += x.w * w;
                 }
             }
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            out[2 * h + c] = make_uint4(pack_bf16(o[2 * c].x * inv, o[2 * c].y * inv), pack_bf16(o[2 * c].z * inv, o[2 * c].w * inv),
+        for (int c = 0; c < 4; ++c)
+            out[4 * h + c] = make_uint4(pack_bf16(o[2 * c].x * inv, o[2 * c].y * inv), pack_bf16(o[2 * c].z * inv, o[2 * c].w * inv),
                                         pack_bf16(o[2 * c + 1].x * inv, o[2 * c + 1].y * inv), pack_bf16(o[2 * c + 1].z * inv, o[2 * c + 1].w * inv));
     }
 }
@@ -291,13 +271,12 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
     const uint32_t raw_full = smem_addr(bars), raw_empty = raw_full + 8 * kT8Raw;
     const uint32_t kv_full = raw_empty + 8 * kT8Raw, kv_empty = kv_full + 8 * kT8Stages;
     const uint32_t s_full = kv_empty + 8 * kT8Stages, p_full = s_full + 16, o_done = p_full + 16;
-    const uint32_t q_full = o_done + 16, drain = q_full + 16;
+    const uint32_t q_full = o_done + 16, q_free = q_full + 16, drain = q_free + 16;
     __shared__ __align__(16) uint32_t s_vfac[2 * kT8Tiles][kPage / 2];  // V factors of a tile: 16 fp16 values
     // a raw tile's tokens that are keys: [x & 255, x >> 8 & 255), none where there is no page; bit 16: its unit is the
     // segment's first here
     __shared__ int s_keys[kT8Raw][kT8Tiles];
-    __shared__ T8Walk s_walk[4][2];  // a row warp's segment and its next one, out of the registers' way
-    __shared__ long long s_begin[4];
+    __shared__ T8Seg s_seg[4];
     __shared__ int4 s_start;
     __shared__ long long s_range[3];  // the CTA's first unit, its units, all units
     __shared__ uint32_t s_tmem;
@@ -316,7 +295,9 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             mbar_init(s_full + 8 * s, 2);  // the products, and the issuing thread
             mbar_init(p_full + 8 * s, 4);  // the four row warps
             mbar_init(o_done + 8 * s, 1);
-            mbar_init(q_full + 8 * s, 4);
+            mbar_init(q_full + 8 * s, 2);  // the two warps that load query rows
+            mbar_init(q_free + 8 * s, 5);  // the segment's products done, and the row warps past q_full (the products of a
+                                           // segment of one unit can be done before the rows have looked)
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -326,7 +307,8 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                      "r"(kT8TmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The kernel before is this call's append, which waited for everything before it and let this one start only
+    // then: all but the cache may be read, and the output written, at once. Warp 13, which copies from the cache, waits.
 
     // ---- the CTA's units; the output rows that have no query: zeros
     long long *pre = reinterpret_cast<long long *>(sKV);
@@ -506,6 +488,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
         }
     } else if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 13) asm volatile("griddepcontrol.wait;" ::: "memory");  // (also without units: the kernels after wait for this one alone)
         if (warp == 13 && units > 0) {
             // ---- copies: lane u < 4 the block of tile u of every unit
             const uint64_t policy = evict_first_policy();
@@ -558,6 +541,46 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             // nothing may still be landing when the CTA leaves: the last copy of every raw block
             for (int k = max(0, i - kT8Raw); k < i; ++k) mbar_wait_idle(raw_full + 8 * (k % kT8Raw), (k / kT8Raw) & 1);
             __syncwarp();
+        } else if (warp >= 14 && units > 0) {
+            // ---- query rows as fp16 (zeros past the valid ones), 64 by each of the two warps, a segment ahead of the rows
+            T8Walk w;
+            w.start(p, s_start, units);
+            long long begin = s_range[0] - w.u0;
+            bool more = true;
+            for (int k = 0; more; ++k) {
+                const int buf = k & 1;
+                if (k >= 2 && __any_sync(0xffffffffu, !mbar_wait_idle(q_free + 8 * buf, ((k >> 1) - 1) & 1))) {
+                    failed = true;
+                    break;
+                }
+                T8Walk ahead = w;
+                more = ahead.next(p);
+                if (warp == 14 && lane == 0)  // (the rows are past segment k - 3: they have looked at segment k - 2)
+                    s_seg[k & 3] = T8Seg{w.b, w.g, w.rb, w.seq.n, w.seq.L - w.seq.n, w.keys.pt_lo, w.u0, w.u1, w.keys.units, more ? 0 : 1, begin};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int rl = (warp - 14) * 64 + 32 * h + lane, r = w.rb * kT8Rows + rl, t = r / p.G;
+                    const bool ok = t < w.seq.n;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        p.q + (ok ? ((static_cast<size_t>(w.b) * p.T + t) * p.Hq + w.g * p.G + (r - t * p.G)) * kD : 0));
+                    uint8_t *dst = sQ + buf * kT8QBytes + rl * 128;
+#pragma unroll
+                    for (int c0 = 0; c0 < 8; c0 += 4) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) v[c] = ok ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            *reinterpret_cast<uint4 *>(dst + (((c0 + c) ^ (rl & 7)) << 4)) =
+                                make_uint4(bf16x2_to_f16x2(v[c].x), bf16x2_to_f16x2(v[c].y), bf16x2_to_f16x2(v[c].z), bf16x2_to_f16x2(v[c].w));
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the tensor cores
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full + 8 * buf);
+                begin += w.keys.units;
+                w = ahead;
+            }
         } else if (warp == 12 && units > 0) {
         // ---- MMA issuer: S_i = Q K'_i^T, then O += P_{i-1} V'_{i-1}
         const bool leader = elect_one();
@@ -577,6 +600,8 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 }
                 fresh = __float_as_int(s_fac[s * kT8Tiles].w) != 0;
                 if (fresh) {
+                    if (leader && seg >= 0) umma_commit(q_free + 8 * (seg & 1));  // the last segment's products are all issued
+                    __syncwarp();
                     ++seg;
                     if (!wait_all(q_full + 8 * (seg & 1), (seg >> 1) & 1)) {
                         failed = true;
@@ -624,61 +649,28 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
         // ---- query rows: one per thread
         if (units > 0) {
         const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-        auto row_off = [&](const T8Walk &x, int r) {
-            const int t = r / p.G, hl = r - t * p.G;
-            return ((static_cast<size_t>(x.b) * p.T + t) * p.Hq + x.g * p.G + hl) * kD;
-        };
-        // a segment's query rows as fp16, zeros past its valid ones, into buffer buf
-        auto load_q = [&](const T8Walk &x, int buf) {
-            const int r = x.rb * kT8Rows + tid;
-            const bool ok = r < x.seq.n * p.G;
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (ok ? row_off(x, r) : 0));
-            uint8_t *dst = sQ + buf * kT8QBytes + tid * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint4 v = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
-                *reinterpret_cast<uint4 *>(dst + ((c ^ (tid & 7)) << 4)) = v;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the tensor cores
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full + 8 * buf);
-        };
-        {
-            T8Walk w;
-            w.start(p, s_start, units);
-            load_q(w, 0);
-            if (lane == 0) {
-                s_walk[warp][1] = w;
-                s_begin[warp] = s_range[0] - w.u0;  // the segment's first unit among all
-            }
-            __syncwarp();
-        }
-        int i = 0, seg = 0, st = 0;
-        bool more = true;
-        while (more) {  // (a warp that gave up still counts itself at its shared segments, whose counters return to zero)
+        int i = 0, st = 0;
+        for (int seg = 0; !failed; ++seg) {
             int pr, lor, jf, count;  // the row's keys [lor, pr], the unit's first position, the segment's units here
             bool valid, warp_active;
+            float sink = -INFINITY;  // log2 units
+            if (__any_sync(0xffffffffu, !mbar_wait_bounded(q_full + 8 * (seg & 1), (seg >> 1) & 1))) {
+                failed = true;
+                break;
+            }
             {
-                T8Walk w = s_walk[warp][1];
-                const int r = w.rb * kT8Rows + tid, r_valid = min(p.T, w.seq.n) * p.G;
+                const T8Seg &w = s_seg[seg & 3];
+                const int r = w.rb * kT8Rows + tid, r_valid = w.n * p.G, t = r / p.G;
                 valid = r < r_valid;
                 warp_active = w.rb * kT8Rows + 32 * warp < r_valid;
-                const int pos = w.seq.L - w.seq.n + r / p.G;
-                pr = valid ? pos : -1;
-                lor = valid && p.window > 0 ? max(0, pos - p.window + 1) : 0;
-                jf = (w.keys.pt_lo + w.u0 * kT8Tiles) * kPage;
+                pr = valid ? w.base + t : -1;
+                lor = valid && p.window > 0 ? max(0, w.base + t - p.window + 1) : 0;
+                jf = (w.pt_lo + w.u0 * kT8Tiles) * kPage;
                 count = w.u1 - w.u0;
-                T8Walk ahead = w;
-                more = ahead.next(p);
-                if (more && !failed) load_q(ahead, (seg + 1) & 1);  // (its buffer's last segment is finished)
-                __syncwarp();
-                if (lane == 0) {
-                    s_walk[warp][0] = w;
-                    s_walk[warp][1] = ahead;
-                }
-                __syncwarp();
+                if (valid && p.sinks != nullptr) sink = __ldg(p.sinks + w.g * p.G + (r - t * p.G)) * kLog2e;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_free + 8 * (seg & 1));
             float R = -INFINITY, l = 0.f;
             for (int k = 0; k < count && !failed; ++k, ++i, jf += kT8Keys) {
                 const int sb = i & 1;
@@ -705,33 +697,39 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                         }
                     };
                     float l_unit;
-                    // the probabilities with the reference R; true: one may be too large
-                    auto probabilities = [&]() {
+                    // half the unit's probabilities with the reference R into P; true: one may be too large
+                    auto half = [&](int h, const uint32_t(&x)[32]) {
                         const float mr = kT8Shift - (R == -INFINITY ? 0.f : R);
+                        uint32_t pk[16];
+                        bool over = false;
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const float4 f = fac[2 * h + v];
+                            const float2 mul = make_float2(f.x, f.x), add = make_float2(f.y + mr, f.y + mr);
+                            float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const float2 y = fma2(make_float2(__uint_as_float(x[16 * v + 2 * c]), __uint_as_float(x[16 * v + 2 * c + 1])), mul, add);
+                                const float a0 = fast_exp2(y.x), a1 = fast_exp2(y.y);
+                                ls[c & 1] = add2(ls[c & 1], make_float2(a0, a1));
+                                pk[8 * v + c] = pack_f16(a0, a1);
+                            }
+                            const float2 s2 = add2(ls[0], ls[1]);
+                            const float sum = s2.x + s2.y;
+                            over = over || sum > kT8TileMax;
+                            l_unit = fmaf(sum, f.z, l_unit);
+                        }
+                        tmem_st16(pc + 16 * h, pk);
+                        return over;
+                    };
+                    auto probabilities = [&]() {
                         bool over = false;
                         l_unit = 0.f;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            uint32_t x[32], pk[16];
+                            uint32_t x[32];
                             scores(h, x);
-#pragma unroll
-                            for (int v = 0; v < 2; ++v) {
-                                const float4 f = fac[2 * h + v];
-                                const float2 mul = make_float2(f.x, f.x), add = make_float2(f.y + mr, f.y + mr);
-                                float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const float2 y = fma2(make_float2(__uint_as_float(x[16 * v + 2 * c]), __uint_as_float(x[16 * v + 2 * c + 1])), mul, add);
-                                    const float a0 = fast_exp2(y.x), a1 = fast_exp2(y.y);
-                                    ls[c & 1] = add2(ls[c & 1], make_float2(a0, a1));
-                                    pk[8 * v + c] = pack_f16(a0, a1);
-                                }
-                                const float2 s2 = add2(ls[0], ls[1]);
-                                const float sum = s2.x + s2.y;
-                                over = over || sum > kT8TileMax;
-                                l_unit = fmaf(sum, f.z, l_unit);
-                            }
-                            tmem_st16(pc + 16 * h, pk);
+                            over = half(h, x) || over;
                         }
                         return over;
                     };
@@ -739,9 +737,9 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                     if (!__any_sync(0xffffffffu, need)) need = probabilities();
                     if (__any_sync(0xffffffffu, need)) {
                         float mb = -INFINITY;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t x[32];
+                        uint32_t x[32];
+#pragma unroll 1
+                        for (int h = 1; h >= 0; --h) {  // (the first half last: its scores are then at hand)
                             scores(h, x);
 #pragma unroll
                             for (int v = 0; v < 2; ++v) {
@@ -762,7 +760,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                                 break;
                             }
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < 4; ++h) {
                                 uint32_t o[16];
                                 tmem_ld16(tm + lanes + kT8ColO + 16 * h, o);
@@ -776,7 +774,10 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                         l *= f;
                         R = Rn;
                         tmem_wait_st();
-                        probabilities();
+                        l_unit = 0.f;
+                        half(0, x);
+                        scores(1, x);
+                        half(1, x);
                     }
                     l += l_unit;
                     tmem_wait_st();
@@ -790,28 +791,29 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             const int last = i - 1;
             if (!failed && warp_active && __any_sync(0xffffffffu, !mbar_wait_bounded(o_done + 8 * (last & 1), (last >> 1) & 1)))
                 failed = true;
-            const T8Walk w = s_walk[warp][0];
-            const int r0 = w.rb * kT8Rows, r = r0 + tid, r_end = min(r0 + kT8Rows, p.T * p.G);
-            const bool whole = w.u0 == 0 && w.u1 == w.keys.units;
-            const int slot_k = seg == 0 ? 0 : 1;
+            if (failed) break;
+            const T8Seg &w = s_seg[seg & 3];
+            const int r0 = w.rb * kT8Rows, r = r0 + tid, r_end = min(r0 + kT8Rows, p.T * p.G), t = r / p.G;
+            uint4 *const dst = reinterpret_cast<uint4 *>(
+                p.out + (r < r_end ? ((static_cast<size_t>(w.b) * p.T + t) * p.Hq + w.g * p.G + (r - t * p.G)) * kD : 0));
+            const bool whole = w.u0 == 0 && w.u1 == w.units;
             const float m_row = R - kT8Shift;
             float f = 0.f;  // rows that are not queries: zeros
             if (whole && valid) {
-                const float sg = p.sinks != nullptr ? __ldg(p.sinks + w.g * p.G + r % p.G) * kLog2e : -INFINITY;
-                const float M = fmaxf(m_row, sg);
+                const float M = fmaxf(m_row, sink);
                 if (M != -INFINITY) {
-                    const float den = l * exp2f(m_row - M) + (sg == -INFINITY ? 0.f : exp2f(sg - M));
+                    const float den = l * exp2f(m_row - M) + (sink == -INFINITY ? 0.f : exp2f(sink - M));
                     f = den > 0.f ? exp2f(m_row - M) / den : den == den ? 0.f : den;
                 }
             }
-            float *slot = p.part + (static_cast<size_t>(cta) * 2 + slot_k) * kT8SlotFloats + static_cast<size_t>(tid) * kMSlotFloats;
-            if (!whole && valid && !failed) {
-                slot[0] = m_row;
-                slot[1] = l;
+            float *const slot = p.part + (static_cast<size_t>(cta) * 2 + (seg == 0 ? 0 : 1)) * kT8SlotFloats;
+            if (!whole && valid) {
+                slot[tid] = m_row;
+                slot[kT8Rows + tid] = l;
             }
             tc_fence_after();
 #pragma unroll
-            for (int h = 0; h < 4 && !failed; ++h) {
+            for (int h = 0; h < 4; ++h) {
                 uint32_t x[16];
                 if (warp_active) {
                     tmem_ld16(tm + lanes + kT8ColO + 16 * h, x);
@@ -822,7 +824,6 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 for (int c = 0; c < 16; ++c) o[c] = valid ? __uint_as_float(x[c]) : 0.f;
                 if (whole) {
                     if (r < r_end) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row_off(w, r)) + 2 * h;
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint4 y;
@@ -830,37 +831,32 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                             y.y = pack_bf16(o[8 * c + 2] * f, o[8 * c + 3] * f);
                             y.z = pack_bf16(o[8 * c + 4] * f, o[8 * c + 5] * f);
                             y.w = pack_bf16(o[8 * c + 6] * f, o[8 * c + 7] * f);
-                            dst[c] = y;
+                            dst[2 * h + c] = y;
                         }
                     }
                 } else if (valid) {
-                    float4 *acc = reinterpret_cast<float4 *>(slot + kMAccOff) + 4 * h;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    for (int c = 0; c < 4; ++c)
+                        *const_cast<float4 *>(t8_acc(slot, 4 * h + c, tid)) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 }
             }
             tc_fence_before();  // (the next segment's first PV writes O after this warp's next P)
             if (!whole && !p.defer && r0 + 32 * warp < r_end) {
                 // the last of the CTAs that share the segment folds its partials, every warp its own 32 rows: a
                 // counter per warp, at the segment's first CTA (which has no other segment that goes on)
-                const long long begin = s_begin[warp], U = s_range[2];
-                const int c0 = t8_owner(U, nc, begin), c1 = t8_owner(U, nc, begin + w.keys.units - 1);
+                const long long U = s_range[2];
+                const int c0 = t8_owner(U, nc, w.begin), c1 = t8_owner(U, nc, w.begin + w.units - 1);
                 __threadfence();
                 __syncwarp();
-                int *ctr = p.counters + 4 * c0 + warp;
                 int ticket = 0;
-                if (lane == 0) ticket = atomicAdd(ctr, 1);
+                if (lane == 0) ticket = atomicAdd(p.counters + 4 * c0 + warp, 1);
                 if (__shfl_sync(0xffffffffu, ticket, 0) == c1 - c0) {
                     __threadfence();
-                    const int k0 = t8_first(U, nc, c0) < begin ? 1 : 0;
                     if (r < r_end)
-                        t8_fold_thread(p, c0, k0, c1 - c0 + 1, tid, w.g * p.G + r % p.G, valid, reinterpret_cast<uint4 *>(p.out + row_off(w, r)));
-                    if (lane == 0) *ctr = 0;  // ready for the next call
+                        t8_fold(p, c0, t8_first(U, nc, c0) < w.begin ? 1 : 0, c1 - c0 + 1, tid, w.g * p.G + (r - t * p.G), valid, dst);
                 }
             }
-            __syncwarp();
-            if (lane == 0) s_begin[warp] += w.keys.units;
-            ++seg;
+            if (w.last) break;
         }
         }
     }
@@ -875,26 +871,86 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
     }
 }
 
-// The partials of the segments that several CTAs share, folded after the attention, one warp per query row:
-// where few segments are spread over the whole grid the CTA that comes last would fold dozens alone.
-// One CTA per four rows of a segment; the split is worked out again from the lengths.
-constexpr int kT8FoldWarps = 4;
+// The partials of the segments that several CTAs share, folded after the attention: where few segments are spread over
+// the whole grid the CTA that comes last would fold dozens alone. One CTA per 32 rows of a segment; a thread has a row,
+// and each of the eight warps every eighth partial; the warps' sums meet in shared memory. The split is worked
+// out again from the lengths.
+constexpr int kT8FoldWarps = 8;
 __global__ void __launch_bounds__(kT8FoldWarps * 32) t8_combine_kernel(const MultiParams p, int grid) {
-    __shared__ long long pre[kMaxBatch + 1];
+    __shared__ union {
+        long long pre[kMaxBatch + 1];
+        float sum[kT8FoldWarps][32][17];
+    } sh;
+    __shared__ float s_m[kT8FoldWarps][32], s_l[kT8FoldWarps][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rb = blockIdx.x / (kT8Rows / kT8FoldWarps), rl = blockIdx.x % (kT8Rows / kT8FoldWarps) * kT8FoldWarps + warp;
+    const int rb = blockIdx.x / 4, rl = blockIdx.x % 4 * 32 + lane;
     const int g = blockIdx.y, b = blockIdx.z;
     const T8Seq s = t8_seq(p, b);
     if (rb >= s.blocks) return;  // zeros, written by the attention
-    t8_prefix(p, pre, warp, kT8FoldWarps, lane);
-    const long long U = pre[p.B];
+    t8_prefix(p, sh.pre, warp, kT8FoldWarps, lane);
+    const long long U = sh.pre[p.B];
     const int nc = t8_ctas(U, grid);
-    long long begin = pre[b] + (pre[b + 1] - pre[b]) / p.Hkv * g;
+    long long begin = sh.pre[b] + (sh.pre[b + 1] - sh.pre[b]) / p.Hkv * g;
     for (int i = 0; i < rb; ++i) begin += t8_keys(p, s, i).units;
     const int c0 = t8_owner(U, nc, begin), c1 = t8_owner(U, nc, begin + t8_keys(p, s, rb).units - 1);
-    const int r = rb * kT8Rows + rl, t = r / p.G, hl = r - t * p.G;
-    if (c0 == c1 || r >= p.T * p.G) return;
-    const uint32_t y = t < s.n ? t8_fold_row(p, c0, t8_first(U, nc, c0) < begin ? 1 : 0, c1 - c0 + 1, rl, g * p.G + hl, lane) : 0u;
-    reinterpret_cast<uint32_t *>(p.out + ((static_cast<size_t>(b) * p.T + t) * p.Hq + g * p.G + hl) * kD)[lane] = y;
+    const int r0 = rb * kT8Rows;
+    if (c0 == c1 || r0 + blockIdx.x % 4 * 32 >= p.T * p.G) return;
+    const int count = c1 - c0 + 1, k0 = t8_first(U, nc, c0) < begin ? 1 : 0;
+    const int r = r0 + rl, t = r / p.G, hl = r - t * p.G;
+    const bool row = r < p.T * p.G, query = row && t < s.n;
+    float M = -INFINITY;
+    if (query) {
+#pragma unroll 4
+        for (int i = warp; i < count; i += kT8FoldWarps) M = fmaxf(M, __ldcg(t8_slot(p, c0, k0, i) + rl));
+    }
+    s_m[warp][lane] = M;
+    __syncthreads();  // (and the prefix has been read)
+    const float sg = query && p.sinks != nullptr ? __ldg(p.sinks + g * p.G + hl) * kLog2e : -INFINITY;
+    float Mf = sg;
+#pragma unroll
+    for (int w = 0; w < kT8FoldWarps; ++w) Mf = fmaxf(Mf, s_m[w][lane]);
+    float d = 0.f;
+    float4 o[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (query && Mf != -INFINITY)
+        for (int i = warp; i < count; i += kT8FoldWarps) {
+            const float *sl = t8_slot(p, c0, k0, i);
+            const float m = __ldcg(sl + rl);
+            if (m == -INFINITY) continue;  // no key of the row there
+            const float w = exp2f(m - Mf);
+            d += __ldcg(sl + kT8Rows + rl) * w;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float4 x = __ldcg(t8_acc(sl, c, rl));
+                o[c].x += x.x * w, o[c].y += x.y * w, o[c].z += x.z * w, o[c].w += x.w * w;
+            }
+        }
+    s_l[warp][lane] = d;
+    float den = 0.f, inv = 0.f;
+    uint32_t *out = reinterpret_cast<uint32_t *>(p.out + ((static_cast<size_t>(b) * p.T + t) * p.Hq + g * p.G + hl) * kD);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {  // 16 columns at a time; this thread adds up columns 2 warp, 2 warp + 1 of its row
+        __syncthreads();
+        if (h == 0) {
+            den = sg == -INFINITY ? 0.f : exp2f(sg - Mf);
+#pragma unroll
+            for (int w = 0; w < kT8FoldWarps; ++w) den += s_l[w][lane];
+            inv = den > 0.f ? 1.f / den : den == den ? 0.f : den;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float *x = &sh.sum[warp][lane][4 * c];
+            x[0] = o[4 * h + c].x, x[1] = o[4 * h + c].y, x[2] = o[4 * h + c].z, x[3] = o[4 * h + c].w;
+        }
+        __syncthreads();
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kT8FoldWarps; ++w) {
+            x0 += sh.sum[w][lane][2 * warp];
+            x1 += sh.sum[w][lane][2 * warp + 1];
+        }
+        if (row) out[8 * h + warp] = pack_bf16(x0 * inv, x1 * inv);
+    }
 }
