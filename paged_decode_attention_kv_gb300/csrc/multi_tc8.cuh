@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             }
         }
     } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 13) asm volatile("griddepcontrol.wait;" ::: "memory");  // (also without units: the kernels after wait for this one alone)
         if (warp == 13 && units > 0) {
             // ---- copies: lane u < 4 the block of tile u of every unit
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
         __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
         // ---- query rows: one per thread
         if (units > 0) {
         const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
@@ -687,68 +687,68 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                     const float4 *fac = s_fac + st * kT8Tiles;
                     const bool interior = __all_sync(0xffffffffu, jf >= lor && jf + kT8Keys - 1 <= pr);
                     const int a = lor - jf, e = pr + 1 - jf;  // keys [a, e) of the unit are this row's
-                    auto scores = [&](int h, uint32_t(&x)[32]) {
-                        tmem_ld32(sc + 32 * h, x);
-                        tmem_wait_ld();
+                    // one tile's scores; keys that are not the row's: -inf
+                    auto mask = [&](int u, uint32_t(&x)[16]) {
                         if (!interior) {
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (32 * h + c < a || 32 * h + c >= e) x[c] = 0xff800000u;
+                            for (int c = 0; c < 16; ++c)
+                                if (16 * u + c < a || 16 * u + c >= e) x[c] = 0xff800000u;
                         }
                     };
                     float l_unit;
-                    // half the unit's probabilities with the reference R into P; true: one may be too large
-                    auto half = [&](int h, const uint32_t(&x)[32]) {
-                        const float mr = kT8Shift - (R == -INFINITY ? 0.f : R);
-                        uint32_t pk[16];
-                        bool over = false;
+                    // a tile's probabilities with the reference R into P; true: one may be too large
+                    auto tile = [&](int u, uint32_t(&x)[16]) {
+                        mask(u, x);
+                        const float4 f = fac[u];
+                        const float ad = f.y + (kT8Shift - (R == -INFINITY ? 0.f : R));
+                        const float2 mul = make_float2(f.x, f.x), add = make_float2(ad, ad);
+                        float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                        uint32_t pk[8];
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            const float4 f = fac[2 * h + v];
-                            const float2 mul = make_float2(f.x, f.x), add = make_float2(f.y + mr, f.y + mr);
-                            float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float2 y = fma2(make_float2(__uint_as_float(x[16 * v + 2 * c]), __uint_as_float(x[16 * v + 2 * c + 1])), mul, add);
-                                const float a0 = fast_exp2(y.x), a1 = fast_exp2(y.y);
-                                ls[c & 1] = add2(ls[c & 1], make_float2(a0, a1));
-                                pk[8 * v + c] = pack_f16(a0, a1);
-                            }
-                            const float2 s2 = add2(ls[0], ls[1]);
-                            const float sum = s2.x + s2.y;
-                            over = over || sum > kT8TileMax;
-                            l_unit = fmaf(sum, f.z, l_unit);
+                        for (int c = 0; c < 8; ++c) {
+                            const float2 y = fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), mul, add);
+                            const float a0 = fast_exp2(y.x), a1 = fast_exp2(y.y);
+                            ls[c & 1] = add2(ls[c & 1], make_float2(a0, a1));
+                            pk[c] = pack_f16(a0, a1);
                         }
-                        tmem_st16(pc + 16 * h, pk);
-                        return over;
+                        tmem_st8(pc + 8 * u, pk);
+                        const float2 s2 = add2(ls[0], ls[1]);
+                        const float sum = s2.x + s2.y;
+                        l_unit = fmaf(sum, f.z, l_unit);
+                        return sum > kT8TileMax;
                     };
+                    // (a tile's scores are fetched while the one before is worked on)
                     auto probabilities = [&]() {
-                        bool over = false;
+                        uint32_t x0[16], x1[16];
                         l_unit = 0.f;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t x[32];
-                            scores(h, x);
-                            over = half(h, x) || over;
-                        }
-                        return over;
+                        tmem_ld16(sc, x0);
+                        tmem_wait_ld();
+                        tmem_ld16(sc + 16, x1);
+                        bool over = tile(0, x0);
+                        tmem_wait_ld();
+                        tmem_ld16(sc + 32, x0);
+                        over = tile(1, x1) || over;
+                        tmem_wait_ld();
+                        tmem_ld16(sc + 48, x1);
+                        over = tile(2, x0) || over;
+                        tmem_wait_ld();
+                        return tile(3, x1) || over;
                     };
                     bool need = R == -INFINITY && valid;
                     if (!__any_sync(0xffffffffu, need)) need = probabilities();
                     if (__any_sync(0xffffffffu, need)) {
                         float mb = -INFINITY;
-                        uint32_t x[32];
 #pragma unroll 1
-                        for (int h = 1; h >= 0; --h) {  // (the first half last: its scores are then at hand)
-                            scores(h, x);
+                        for (int u = 0; u < kT8Tiles; ++u) {
+                            uint32_t x[16];
+                            tmem_ld16(sc + 16 * u, x);
+                            tmem_wait_ld();
+                            mask(u, x);
+                            const float4 f = fac[u];
+                            float mt = -INFINITY;
 #pragma unroll
-                            for (int v = 0; v < 2; ++v) {
-                                const float4 f = fac[2 * h + v];
-                                float mt = -INFINITY;
-#pragma unroll
-                                for (int c = 0; c < 16; c += 2) mt = max3(mt, __uint_as_float(x[16 * v + c]), __uint_as_float(x[16 * v + c + 1]));
-                                mb = fmaxf(mb, fmaf(mt, f.x, f.y));  // the multiplier is positive
-                            }
+                            for (int c = 0; c < 16; c += 2) mt = max3(mt, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                            mb = fmaxf(mb, fmaf(mt, f.x, f.y));  // the multiplier is positive
                         }
                         const float Rn = need ? fmaxf(R, ceilf(mb)) : R;  // an integer: F - R and the rescaling are exact
                         const float f = Rn == R ? 1.f : exp2f(R - Rn);    // R = -inf: 0 (O and l are 0)
@@ -774,10 +774,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                         l *= f;
                         R = Rn;
                         tmem_wait_st();
-                        l_unit = 0.f;
-                        half(0, x);
-                        scores(1, x);
-                        half(1, x);
+                        probabilities();
                     }
                     l += l_unit;
                     tmem_wait_st();
