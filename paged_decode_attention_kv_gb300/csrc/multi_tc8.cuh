@@ -696,10 +696,10 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                         }
                     };
                     float l_unit;
-                    // a tile's probabilities with the reference R into P; true: one may be too large
+                    // a tile's probabilities with the reference R into P, and their sum
                     auto tile = [&](int u, uint32_t(&x)[16]) {
                         mask(u, x);
-                        const float4 f = fac[u];
+                        const float2 f = *reinterpret_cast<const float2 *>(fac + u);
                         const float ad = f.y + (kT8Shift - (R == -INFINITY ? 0.f : R));
                         const float2 mul = make_float2(f.x, f.x), add = make_float2(ad, ad);
                         float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -712,27 +712,27 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                             pk[c] = pack_f16(a0, a1);
                         }
                         tmem_st8(pc + 8 * u, pk);
-                        const float2 s2 = add2(ls[0], ls[1]);
-                        const float sum = s2.x + s2.y;
-                        l_unit = fmaf(sum, f.z, l_unit);
-                        return sum > kT8TileMax;
+                        return add2(ls[0], ls[1]);
                     };
-                    // (a tile's scores are fetched while the one before is worked on)
+                    // (a tile's scores are fetched while the one before is worked on; the sums are looked at at the end, where
+                    // their latencies overlap); true: a probability may be too large
                     auto probabilities = [&]() {
                         uint32_t x0[16], x1[16];
-                        l_unit = 0.f;
                         tmem_ld16(sc, x0);
                         tmem_wait_ld();
                         tmem_ld16(sc + 16, x1);
-                        bool over = tile(0, x0);
+                        const float2 s0 = tile(0, x0);
                         tmem_wait_ld();
                         tmem_ld16(sc + 32, x0);
-                        over = tile(1, x1) || over;
+                        const float2 s1 = tile(1, x1);
                         tmem_wait_ld();
                         tmem_ld16(sc + 48, x1);
-                        over = tile(2, x0) || over;
+                        const float2 s2 = tile(2, x0);
                         tmem_wait_ld();
-                        return tile(3, x1) || over;
+                        const float2 s3 = tile(3, x1);
+                        const float t0 = s0.x + s0.y, t1 = s1.x + s1.y, t2 = s2.x + s2.y, t3 = s3.x + s3.y;
+                        l_unit = fmaf(t0, fac[0].z, t1 * fac[1].z) + fmaf(t2, fac[2].z, t3 * fac[3].z);
+                        return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) > kT8TileMax;
                     };
                     bool need = R == -INFINITY && valid;
                     if (!__any_sync(0xffffffffu, need)) need = probabilities();
