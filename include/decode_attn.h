@@ -485,8 +485,8 @@ DA_API int kv_read_fp8(const void *kv_cache, const int32_t *block_table, const i
  * largest one; V scales outside 2^-60 .. 2^60 lose bits. Cells outside a sequence's
  * [window start, length) may hold anything; the cached and the new tokens of a sequence must be
  * finite (a NaN may reach rows of its sequence that do not attend it).
- * One launch for up to four tokens with T * G <= 32, else two, and one more where a sequence's keys
- * are cut into many splits. Multi-token workspace
+ * One launch for up to four tokens with T * G <= 32, else two, and one more where a few blocks of
+ * query rows share the whole GPU. q_tokens up to 4096. Multi-token workspace
  * (decode_attn_paged_fp8_multi_workspace_bytes, decode_attn_multi_reserve). The ring form is not
  * there: a call's early tokens attend cells that its later ones overwrite.
  */

@@ -736,9 +736,12 @@ def kv_append_fp8(k_new, v_new, kv_cache, seq_lens, block_table=None, q_lens=Non
     kp, bp, lp, B, Hkv, window, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
     T = k_new.shape[1] if k_new.dim() == 4 else 1
     rows = (B, T, Hkv, 64) if k_new.dim() == 4 else (B, Hkv, 64)
+    knp, vnp = _tensor("k_new", k_new, torch.bfloat16, rows, dev), _tensor("v_new", v_new, torch.bfloat16, rows, dev)
+    qlp = None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev)
+    if B == 0:  # (an empty tensor has no address)
+        return
     _check(load_library().kv_append_fp8(
-        _tensor("k_new", k_new, torch.bfloat16, rows, dev), _tensor("v_new", v_new, torch.bfloat16, rows, dev), kp, bp, lp,
-        None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev), window, int(scale_rule),
+        knp, vnp, kp, bp, lp, qlp, window, int(scale_rule),
         da_shape(B, Hkv, Hkv, 64), T, *sizes, _raw_stream(stream, dev)))
 
 
@@ -749,10 +752,13 @@ def kv_read_fp8(kv_cache, seq_lens, k_out, v_out, block_table=None, starts=None,
     dev = torch.cuda.current_device()
     kp, bp, lp, B, Hkv, window, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
     rows = k_out.shape[1] if k_out.dim() > 1 else 0
+    kop = _tensor("k_out", k_out, torch.bfloat16, (B, rows, Hkv, 64), dev)
+    vop = _tensor("v_out", v_out, torch.bfloat16, (B, rows, Hkv, 64), dev)
+    stp = None if starts is None else _tensor("starts", starts, torch.int32, (B,), dev)
+    if B == 0:
+        return k_out, v_out
     _check(load_library().kv_read_fp8(
-        kp, bp, lp, None if starts is None else _tensor("starts", starts, torch.int32, (B,), dev), window,
-        _tensor("k_out", k_out, torch.bfloat16, (B, rows, Hkv, 64), dev), _tensor("v_out", v_out, torch.bfloat16, (B, rows, Hkv, 64), dev),
-        rows, da_shape(B, Hkv, Hkv, 64), *sizes, _raw_stream(stream, dev)))
+        kp, bp, lp, stp, window, kop, vop, rows, da_shape(B, Hkv, Hkv, 64), *sizes, _raw_stream(stream, dev)))
     return k_out, v_out
 
 
@@ -767,8 +773,11 @@ def decode_attn_paged_fp8_multi(q, k_new, v_new, kv_cache, block_table, seq_lens
     kp, bp, lp, B, Hkv, _, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
     T = q.shape[1]
     qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B, T), Hkv, dev)
+    qlp = None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev)
+    if B == 0:
+        return out
     _check(load_library().decode_attn_paged_fp8_multi(
-        qp, knp, vnp, kp, bp, lp, None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev), sp, int(window),
+        qp, knp, vnp, kp, bp, lp, qlp, sp, int(window),
         float(scale), int(scale_rule), op, da_shape(B, Hq, Hkv, 64), T, *sizes, _raw_stream(stream, dev)))
     return out
 

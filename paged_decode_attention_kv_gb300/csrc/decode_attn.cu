@@ -2988,14 +2988,15 @@ int run_rotate(const da_rows *q, const da_rows *k, const da_rows *v, int tokens,
                void *stream) {
     if (!q || !k || tokens < 0 || Hq <= 0 || Hkv <= 0 || head_dim <= 0) return DA_ERR_INVALID_ARG;
     if (head_dim != kD || Hq > kMaxQHeads || Hkv > kMaxQHeads) return DA_ERR_UNSUPPORTED;
-    if (!positions || !rope_cos || !rope_sin || max_position <= 0 || !aligned16(rope_cos) || !aligned16(rope_sin))
+    // (of no token there may be no address: an empty tensor has none)
+    if ((!positions && tokens > 0) || !rope_cos || !rope_sin || max_position <= 0 || !aligned16(rope_cos) || !aligned16(rope_sin))
         return DA_ERR_INVALID_ARG;
     if (axes < 1 || axes > 3 || (axes > 1 && !pair_axis)) return DA_ERR_INVALID_ARG;
     if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !(eps >= 0.f) || eps == INFINITY)
         return DA_ERR_INVALID_ARG;
     auto rows_ok = [&](const da_rows *r, int heads) {
         const long long least = static_cast<long long>(heads) * kD;
-        return r->in && r->out && aligned16(r->in) && aligned16(r->out) && r->in_stride % 8 == 0 && r->out_stride % 8 == 0 &&
+        return ((r->in && r->out) || tokens == 0) && aligned16(r->in) && aligned16(r->out) && r->in_stride % 8 == 0 && r->out_stride % 8 == 0 &&
                (tokens <= 1 || (r->in_stride >= least && r->out_stride >= least));
     };
     if (!rows_ok(q, Hq) || !rows_ok(k, Hkv) || (v && !rows_ok(v, Hkv))) return DA_ERR_INVALID_ARG;
@@ -3085,7 +3086,8 @@ int run_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t
                  int num_pages, int max_seq_len, void *stream) {
     int rc = check_blocks(kv_cache, block_table, seq_lens, window, s, page_size, max_pages, num_pages, max_seq_len);
     if (rc != DA_OK) return rc;
-    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || rows < 0) return DA_ERR_INVALID_ARG;
+    if (((!k_out || !v_out) && rows > 0) || !aligned16(k_out) || !aligned16(v_out) || rows < 0)
+        return DA_ERR_INVALID_ARG;
     if (s.batch == 0 || rows == 0) return DA_OK;
     dim3 grid;
     rc = launch_blocks_grid(rows, block_table ? max_seq_len : window, s.num_kv_heads, s.batch, &grid);

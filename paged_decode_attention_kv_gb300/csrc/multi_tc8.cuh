@@ -27,19 +27,31 @@
 // CTAs cut for the longest sequence instead, 64 sequences of 1024 to 8192 tokens took 248 us.
 //
 // 16 warps stream through the CTA's units without a break between segments:
-//   warps 0-3   one query row per thread (TMEM lane = row): the softmax and the finish, and the next
-//               segment's query rows as fp16 into the other of two Q buffers
+//   warps 0-3   one query row per thread (TMEM lane = row): the softmax and the finish
 //   warps 4-11  two teams of four that take turns: warp u of a team turns tile u of its unit into K' and V'
 //   warp 12     issues the MMAs: S_i = Q K'_i^T and O += P_i V'_i (V' as it is stored, transposed:
 //               tokens contiguous, so both operands are K-major)
 //   warp 13     copies the units' fp8 blocks (2176 bytes each, one bulk copy), lane u tile u
+//   warps 14-15 the next segment's query rows as fp16 into the other of two Q buffers, and its place for the row
+//               warps (done by the row warps themselves, with their partials' stores a row at a time, 64 sequences x 16
+//               tokens took 194 us instead of 173, four prompts 402 instead of 350)
 // Two teams because one is a chain of latencies (copy landed, scales' maximum, factors, operands) of about
-// 2400 cycles a unit. Registers go where they are needed (setmaxnreg): 64 a thread at launch, then 104 for
-// the rows, 56 for the teams, 40 for the last four warps, 4 x 64 in all.
+// 2400 cycles a unit. Registers go where they are needed (setmaxnreg): 64 a thread at launch, then 88 for
+// the rows, 56 for the others, 4 x 64 in all.
 // The softmax takes the probabilities with the reference it has, and looks for a larger one only if a
 // tile's sum shows that one may have left fp16's range (or the row has no reference yet): the scores then
-// still stand in TMEM (P has its own columns) and are taken again. The maxima of every unit cost 40 of
-// 230 instructions, and holding 64 scores in registers for them 84 bytes of spills.
+// still stand in TMEM (P has its own columns) and are taken again. The maxima of every unit cost 40 of its
+// 230 instructions. It works a tile (16 keys) at a time and fetches the next one's scores meanwhile: 32 keys at a
+// time, one after the other, took 173 us for 64 x 16 tokens, this 168, and 164 with the unit's sums added up at its end.
+//
+// What bounds it: the row warps' chain S complete -> scores -> probabilities -> P stored -> arrival, about 1920 cycles
+// a unit with two CTAs on an SM (1440 alone), in which the SM issues 54% of the time (2500 instructions a unit: rows
+// 1090, teams 690, waits, copies and MMAs the rest); the tensor cores work 21% of it, the exponentials' unit 256 cycles
+// a unit. A segment's start and end cost about 12000 cycles, a CTA's first unit is 17000 cycles from its launch.
+// 64 sequences of 1024 to 8192 tokens, 16 tokens each: 164 us (2.0 TB/s, 457 TFLOP/s); 512 tokens behind 7680: 128 us
+// (520 TFLOP/s); four prompts of 1201 to 2048: 328 us; G = 8, 64 query heads throughout. Tried, without a gain: three
+// or four stages, more raw units, S and PV issued by two warps, the next S issued before P has arrived, all 64
+// scores in registers (they spill).
 constexpr int kT8Rows = 128, kT8Keys = 64, kT8Tiles = kT8Keys / kPage;
 #ifndef DA_T8_STAGES
 #define DA_T8_STAGES 3

@@ -37,6 +37,7 @@ def test_rotate_refusals(lib):
     assert rotate(lib, D=128) == -2
     assert rotate(lib, Hq=1025, q=dict(in_stride=65600, out_stride=65600)) == -2
     assert rotate(lib, n=0) == 0
+    assert rotate(lib, n=0, pos=None, q=dict(in_=None, out=None), k=dict(in_=None, out=None)) == 0  # empty tensors have no address
     assert rotate(lib, n=0, axes=3, table=bytes([0, 1, 2, 2] * 8)) == 0
 
 
@@ -79,6 +80,7 @@ def test_refusals_of_the_cache_calls(lib):
         assert call(lib, rule=2) == -1
     assert read(lib, rows=-1) == -1
     assert read(lib, rows=0) == 0
+    assert read(lib, rows=0, k=None, v=None) == 0                  # empty tensors have no address
     for change in (dict(q=None), dict(out=BAD), dict(bt=None), dict(scale=0.0), dict(scale=-0.125), dict(scale=float("inf")), dict(scale=float("nan")),
                    dict(window=-1), dict(s=_shape(Hq=6, Hkv=4))):
         assert multi(lib, **change) == -1, change

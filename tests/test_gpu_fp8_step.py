@@ -49,3 +49,27 @@ def test_prompt_drafts_and_decode(Hq, Hkv):
         assert_blocks_equal(from_dev(kv), cache)
     assert da.decode_attn_device_status() == 0
     check_read(kv, cache, lens, int(lens.max()), table, starts=np.array([0, 17, 5], np.int32))
+
+
+def test_nothing_to_do():
+    """No token, no sequence, no row to read: every call returns, and the cache stays as it is."""
+    def rows(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+    cos, sin = tables(16)
+    da.qk_norm_rope(rows(0, 8, 64), rows(0, 2, 64), torch.empty(0, dtype=torch.int32, device=DEV), cos, sin, rows(0, 8, 64), rows(0, 2, 64),
+                    v=rows(0, 2, 64), v_out=rows(0, 2, 64))
+    da.qk_norm_rope(rows(0, 8, 64), rows(0, 2, 64), torch.empty((3, 0), dtype=torch.int32, device=DEV), cos, sin, rows(0, 8, 64),
+                    rows(0, 2, 64), sections=(12, 10, 10))
+    kv = torch.randint(0, 120, (4, 2, da.FP8_BLOCK_BYTES), dtype=torch.uint8, device=DEV)
+    before = kv.clone()
+    sinks = torch.zeros(8, device=DEV)
+    table, lens = torch.zeros((0, 4), dtype=torch.int32, device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV)
+    da.kv_append_fp8(rows(0, 5, 2, 64), rows(0, 5, 2, 64), kv, lens, block_table=table)
+    da.kv_append_fp8(rows(0, 5, 2, 64), rows(0, 5, 2, 64), kv[:0].view(0, 2, 1, da.FP8_BLOCK_BYTES), lens)
+    da.kv_read_fp8(kv, lens, rows(0, 7, 2, 64), rows(0, 7, 2, 64), block_table=table)
+    for T in (2, 40):
+        da.decode_attn_paged_fp8_multi(rows(0, T, 8, 64), rows(0, T, 2, 64), rows(0, T, 2, 64), kv, table, lens, sinks, 0, 0.125, rows(0, T, 8, 64))
+    table, lens = torch.zeros((2, 4), dtype=torch.int32, device=DEV), torch.tensor([9, 0], dtype=torch.int32, device=DEV)
+    da.kv_read_fp8(kv, lens, rows(2, 0, 2, 64), rows(2, 0, 2, 64), block_table=table)
+    torch.cuda.synchronize()
+    assert da.decode_attn_device_status() == 0 and torch.equal(kv, before)
