@@ -20,11 +20,11 @@
 // 2^60 (V) lose bits.
 //
 // The work is cut on the device: a unit is a block of 64 keys of a segment (sequence, KV head, block of
-// 128 query rows), and every CTA of the grid (two per SM) takes the same number of consecutive units,
-// whatever the lengths. A segment that lies in one CTA is finished there; one that is shared leaves fp32
-// partials (m, l, O per row; two slots per CTA), folded by the CTA that comes last, or, where the host
-// sees that a few segments fill the whole grid, by t8_combine_kernel. With a grid of (segment, key split)
-// CTAs cut for the longest sequence instead, 64 sequences of 1024 to 8192 tokens took 248 us.
+// 128 query rows); a segment costs its units and kT8SegCost more, for its start and end, and every CTA of the grid (two
+// per SM) takes the same cost of consecutive units, whatever the lengths. A segment that lies in one CTA is finished
+// there; one that is shared leaves fp32 partials (m, l, O per row; two slots per CTA), folded by the CTA that comes last,
+// or, where the host sees that a few segments fill the whole grid, by t8_combine_kernel. With a grid of (segment, key
+// split) CTAs cut for the longest sequence instead, 64 sequences of 1024 to 8192 tokens took 248 us.
 //
 // 16 warps stream through the CTA's units without a break between segments:
 //   warps 0-3   one query row per thread (TMEM lane = row): the softmax and the finish
@@ -74,12 +74,25 @@ constexpr int kT8Bars = 2 * kT8Raw + 2 * kT8Stages + 5 * 2 + 1;
 constexpr int kT8Smem = 1024 + 2 * kT8QBytes + kT8Stages * kT8StageBytes + kT8RawBytes + kT8Stages * kT8Tiles * 16 + kT8Bars * 8;
 constexpr int kT8Warps = 16, kT8Threads = kT8Warps * 32, kT8CtasPerSm = 2;
 static_assert(kT8CtasPerSm * (kT8Smem + 1024 + 1024) <= 233472, "two CTAs' shared memory on one SM");
-static_assert((kMaxBatch + 1) * 8 <= kT8Stages * kT8StageBytes, "the prefix of units fits the stages");
+static_assert((kMaxBatch + 1) * 12 <= kT8Stages * kT8StageBytes, "the prefixes of costs and segments fit the stages");
 constexpr uint32_t kT8TmemCols = 256, kT8ColS = 0, kT8ColO = 128, kT8ColP = 192;  // S and P: two buffers each
 constexpr float kT8Shift = 7.f, kT8TileMax = 32768.f;  // log2 of the probabilities' unit; the most a tile's may add up to
 constexpr int kT8MaxE = 100, kT8MaxF = 60;
 constexpr int kT8Counters = 4 * kT8CtasPerSm * kMaxSms;  // arrivals at a shared segment: one per row warp, at its first CTA
-constexpr int kT8MinUnits = 4;                         // units per CTA at least, where there are so few
+// What a segment's start and end cost, in units. A prompt's first row blocks see few keys, and CTAs that took as many
+// units as the others had several times their segments. With 0 / 3 / 6 / 9 / 12, four prompts took 333 / 276 / 268 / 274 /
+// 279 us, 64 sequences x 16 tokens 165 / 158 / 156 / 159 / 162, slots behind a window 82 / 79 / 78 / 79 / 81, and a
+// 512-token chunk, whose segments are alike, 130 / 130 / 130 / 132 / 133.
+#ifndef DA_T8_SEG
+#define DA_T8_SEG 6
+#endif
+constexpr int kT8SegCost = DA_T8_SEG;
+// A CTA's share at least, where there is so little: with 4 / 8 / 10, 36 short slots (9 to 300 tokens) took 35 / 30 / 32 us,
+// 16 tokens behind 1024 30 / 31 / 28, behind 4096 28 / 27 / 28, four prompts of 100 to 300 42 each.
+#ifndef DA_T8_MIN
+#define DA_T8_MIN 8
+#endif
+constexpr int kT8MinCost = DA_T8_MIN;
 constexpr size_t kT8SlotFloats = static_cast<size_t>(kT8Rows) * (2 + kD);
 
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
@@ -127,77 +140,125 @@ __device__ __forceinline__ T8Keys t8_keys(const MultiParams &p, const T8Seq &s, 
     k.units = (k.ntiles + kT8Tiles - 1) / kT8Tiles;
     return k;
 }
-// The units of one KV head of sequence b, added up by a warp.
-__device__ __forceinline__ long long t8_units(const MultiParams &p, int b, int lane) {
-    const T8Seq s = t8_seq(p, b);
-    long long sum = 0;
-    for (int rb = lane; rb < s.blocks; rb += 32) sum += t8_keys(p, s, rb).units;
+// The cost of a row block.
+__device__ __forceinline__ int t8_cost(const MultiParams &p, const T8Seq &s, int rb) { return kT8SegCost + t8_keys(p, s, rb).units; }
+
+// a[1 .. B] added up by a warp, from a[0] = 0.
+template <typename N>
+__device__ __forceinline__ void t8_scan(N *a, int B, int lane) {
+    N run = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + lane;
+        N x = b < B ? a[b + 1] : 0;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    return sum;
+        for (int off = 1; off < 32; off <<= 1) {
+            const N y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (b < B) a[b + 1] = run + x;
+        run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) a[0] = 0;
 }
 
-// Exclusive prefix over the sequences of their units (all KV heads) into pre[0 .. B], by all threads of the CTA.
-__device__ __forceinline__ void t8_prefix(const MultiParams &p, long long *pre, int warp, int nwarps, int lane) {
+// Exclusive prefixes over the sequences (all KV heads) of their cost into pre[0 .. B] and of their segments into segs
+// (null: not wanted), by all threads of the CTA.
+__device__ __forceinline__ void t8_prefix(const MultiParams &p, long long *pre, int *segs, int warp, int nwarps, int lane) {
     const int tid = warp * 32 + lane;
     if (p.row_blocks <= 4) {  // a thread per sequence
         for (int b = tid; b < p.B; b += nwarps * 32) {
             const T8Seq s = t8_seq(p, b);
             long long sum = 0;
-            for (int rb = 0; rb < s.blocks; ++rb) sum += t8_keys(p, s, rb).units;
+            for (int rb = 0; rb < s.blocks; ++rb) sum += t8_cost(p, s, rb);
             pre[b + 1] = sum * p.Hkv;
+            if (segs != nullptr) segs[b + 1] = s.blocks * p.Hkv;
         }
     } else {
         for (int b = warp; b < p.B; b += nwarps) {
-            const long long sum = t8_units(p, b, lane);
-            if (lane == 0) pre[b + 1] = sum * p.Hkv;
+            const T8Seq s = t8_seq(p, b);
+            long long sum = 0;
+            for (int rb = lane; rb < s.blocks; rb += 32) sum += t8_cost(p, s, rb);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) {
+                pre[b + 1] = sum * p.Hkv;
+                if (segs != nullptr) segs[b + 1] = s.blocks * p.Hkv;
+            }
         }
     }
     __syncthreads();
-    if (warp == 0) {
-        long long run = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            long long x = b < p.B ? pre[b + 1] : 0;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, off);
-                if (lane >= off) x += y;
-            }
-            if (b < p.B) pre[b + 1] = run + x;
-            run += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (lane == 0) pre[0] = 0;
-    }
+    if (warp == 0) t8_scan(pre, p.B, lane);
+    if (warp == 1 && segs != nullptr) t8_scan(segs, p.B, lane);
     __syncthreads();
 }
 
-// CTA c of nc takes the units [c U / nc, (c + 1) U / nc); the CTA that holds unit x.
+// CTA c of nc takes the places [c U / nc, (c + 1) U / nc) of all U; the CTA that holds place x.
 __device__ __forceinline__ long long t8_first(long long U, int nc, int c) { return c * U / nc; }
 __device__ __forceinline__ int t8_owner(long long U, int nc, long long x) { return static_cast<int>(((x + 1) * nc - 1) / U); }
 __device__ __forceinline__ int t8_ctas(long long U, int grid) {
-    return static_cast<int>(max(1ll, min(static_cast<long long>(grid), (U + kT8MinUnits - 1) / kT8MinUnits)));
+    return static_cast<int>(max(1ll, min(static_cast<long long>(grid), (U + kT8MinCost - 1) / kT8MinCost)));
+}
+
+// The segment that place x lies in, found by a warp.
+struct T8At {
+    int b, g, rb, units;
+    long long begin, before;  // the place of its first unit; the units of all segments before it
+};
+__device__ __forceinline__ T8At t8_at(const MultiParams &p, const long long *pre, const int *segs, long long x, int lane) {
+    int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before it
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    const T8Seq s = t8_seq(p, lo);
+    const long long per = (pre[lo + 1] - pre[lo]) / p.Hkv;
+    T8At at;
+    at.b = lo;
+    at.g = static_cast<int>((x - pre[lo]) / per);
+    at.rb = at.units = 0;
+    long long start = pre[lo] + at.g * per;
+    for (int r0 = 0; r0 < s.blocks; r0 += 32) {  // 32 row blocks at a time
+        const int u = r0 + lane < s.blocks ? t8_cost(p, s, r0 + lane) : 0;
+        int sum = u;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += y;
+        }
+        const uint32_t in = __ballot_sync(0xffffffffu, x < start + sum);
+        if (in != 0) {
+            const int k = __ffs(static_cast<int>(in)) - 1;
+            start += __shfl_sync(0xffffffffu, sum - u, k);
+            at.rb = r0 + k;
+            at.units = __shfl_sync(0xffffffffu, u, k) - kT8SegCost;
+            break;
+        }
+        start += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    at.begin = start + kT8SegCost;
+    at.before = start - static_cast<long long>(kT8SegCost) * (segs[lo] + at.g * s.blocks + at.rb);
+    return at;
 }
 
 // A walk over a CTA's units, segment by segment: the segment's place and keys, and the units [u0, u1)
 // of it that are the CTA's.
 struct T8Walk {
     int b, g, rb, u0, u1;
-    long long left;  // the CTA's units after this segment
+    long long begin, end;  // the place of the segment's first unit, the CTA's last place + 1
     T8Seq seq;
     T8Keys keys;
-    __device__ __forceinline__ void cut() {
-        u1 = static_cast<int>(min(static_cast<long long>(keys.units), u0 + left));
-        left -= u1 - u0;
-    }
-    __device__ __forceinline__ void start(const MultiParams &p, const int4 &at, long long units) {
-        b = at.x, g = at.y, rb = at.z, u0 = at.w, left = units;
+    __device__ __forceinline__ void cut() { u1 = static_cast<int>(min(static_cast<long long>(keys.units), end - begin)); }
+    __device__ __forceinline__ void start(const MultiParams &p, const int4 &at, const long long *range) {
+        b = at.x, g = at.y, rb = at.z, u0 = at.w, begin = range[0], end = range[1];
         seq = t8_seq(p, b);
         keys = t8_keys(p, seq, rb);
         cut();
     }
     __device__ __forceinline__ bool next(const MultiParams &p) {  // false: that was the last one
-        if (left <= 0) return false;
+        const long long then = begin + keys.units + kT8SegCost;
+        if (then >= end) return false;
+        begin = then;
         if (++rb >= seq.blocks) {
             rb = 0;
             if (++g >= p.Hkv) {
@@ -218,7 +279,7 @@ struct T8Seg {
     int b, g, rb, n, base;        // base: position of the first new token
     int pt_lo, u0, u1, units;     // first tile; the CTA's units [u0, u1) of all
     int last;
-    long long begin;              // the segment's first unit among the call's
+    long long begin;              // the place of the segment's first unit
 };
 
 // Partials of a segment: m [128 rows], l [128 rows], O as [16][128 rows] float4 (so that 32 rows' loads and stores are
@@ -290,7 +351,8 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
     __shared__ int s_keys[kT8Raw][kT8Tiles];
     __shared__ T8Seg s_seg[4];
     __shared__ int4 s_start;
-    __shared__ long long s_range[3];  // the CTA's first unit, its units, all units
+    __shared__ long long s_range[3];  // the place of the first segment's first unit, the CTA's last place + 1, all places
+    __shared__ long long s_before[2]; // the units before the CTA's places, and before those after them
     __shared__ uint32_t s_tmem;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -324,46 +386,26 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
 
     // ---- the CTA's units; the output rows that have no query: zeros
     long long *pre = reinterpret_cast<long long *>(sKV);
-    t8_prefix(p, pre, warp, kT8Warps, lane);
+    int *segs = reinterpret_cast<int *>(pre + kMaxBatch + 1);
+    t8_prefix(p, pre, segs, warp, kT8Warps, lane);
     const long long U = pre[p.B];
     const int nc = t8_ctas(U, gridDim.x), cta = blockIdx.x;
-    if (warp == 0) {
-        const long long first = cta < nc ? t8_first(U, nc, cta) : U, units = (cta < nc ? t8_first(U, nc, cta + 1) : U) - first;
-        if (units > 0) {
-            int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before it
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (pre[mid] <= first) lo = mid;
-                else hi = mid - 1;
+    if (warp < 2) {
+        const long long first = cta < nc ? t8_first(U, nc, cta) : U, end = cta < nc ? t8_first(U, nc, cta + 1) : U;
+        const long long x = warp == 0 ? first : end;
+        long long before = U - static_cast<long long>(kT8SegCost) * segs[p.B];
+        if (x < U) {
+            const T8At at = t8_at(p, pre, segs, x, lane);
+            const long long u = max(0ll, x - at.begin);  // its units before x
+            before = at.before + u;
+            if (warp == 0 && lane == 0) {
+                s_start = make_int4(at.b, at.g, at.rb, static_cast<int>(u));
+                s_range[0] = at.begin;
             }
-            const T8Seq s = t8_seq(p, lo);
-            const long long per = (pre[lo + 1] - pre[lo]) / p.Hkv;
-            const int g = static_cast<int>((first - pre[lo]) / per);
-            long long x = first - pre[lo] - g * per;
-            int rb = 0;
-            for (int r0 = 0; r0 < s.blocks; r0 += 32) {  // 32 row blocks at a time
-                const int u = r0 + lane < s.blocks ? t8_keys(p, s, r0 + lane).units : 0;
-                int sum = u;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, sum, off);
-                    if (lane >= off) sum += y;
-                }
-                const uint32_t in = __ballot_sync(0xffffffffu, x < sum);
-                if (in != 0) {
-                    const int at = __ffs(static_cast<int>(in)) - 1;
-                    x -= __shfl_sync(0xffffffffu, sum - u, at);
-                    rb = r0 + at;
-                    break;
-                }
-                x -= __shfl_sync(0xffffffffu, sum, 31);
-            }
-            if (lane == 0) s_start = make_int4(lo, g, rb, static_cast<int>(x));
         }
         if (lane == 0) {
-            s_range[0] = first;
-            s_range[1] = units;
-            s_range[2] = U;
+            s_before[warp] = before;
+            s_range[1 + warp] = warp == 0 ? end : U;
         }
     }
     for (int i = cta; i < p.B * p.row_blocks; i += gridDim.x) {
@@ -383,7 +425,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tmem;
-    const int units = static_cast<int>(s_range[1]);
+    const int units = static_cast<int>(s_before[1] - s_before[0]);
 
     bool failed = false;
     if (warp >= 4 && warp < 12) {
@@ -505,7 +547,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             // ---- copies: lane u < 4 the block of tile u of every unit
             const uint64_t policy = evict_first_policy();
             T8Walk w;
-            w.start(p, s_start, units);
+            w.start(p, s_start, s_range);
             int wu = w.u0;
             // the block-table entry of the next copy is read one copy early; -2: past the segment's tiles
             auto page_of = [&]() {
@@ -556,8 +598,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
         } else if (warp >= 14 && units > 0) {
             // ---- query rows as fp16 (zeros past the valid ones), 64 by each of the two warps, a segment ahead of the rows
             T8Walk w;
-            w.start(p, s_start, units);
-            long long begin = s_range[0] - w.u0;
+            w.start(p, s_start, s_range);
             bool more = true;
             for (int k = 0; more; ++k) {
                 const int buf = k & 1;
@@ -568,7 +609,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 T8Walk ahead = w;
                 more = ahead.next(p);
                 if (warp == 14 && lane == 0)  // (the rows are past segment k - 3: they have looked at segment k - 2)
-                    s_seg[k & 3] = T8Seg{w.b, w.g, w.rb, w.seq.n, w.seq.L - w.seq.n, w.keys.pt_lo, w.u0, w.u1, w.keys.units, more ? 0 : 1, begin};
+                    s_seg[k & 3] = T8Seg{w.b, w.g, w.rb, w.seq.n, w.seq.L - w.seq.n, w.keys.pt_lo, w.u0, w.u1, w.keys.units, more ? 0 : 1, w.begin};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int rl = (warp - 14) * 64 + 32 * h + lane, r = w.rb * kT8Rows + rl, t = r / p.G;
@@ -590,7 +631,6 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the tensor cores
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full + 8 * buf);
-                begin += w.keys.units;
                 w = ahead;
             }
         } else if (warp == 12 && units > 0) {
@@ -862,7 +902,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 if (__shfl_sync(0xffffffffu, ticket, 0) == c1 - c0) {
                     __threadfence();
                     if (r < r_end)
-                        t8_fold(p, c0, t8_first(U, nc, c0) < w.begin ? 1 : 0, c1 - c0 + 1, tid, w.g * p.G + (r - t * p.G), valid, dst);
+                        t8_fold(p, c0, t8_first(U, nc, c0) < w.begin - kT8SegCost ? 1 : 0, c1 - c0 + 1, tid, w.g * p.G + (r - t * p.G), valid, dst);
                 }
             }
             if (w.last) break;
@@ -897,15 +937,16 @@ __global__ void __launch_bounds__(kT8FoldWarps * 32) t8_combine_kernel(const Mul
     const int g = blockIdx.y, b = blockIdx.z;
     const T8Seq s = t8_seq(p, b);
     if (rb >= s.blocks) return;  // zeros, written by the attention
-    t8_prefix(p, sh.pre, warp, kT8FoldWarps, lane);
+    t8_prefix(p, sh.pre, nullptr, warp, kT8FoldWarps, lane);
     const long long U = sh.pre[p.B];
     const int nc = t8_ctas(U, grid);
     long long begin = sh.pre[b] + (sh.pre[b + 1] - sh.pre[b]) / p.Hkv * g;
-    for (int i = 0; i < rb; ++i) begin += t8_keys(p, s, i).units;
+    for (int i = 0; i < rb; ++i) begin += t8_cost(p, s, i);
+    begin += kT8SegCost;
     const int c0 = t8_owner(U, nc, begin), c1 = t8_owner(U, nc, begin + t8_keys(p, s, rb).units - 1);
     const int r0 = rb * kT8Rows;
     if (c0 == c1 || r0 + blockIdx.x % 4 * 32 >= p.T * p.G) return;
-    const int count = c1 - c0 + 1, k0 = t8_first(U, nc, c0) < begin ? 1 : 0;
+    const int count = c1 - c0 + 1, k0 = t8_first(U, nc, c0) < begin - kT8SegCost ? 1 : 0;
     const int r = r0 + rl, t = r / p.G, hl = r - t * p.G;
     const bool row = r < p.T * p.G, query = row && t < s.n;
     float M = -INFINITY;
