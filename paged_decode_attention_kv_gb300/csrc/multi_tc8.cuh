@@ -77,14 +77,15 @@ static_assert(kT8CtasPerSm * (kT8Smem + 1024 + 1024) <= 233472, "two CTAs' share
 static_assert((kMaxBatch + 1) * 12 <= kT8Stages * kT8StageBytes, "the prefixes of costs and segments fit the stages");
 constexpr uint32_t kT8TmemCols = 256, kT8ColS = 0, kT8ColO = 128, kT8ColP = 192;  // S and P: two buffers each
 constexpr float kT8Shift = 7.f, kT8TileMax = 32768.f;  // log2 of the probabilities' unit; the most a tile's may add up to
+constexpr float kT8Ahead = 8.f;  // log2 of how far a score may lie above the reference (none alone passes kT8TileMax then)
 constexpr int kT8MaxE = 100, kT8MaxF = 60;
 constexpr int kT8Counters = 4 * kT8CtasPerSm * kMaxSms;  // arrivals at a shared segment: one per row warp, at its first CTA
 // What a segment's start and end cost, in units. A prompt's first row blocks see few keys, and CTAs that took as many
-// units as the others had several times their segments. With 0 / 3 / 6 / 9 / 12, four prompts took 333 / 276 / 268 / 274 /
-// 279 us, 64 sequences x 16 tokens 165 / 158 / 156 / 159 / 162, slots behind a window 82 / 79 / 78 / 79 / 81, and a
-// 512-token chunk, whose segments are alike, 130 / 130 / 130 / 132 / 133.
+// units as the others had several times their segments. With 3 / 4 / 5 / 6, four prompts took 237 / 230 / 232 / 235 us,
+// 64 sequences x 16 tokens 150 / 148 / 150 / 149, slots behind a window 75 each, a 512-token chunk 123 each; with 0
+// instead of 6, when a start cost more than now, 333 instead of 268, 165 instead of 156 and 82 instead of 78.
 #ifndef DA_T8_SEG
-#define DA_T8_SEG 6
+#define DA_T8_SEG 4
 #endif
 constexpr int kT8SegCost = DA_T8_SEG;
 // A CTA's share at least, where there is so little: with 4 / 8 / 10, 36 short slots (9 to 300 tokens) took 35 / 30 / 32 us,
@@ -702,10 +703,12 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
         if (units > 0) {
         const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
         int i = 0, st = 0;
+        float R = -INFINITY;
         for (int seg = 0; !failed; ++seg) {
             int pr, lor, jf, count;  // the row's keys [lor, pr], the unit's first position, the segment's units here
             bool valid, warp_active;
-            float sink = -INFINITY;  // log2 units
+            int place;  // the row's among its sequence's output rows, or -1
+            float sink = -INFINITY;
             if (__any_sync(0xffffffffu, !mbar_wait_bounded(q_full + 8 * (seg & 1), (seg >> 1) & 1))) {
                 failed = true;
                 break;
@@ -713,17 +716,18 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             {
                 const T8Seg &w = s_seg[seg & 3];
                 const int r = w.rb * kT8Rows + tid, r_valid = w.n * p.G, t = r / p.G;
+                place = t < p.T ? t * p.Hq + w.g * p.G + (r - t * p.G) : -1;
                 valid = r < r_valid;
                 warp_active = w.rb * kT8Rows + 32 * warp < r_valid;
                 pr = valid ? w.base + t : -1;
                 lor = valid && p.window > 0 ? max(0, w.base + t - p.window + 1) : 0;
                 jf = (w.pt_lo + w.u0 * kT8Tiles) * kPage;
                 count = w.u1 - w.u0;
-                if (valid && p.sinks != nullptr) sink = __ldg(p.sinks + w.g * p.G + (r - t * p.G)) * kLog2e;
+                if (valid && p.sinks != nullptr) sink = __ldg(p.sinks + w.g * p.G + (r - t * p.G));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(q_free + 8 * (seg & 1));
-            float R = -INFINITY, l = 0.f;
+            float l = 0.f;
             for (int k = 0; k < count && !failed; ++k, ++i, jf += kT8Keys) {
                 const int sb = i & 1;
                 // every row warp waits for S_i, rows or not, so that no warp's arrival on p_full can run ahead
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                         return add2(ls[0], ls[1]);
                     };
                     // (a tile's scores are fetched while the one before is worked on; the sums are looked at at the end, where
-                    // their latencies overlap); true: a probability may be too large
+                    // their latencies overlap); the largest tile's sum
                     auto probabilities = [&]() {
                         uint32_t x0[16], x1[16];
                         tmem_ld16(sc, x0);
@@ -784,10 +788,15 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                         const float2 s3 = tile(3, x1);
                         const float t0 = s0.x + s0.y, t1 = s1.x + s1.y, t2 = s2.x + s2.y, t3 = s3.x + s3.y;
                         l_unit = fmaf(t0, fac[0].z, t1 * fac[1].z) + fmaf(t2, fac[2].z, t3 * fac[3].z);
-                        return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) > kT8TileMax;
+                        return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
                     };
                     bool need = R == -INFINITY && valid;
-                    if (!__any_sync(0xffffffffu, need)) need = probabilities();
+                    if (!__any_sync(0xffffffffu, need)) {
+                        // a segment's first unit is tried with the last one's reference (mostly the same head's, a few tokens
+                        // before), kept where the probabilities have not sunk in fp16's range
+                        const float top = probabilities();
+                        need = top > kT8TileMax || (k == 0 && valid && !(top >= 16.f));
+                    }
                     if (__any_sync(0xffffffffu, need)) {
                         float mb = -INFINITY;
 #pragma unroll 1
@@ -802,8 +811,10 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                             for (int c = 0; c < 16; c += 2) mt = max3(mt, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
                             mb = fmaxf(mb, fmaf(mt, f.x, f.y));  // the multiplier is positive
                         }
-                        const float Rn = need ? fmaxf(R, ceilf(mb)) : R;  // an integer: F - R and the rescaling are exact
-                        const float f = Rn == R ? 1.f : exp2f(R - Rn);    // R = -inf: 0 (O and l are 0)
+                        // (also where a row without a reference called for this, and nothing was tried)
+                        need = need || (valid && (k == 0 || mb > R + kT8Ahead));
+                        const float Rn = need ? (k == 0 ? ceilf(mb) : fmaxf(R, ceilf(mb))) : R;  // an integer: F - R and the rescaling are exact
+                        const float f = k == 0 || Rn == R ? 1.f : exp2f(R - Rn);  // R = -inf: 0 (O and l are 0)
                         if (k > 0) {
                             // O holds the segment's PVs up to PV_{i-1}, whose barrier cannot be a phase further:
                             // PV_{i+1} waits for P_{i+1}
@@ -842,9 +853,8 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 failed = true;
             if (failed) break;
             const T8Seg &w = s_seg[seg & 3];
-            const int r0 = w.rb * kT8Rows, r = r0 + tid, r_end = min(r0 + kT8Rows, p.T * p.G), t = r / p.G;
-            uint4 *const dst = reinterpret_cast<uint4 *>(
-                p.out + (r < r_end ? ((static_cast<size_t>(w.b) * p.T + t) * p.Hq + w.g * p.G + (r - t * p.G)) * kD : 0));
+            if (l == 0.f) R = -INFINITY;  // no key of the row here
+            sink *= kLog2e;
             const bool whole = w.u0 == 0 && w.u1 == w.units;
             const float m_row = R - kT8Shift;
             float f = 0.f;  // rows that are not queries: zeros
@@ -861,36 +871,35 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 slot[kT8Rows + tid] = l;
             }
             tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t x[16];
-                if (warp_active) {
-                    tmem_ld16(tm + lanes + kT8ColO + 16 * h, x);
-                    tmem_wait_ld();
-                }
+            uint4 *const dst = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(w.b) * p.T * p.Hq + max(place, 0)) * kD);
+            auto columns = [&](int h, uint32_t(&x)[16]) {  // columns 16 h .. + 15
                 float o[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) o[c] = valid ? __uint_as_float(x[c]) : 0.f;
                 if (whole) {
-                    if (r < r_end) {
+                    if (place >= 0) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint4 y;
-                            y.x = pack_bf16(o[8 * c] * f, o[8 * c + 1] * f);
-                            y.y = pack_bf16(o[8 * c + 2] * f, o[8 * c + 3] * f);
-                            y.z = pack_bf16(o[8 * c + 4] * f, o[8 * c + 5] * f);
-                            y.w = pack_bf16(o[8 * c + 6] * f, o[8 * c + 7] * f);
-                            dst[2 * h + c] = y;
-                        }
+                        for (int c = 0; c < 2; ++c)
+                            dst[2 * h + c] = make_uint4(pack_bf16(o[8 * c] * f, o[8 * c + 1] * f), pack_bf16(o[8 * c + 2] * f, o[8 * c + 3] * f),
+                                                        pack_bf16(o[8 * c + 4] * f, o[8 * c + 5] * f), pack_bf16(o[8 * c + 6] * f, o[8 * c + 7] * f));
                     }
                 } else if (valid) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         *const_cast<float4 *>(t8_acc(slot, 4 * h + c, tid)) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 }
+            };
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t x[16] = {};
+                if (warp_active) {
+                    tmem_ld16(tm + lanes + kT8ColO + 16 * h, x);
+                    tmem_wait_ld();
+                }
+                columns(h, x);
             }
             tc_fence_before();  // (the next segment's first PV writes O after this warp's next P)
-            if (!whole && !p.defer && r0 + 32 * warp < r_end) {
+            if (!whole && !p.defer && __any_sync(0xffffffffu, place >= 0)) {
                 // the last of the CTAs that share the segment folds its partials, every warp its own 32 rows: a
                 // counter per warp, at the segment's first CTA (which has no other segment that goes on)
                 const long long U = s_range[2];
@@ -901,8 +910,8 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 if (lane == 0) ticket = atomicAdd(p.counters + 4 * c0 + warp, 1);
                 if (__shfl_sync(0xffffffffu, ticket, 0) == c1 - c0) {
                     __threadfence();
-                    if (r < r_end)
-                        t8_fold(p, c0, t8_first(U, nc, c0) < w.begin - kT8SegCost ? 1 : 0, c1 - c0 + 1, tid, w.g * p.G + (r - t * p.G), valid, dst);
+                    if (place >= 0)
+                        t8_fold(p, c0, t8_first(U, nc, c0) < w.begin - kT8SegCost ? 1 : 0, c1 - c0 + 1, tid, place % p.Hq, valid, dst);
                 }
             }
             if (w.last) break;

@@ -260,3 +260,36 @@ def test_captured_calls_and_streams(T):
         assert da.decode_attn_device_status() == 0
     finally:
         da.decode_attn_stream_release(side)
+
+
+@pytest.mark.parametrize("lens", ["short", "units"])
+def test_segments_far_from_one_another(lens):
+    """Many short sequences whose scores lie up to 800 apart from one KV head to the next (the last element of every key
+    is 16, exactly, in every form that it takes; the queries' says how far): nothing of one may be left to the next.
+    A softmax does not change by what all of its scores share, so the bar is that of ordinary inputs."""
+    B = 96 if lens == "short" else 40
+    L = [17 + 13 * b % 50 for b in range(B)] if lens == "short" else [16 + 37 * b % 400 for b in range(B)]
+    m = Multi(1995 + B, 64, 8, L, [16 - b % 3 for b in range(B)], 16)
+    for hist in (m.c.hist_k, [m.k_new]):
+        for k in hist:
+            k[..., 63] = 0x4180  # 16 in bf16
+    offset = np.array([0.0, 400.0, -400.0, 32.0, -4.0], np.float32)[(3 * np.arange(B)[:, None] + np.arange(8)[None, :]) % 5]
+    m.q[..., 63] = np.repeat(offset.view(np.uint32) >> 16, 8, axis=1)[:, None, :].astype(np.uint16)
+    run(m, 0, sinks=False)
+    run(m, 40, sinks=False)
+    run(m, 0)
+
+
+def test_rows_without_a_reference_beside_rows_left_behind():
+    """Behind a window of 70, tokens 32 .. 63 of 128 share a warp; the first keys are cut into 96 .. 159 and 160 .. 223. The
+    last seven of the tokens see none of the first, the others a few, whose scores lie 300 below those of the second:
+    all of them find their reference there at the same time."""
+    L, T = 300, 128
+    m = Multi(1998, 4, 4, [L, L, L], [T, T, T], T)
+    for at in range(160, L):  # (the history is the first L - T)
+        (m.c.hist_k[:, at] if at < L - T else m.k_new[:, at - (L - T)])[..., 63] = 0x4180  # 16
+    for at in range(160):
+        m.c.hist_k[:, at, :, 63] = 0
+    m.q[..., 63] = 0x4316  # 150 in bf16: 0.125 * 16 * 150 = 300
+    for window in (70, 75, 40, 0):
+        run(m, window, sinks=False)
