@@ -3102,7 +3102,10 @@ int run_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t
 #define DA_T8_DEFER 4
 #endif
 // How a several-token call over fp8 pages is cut: the decode kernel's several-token form as
-// multi_plan has it, else multi_tc8_kernel. Of shapes only, like multi_plan.
+// multi_plan has it (up to four tokens, at most 32 rows per KV head), else multi_tc8_kernel. Of shapes only, like
+// multi_plan. Both sides, us back to back, decode kernel and tcgen05: 32 sequences of 1024 to 8192 tokens, 8 heads per KV
+// head, 4 tokens 91 and 106, 3 tokens 88 and 105, 2 tokens 66 and 105; 2 tokens of 16 heads 87 and 106; 64 sequences, 4
+// tokens 139 and 166; 4 sequences 30 and 41; 4 tokens behind 131072 69 and 77.
 MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, int sms) {
     MultiPlan m = multi_plan(s, T, false, window, max_seq_len, sms);
     if (m.dec) return m;
@@ -3115,7 +3118,8 @@ MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, 
     m.groups = static_cast<long long>(s.batch) * s.num_kv_heads * m.row_blocks;
     m.splits = 1;
     m.chunk = 0;
-    // segments so few that each is spread over four CTAs or more, if they are about equally long
+    // Segments so few that each is spread over four CTAs or more, if they are about equally long: the fold is a kernel of
+    // its own. 16 tokens behind 8192, with it / without: 8 segments 30 / 72 us, 32 35 / 46, 72 52 / 56, 152 89 / 82.
     m.defer = m.groups * DA_T8_DEFER <= static_cast<long long>(kT8CtasPerSm) * sms;
     m.counter_bytes = static_cast<size_t>(kMMaxGroups) * sizeof(int);
     // two slots per CTA, then its counters (not among those that are zero at rest: every call clears them itself)

@@ -39,19 +39,22 @@
 // 2400 cycles a unit. Registers go where they are needed (setmaxnreg): 64 a thread at launch, then 88 for
 // the rows, 56 for the others, 4 x 64 in all.
 // The softmax takes the probabilities with the reference it has, and looks for a larger one only if a
-// tile's sum shows that one may have left fp16's range (or the row has no reference yet): the scores then
-// still stand in TMEM (P has its own columns) and are taken again. The maxima of every unit cost 40 of its
-// 230 instructions. It works a tile (16 keys) at a time and fetches the next one's scores meanwhile: 32 keys at a
-// time, one after the other, took 173 us for 64 x 16 tokens, this 168, and 164 with the unit's sums added up at its end.
+// tile's sum shows that one may have left fp16's range: the scores then still stand in TMEM (P has its own columns)
+// and are taken again. The maxima of every unit cost 40 of its 230 instructions. A segment's first unit is tried with
+// the last segment's reference and taken again if its probabilities are too small for fp16, too (without: four prompts
+// 297 us instead of 262). It works a tile (16 keys) at a time and fetches the next one's scores meanwhile: 32 keys at a
+// time, one after the other, took 173 us for 64 x 16 tokens instead of 168.
 //
-// What bounds it: the row warps' chain S complete -> scores -> probabilities -> P stored -> arrival, about 1920 cycles
-// a unit with two CTAs on an SM (1440 alone), in which the SM issues 54% of the time (2500 instructions a unit: rows
-// 1090, teams 690, waits, copies and MMAs the rest); the tensor cores work 21% of it, the exponentials' unit 256 cycles
-// a unit. A segment's start and end cost about 12000 cycles, a CTA's first unit is 17000 cycles from its launch.
-// 64 sequences of 1024 to 8192 tokens, 16 tokens each: 164 us (2.0 TB/s, 457 TFLOP/s); 512 tokens behind 7680: 128 us
-// (520 TFLOP/s); four prompts of 1201 to 2048: 328 us; G = 8, 64 query heads throughout. Tried, without a gain: three
-// or four stages, more raw units, S and PV issued by two warps, the next S issued before P has arrived, all 64
-// scores in registers (they spill).
+// What bounds it: the ring S issued -> scores -> probabilities -> P stored -> PV issued, and behind it the stage that PV
+// frees and the teams' next operands: about 2000 cycles a unit with two CTAs on an SM, 1400 of them the rows' work. The SM
+// issues 54% of the time (2500 instructions a unit: rows 1090, teams 690, waits, copies and MMAs the rest); the tensor
+// cores work 21% of it, the exponentials' unit 256 cycles a unit. A segment's start and end are worth about 4 units.
+// 64 sequences of 1024 to 8192 tokens, 16 tokens each: 147 us (2.2 TB/s, 508 TFLOP/s); 512 tokens behind 7680: 123 us
+// (542 TFLOP/s); four prompts of 1201 to 2048: 231 us; 16 tokens behind 65536 of 19 sequences: 643 TFLOP/s; G = 8, 64
+// query heads throughout. Tried, without a gain or slower: four stages, more raw units, S and PV issued by two warps, S_i
+// issued before PV_{i-2} (the stage comes free later: 171 us instead of 156), outputs through shared memory in whole lines
+// (the query buffer is then held to the segment's end: 297 us instead of 268 for the prompts), registers 96 / 56 / 48,
+// 88 / 48 / 72, 80 / 56 / 64, 104 / 48 / 56, all 64 scores in registers (they spill).
 constexpr int kT8Rows = 128, kT8Keys = 64, kT8Tiles = kT8Keys / kPage;
 #ifndef DA_T8_STAGES
 #define DA_T8_STAGES 3
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 if (there) {
                     const uint8_t *src = kv + (static_cast<size_t>(page) * p.Hkv + w.g) * kBlk8Bytes;
                     const uint32_t dst = smem_addr(sRaw + (rs * kT8Tiles + lane) * kBlk8Bytes);
-                    if (p.row_blocks == 1)
+                    if (p.row_blocks == 1)  // (64 x 16 tokens: 164 us, 166 without the hint)
                         bulk_load_hint(dst, src, kBlk8Bytes, bar, policy);
                     else  // other row blocks read it too
                         bulk_load(dst, src, kBlk8Bytes, bar);
