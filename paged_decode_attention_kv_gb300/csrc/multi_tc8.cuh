@@ -4,11 +4,14 @@
 // cache: query row (t, h) at position p = L - n + t attends the cached positions lo .. p.
 //
 // The codes are turned into fp16 operands in shared memory, their token's scale with them. A page
-// (16 tokens) has a power of two 2^E at least as large as its K scales, 2^F for its V scales, and
+// (16 tokens) has a power of two 2^E for its K scales, 2^F for its V scales, the largest scale below 2^7 times it, and
 //     K'_j = fp16(code_j ks_j 2^-E),   V'_j = fp16(code_j fp16(vs_j 2^-F)):
-// code times a factor in (0, 1], nothing to overflow. K' is rounded once (its factor is carried as two
+// code times a factor of at most 2^7: 448 x 128 = 57344, nothing to overflow, and a scale of 2^-20 of its page's largest
+// still has a factor with all of fp16's bits. K' is rounded once (its factor is carried as two
 // fp16 values: an error of the factor would move all of a token's score), V' twice, each time by at most
-// fp16's half step 2^-11. 2^E goes into the page's score multiplier; 2^F into the exponent of
+// fp16's half step 2^-11. A row of zeros, whose scale is 1 by the format whatever the rows around it, counts in
+// neither power: it would push small scales' factors below fp16's range, and in V all the other pages'
+// probabilities. 2^E goes into the page's score multiplier; 2^F into the exponent of
 // its probabilities, so that the output accumulates in one unit:
 //     s_j + F = (q K'_j) (scale log2(e) 2^E) + F,   P_j = fp16(2^(s_j + F - R + 7)),
 //     O = sum P_j V'_j = 2^(7-R) sum 2^(s_j) v_j,   l = sum over pages 2^-F sum P_j = 2^(7-R) sum 2^(s_j)
@@ -16,8 +19,9 @@
 // than 2^8, as in multi_tc_kernel): the probabilities stay below 2^15, and fp16 holds them to 2^-12 (to 2^-31 of the
 // largest for the smallest ones). Multiplying the scores by their token's scale in the softmax
 // instead would be exact, but every factor is then read from shared memory by every row: 4 bytes a
-// lane and key, more than the whole softmax takes. Scales beyond 2^100 (K) or outside 2^-60 ..
-// 2^60 (V) lose bits.
+// lane and key, more than the whole softmax takes. Scales below 2^-100 (K) and 2^-60 (V) lose bits; above 2^100 and
+// 2^60 an operand may become infinite. V's range is the narrower one because it stands in the exponents of fp32
+// probabilities: pages 2^120 apart still count in the same denominators.
 //
 // The work is cut on the device: a unit is a block of 64 keys of a segment (sequence, KV head, block of
 // 128 query rows); a segment costs its units and kT8SegCost more, for its start and end, and every CTA of the grid (two
@@ -81,7 +85,9 @@ static_assert((kMaxBatch + 1) * 12 <= kT8Stages * kT8StageBytes, "the prefixes o
 constexpr uint32_t kT8TmemCols = 256, kT8ColS = 0, kT8ColO = 128, kT8ColP = 192;  // S and P: two buffers each
 constexpr float kT8Shift = 7.f, kT8TileMax = 32768.f;  // log2 of the probabilities' unit; the most a tile's may add up to
 constexpr float kT8Ahead = 8.f;  // log2 of how far a score may lie above the reference (none alone passes kT8TileMax then)
-constexpr int kT8MaxE = 100, kT8MaxF = 60;
+// The power of two above a page's largest scale, at most (and at least, negated): scales up to 2^100, 2^60; and log2 of
+// what the factors may rise to.
+constexpr int kT8MaxE = 101, kT8MaxF = 61, kT8Room = 7;
 constexpr int kT8Counters = 4 * kT8CtasPerSm * kMaxSms;  // arrivals at a shared segment: one per row warp, at its first CTA
 // What a segment's start and end cost, in units. A prompt's first row blocks see few keys, and CTAs that took as many
 // units as the others had several times their segments. With 3 / 4 / 5 / 6, four prompts took 237 / 230 / 232 / 235 us,
@@ -468,13 +474,28 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                     vc[h] = make_uint4(vc[h].x & m[0], vc[h].y & m[1], vc[h].z & m[2], vc[h].w & m[3]);
                 }
             }
-            // the page's powers of two, and each token's factor (K: lanes 0-15, V: 16-31)
+            // rows of zeros, looked for where a scale is theirs (K: lanes 0-15, V: 16-31): they have no scale
+            if (__any_sync(0xffffffffu, sc == 1.f)) {
+                // (four lanes hold a K row, so that a token has four bits of a vote)
+                const uint32_t k0 = __ballot_sync(0xffffffffu, ((kc[0].x | kc[0].y | kc[0].z | kc[0].w) & 0x7f7f7f7fu) != 0);
+                const uint32_t k1 = __ballot_sync(0xffffffffu, ((kc[1].x | kc[1].y | kc[1].z | kc[1].w) & 0x7f7f7f7fu) != 0);
+                uint32_t any = (lane & 8 ? k1 : k0) >> (4 * (lane & 7)) & 15u;
+                // (a lane holds two elements of V of all tokens, four to a word)
+                const uint32_t w[4] = {vc[0].x | vc[1].x, vc[0].y | vc[1].y, vc[0].z | vc[1].z, vc[0].w | vc[1].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t all = __reduce_or_sync(0xffffffffu, w[e]);
+                    if (lane >> 2 == 4 + e) any = all >> (8 * (lane & 3)) & 127u;
+                }
+                if (any == 0) sc = 0.f;
+            }
+            // the page's powers of two, and each token's factor
             float top = fabsf(sc);
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             const int lim = lane < 16 ? kT8MaxE : kT8MaxF;
             const int ex = max(-lim, min(lim, static_cast<int>(__float_as_uint(top) >> 23) - 126));
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 + kT8Room - ex) << 23);
             const float fac = sc * down;
             const __half hi = __float2half_rn(fac), lo = __float2half_rn(fac - __half2float(hi));
             const uint32_t packed = static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
@@ -488,9 +509,9 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                 break;
             }
             float *fo = reinterpret_cast<float *>(s_fac + st * kT8Tiles + u);
-            if (lane == 0) fo[0] = fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23), 1.1754944e-38f);
+            if (lane == 0) fo[0] = fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - kT8Room + ex) << 23), 1.1754944e-38f);
             if (lane == 16) {
-                fo[1] = static_cast<float>(ex);
+                fo[1] = static_cast<float>(ex - kT8Room);
                 fo[2] = down;
                 fo[3] = __int_as_float(keys >> 16);
             }
