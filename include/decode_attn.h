@@ -478,13 +478,17 @@ DA_API int kv_read_fp8(const void *kv_cache, const int32_t *block_table, const i
 /*
  * decode_attn_paged_fp8_multi -- decode_attn_paged_multi over an fp8 cache. The n new tokens of a
  * sequence are quantised into their cells as kv_append_fp8 does it, and every key and value is
- * attended as it is cached, the new ones too: the output does not depend on how a prompt is cut into
- * calls. Masks, q_lens, window, sinks and zero rows as in decode_attn_paged_multi; scale_rule as in
- * kv_append_fp8. scale must be positive and finite. Query rows run in fp16 (|q| < 65504), and so do
- * the cached values times their page's power of two: a token's factor is rounded against its page's
- * largest one; V scales outside 2^-60 .. 2^60 lose bits. Cells outside a sequence's
- * [window start, length) may hold anything; the cached and the new tokens of a sequence must be
- * finite (a NaN may reach rows of its sequence that do not attend it).
+ * attended as it is cached, the new ones too: but for the rounding of its products the output does
+ * not depend on how a prompt is cut into calls. Masks, q_lens, window, sinks and zero rows as in
+ * decode_attn_paged_multi; scale_rule as in kv_append_fp8. scale must be positive and finite.
+ * Query rows run in fp16 (|q| < 65504; below 2^-14 bits are lost), and so do keys, values and
+ * probabilities, times powers of two: V scales of 2^-60 .. 2^60 and K scales of 2^-100 .. 2^100
+ * give the same digits whatever their size (smaller ones lose bits, larger ones may give
+ * infinities). Up to four tokens with T * G <= 32, each token has its own powers. Beyond, the 16
+ * tokens of a page share them: one whose K or V scale is below 2^-20 of the largest in its page,
+ * attended by the row or not, loses bits (rows of zeros have scale 1, but do not count). Cells
+ * outside a sequence's [window start, length) may hold anything; the cached and the new tokens of
+ * a sequence must be finite (a NaN may reach rows of its sequence that do not attend it).
  * One launch for up to four tokens with T * G <= 32, else two, and one more where a few blocks of
  * query rows share the whole GPU. q_tokens up to 4096. Multi-token workspace
  * (decode_attn_paged_fp8_multi_workspace_bytes, decode_attn_multi_reserve). The ring form is not

@@ -791,8 +791,15 @@ __global__ void __launch_bounds__(kThreads, CPS)
     constexpr bool kPair = NT == 1 && (KV8 ? DA_PAIR_FP8 : DA_PAIR_BF16);
     constexpr bool kLazy = KV8 ? DA_LAZY_MAX_FP8 : (MT ? DA_LAZY_MAX_MT : DA_LAZY_MAX_BF16);
     constexpr float kLazyT = KV8 ? kLazyLog2Fp8 : kLazyLog2;  // log2 of the largest probability
+    // fp8 with several query tokens: a V scale is mant 2^F, 1 <= mant < 2, and 2^F goes into the exponent of the token's
+    // probability, so that V of any size (scales of 2^-60 .. 2^60) gives the same digits:
+    //     P_j = fp16(2^(s_j + F_j - m) mant_j),  O = sum P_j code_j,  l = sum 2^(s_j + F_j - m) 2^-F_j,
+    // with m the running maximum of s_j + F_j, the largest contribution instead of the largest probability.
+    // (With the scales as they are in fp16, as the one-token calls have them, V of 1e-3 lost bits and V of 1e5 overflowed.)
+    constexpr bool kVExp = KV8 && MT;
+    constexpr int kVMaxExp = 60;  // (also of a token that has no scale: fp32 holds probabilities that far apart)
     // fp8: the power of two the V scales carry (taken out when a segment closes)
-    constexpr float kV8Factor = kLazy ? 16.f : 256.f;
+    constexpr float kV8Factor = kLazy && !kVExp ? 16.f : 256.f;
     constexpr bool kParIssue = KV8 ? DA_PAR_ISSUE_FP8 : DA_PAR_ISSUE_BF16;
 
     extern __shared__ uint8_t smem_raw[];
@@ -1414,6 +1421,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
             // their shared-memory latency overlaps the QK products
             uint32_t ka[UT][4][4], va[UT][4][4];
             float ks_lo[UT], ks_hi[UT], vs_lo[UT], vs_hi[UT];  // fp8 per-token scales
+            [[maybe_unused]] float ve_lo[UT], ve_hi[UT], vi_lo[UT], vi_hi[UT];  // (kVExp: F and 2^-F of the tokens)
 #pragma unroll
             for (int u = 0; u < UT; ++u) {
                 ks_lo[u] = ks_hi[u] = vs_lo[u] = vs_hi[u] = 1.f;
@@ -1440,14 +1448,49 @@ __global__ void __launch_bounds__(kThreads, CPS)
                     const float *ssr = reinterpret_cast<const float *>(wbase + s_off(stgs[u]));
                     ks_lo[u] = ssr[row_tok];
                     ks_hi[u] = ssr[row_tok + 2];
-                    // V scales carry a factor 2^8 (2^4 with the lazy maximum, whose
-                    // probabilities reach 2^4) so that the fp16 products stay normal; it is
-                    // taken out when the segment closes
-                    vs_lo[u] = ssr[kPage + row_tok] * kV8Factor;
-                    vs_hi[u] = ssr[kPage + row_tok + 2] * kV8Factor;
-                    if (partial[u]) {  // a row outside the attended range may hold a garbage scale
-                        vs_lo[u] = ok_lo[u] ? vs_lo[u] : 0.f;
-                        vs_hi[u] = ok_hi[u] ? vs_hi[u] : 0.f;
+                    if constexpr (kVExp) {
+                        vs_lo[u] = ssr[kPage + row_tok];
+                        vs_hi[u] = ssr[kPage + row_tok + 2];
+                        if (partial[u]) {  // a row outside the attended range may hold a garbage scale
+                            vs_lo[u] = ok_lo[u] ? vs_lo[u] : 0.f;
+                            vs_hi[u] = ok_hi[u] ? vs_hi[u] : 0.f;
+                        }
+                        // A row of zeros has scale 1 whatever the rows around it: it must not raise the maximum
+                        if (__any_sync(0xffffffffu, vs_lo[u] == 1.f || vs_hi[u] == 1.f)) {
+                            uint32_t w0 = 0u, w1 = 0u;  // tokens 4t, 4t + 1; 4t + 2, 4t + 3 of t = lane % 4
+#pragma unroll
+                            for (int mt = 0; mt < 4; ++mt) {
+                                w0 |= va[u][mt][0] | va[u][mt][1];
+                                w1 |= va[u][mt][2] | va[u][mt][3];
+                            }
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1) {
+                                w0 |= __shfl_xor_sync(0xffffffffu, w0, off);
+                                w1 |= __shfl_xor_sync(0xffffffffu, w1, off);
+                            }
+                            // this lane's tokens row_tok and row_tok + 2 are the same half of either word of lane row_tok / 4
+                            const uint32_t sign_off = (row_tok & 1) ? 0x7fff0000u : 0x7fffu;
+                            if ((__shfl_sync(0xffffffffu, w0, row_tok >> 2) & sign_off) == 0u) vs_lo[u] = 0.f;
+                            if ((__shfl_sync(0xffffffffu, w1, row_tok >> 2) & sign_off) == 0u) vs_hi[u] = 0.f;
+                        }
+                        auto split = [&](float &v, float &e, float &inv) {
+                            const int x = max(-kVMaxExp, min(kVMaxExp, static_cast<int>(__float_as_uint(v) >> 23 & 255u) - 127));
+                            e = static_cast<float>(x);
+                            inv = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
+                            v *= inv * kV8Factor;
+                        };
+                        split(vs_lo[u], ve_lo[u], vi_lo[u]);
+                        split(vs_hi[u], ve_hi[u], vi_hi[u]);
+                    } else {
+                        // V scales carry a factor 2^8 (2^4 with the lazy maximum, whose
+                        // probabilities reach 2^4) so that the fp16 products stay normal; it is
+                        // taken out when the segment closes
+                        vs_lo[u] = ssr[kPage + row_tok] * kV8Factor;
+                        vs_hi[u] = ssr[kPage + row_tok + 2] * kV8Factor;
+                        if (partial[u]) {  // a row outside the attended range may hold a garbage scale
+                            vs_lo[u] = ok_lo[u] ? vs_lo[u] : 0.f;
+                            vs_hi[u] = ok_hi[u] ? vs_hi[u] : 0.f;
+                        }
                     }
                 } else {
                     const uint32_t sK = k_tile(stgs[u]), sV = v_tile(stgs[u]);
@@ -1480,10 +1523,17 @@ __global__ void __launch_bounds__(kThreads, CPS)
                     }
                     const float sl_lo = KV8 ? p.scale_log2 * ks_lo[u] : p.scale_log2;
                     const float sl_hi = KV8 ? p.scale_log2 * ks_hi[u] : p.scale_log2;
-                    sv[u][0] = (sc[0] + sd[0]) * sl_lo;
-                    sv[u][1] = (sc[1] + sd[1]) * sl_lo;
-                    sv[u][2] = (sc[2] + sd[2]) * sl_hi;
-                    sv[u][3] = (sc[3] + sd[3]) * sl_hi;
+                    if constexpr (kVExp) {
+                        sv[u][0] = fmaf(sc[0] + sd[0], sl_lo, ve_lo[u]);
+                        sv[u][1] = fmaf(sc[1] + sd[1], sl_lo, ve_lo[u]);
+                        sv[u][2] = fmaf(sc[2] + sd[2], sl_hi, ve_hi[u]);
+                        sv[u][3] = fmaf(sc[3] + sd[3], sl_hi, ve_hi[u]);
+                    } else {
+                        sv[u][0] = (sc[0] + sd[0]) * sl_lo;
+                        sv[u][1] = (sc[1] + sd[1]) * sl_lo;
+                        sv[u][2] = (sc[2] + sd[2]) * sl_hi;
+                        sv[u][3] = (sc[3] + sd[3]) * sl_hi;
+                    }
                     if (partial[u]) {
                         if constexpr (MT) {  // this lane's two key rows against each column's range
                             const int kl = t0[u] + row_tok, kh = kl + (KV8 ? 2 : 8);
@@ -1563,8 +1613,13 @@ __global__ void __launch_bounds__(kThreads, CPS)
                     for (int u = 0; u < UT; ++u) {
                         const float p0 = fast_exp2(sv[u][0] - mr0), p1 = fast_exp2(sv[u][1] - mr1);
                         const float p2 = fast_exp2(sv[u][2] - mr0), p3 = fast_exp2(sv[u][3] - mr1);
-                        ls0 += p0 + p2;
-                        ls1 += p1 + p3;
+                        if constexpr (kVExp) {
+                            ls0 = fmaf(p0, vi_lo[u], fmaf(p2, vi_hi[u], ls0));
+                            ls1 = fmaf(p1, vi_lo[u], fmaf(p3, vi_hi[u], ls1));
+                        } else {
+                            ls0 += p0 + p2;
+                            ls1 += p1 + p3;
+                        }
                         if constexpr (KV8) {
                             pb[u][n][0] = movmatrix_t(pack_f16(p0 * vs_lo[u], p1 * vs_lo[u]));
                             pb[u][n][1] = movmatrix_t(pack_f16(p2 * vs_hi[u], p3 * vs_hi[u]));
@@ -1594,8 +1649,13 @@ __global__ void __launch_bounds__(kThreads, CPS)
                 for (int u = 0; u < UT; ++u) {
                     const float p0 = fast_exp2(sv[u][0] - mr0), p1 = fast_exp2(sv[u][1] - mr1);
                     const float p2 = fast_exp2(sv[u][2] - mr0), p3 = fast_exp2(sv[u][3] - mr1);
-                    ls0 += p0 + p2;
-                    ls1 += p1 + p3;
+                    if constexpr (kVExp) {
+                        ls0 = fmaf(p0, vi_lo[u], fmaf(p2, vi_hi[u], ls0));
+                        ls1 = fmaf(p1, vi_lo[u], fmaf(p3, vi_hi[u], ls1));
+                    } else {
+                        ls0 += p0 + p2;
+                        ls1 += p1 + p3;
+                    }
                     if constexpr (KV8) {  // probabilities times the tokens' V scales, fp16
                         pb[u][n][0] = movmatrix_t(pack_f16(p0 * vs_lo[u], p1 * vs_lo[u]));  // tokens 4t, 4t+1
                         pb[u][n][1] = movmatrix_t(pack_f16(p2 * vs_hi[u], p3 * vs_hi[u]));  // tokens 4t+2, 4t+3
