@@ -760,6 +760,9 @@ struct SmemLayout {
     static_assert(CPS == 1 || CPS * (bytes + 1024) <= 233472, "shared memory budget of the CTAs on one SM");
 };
 
+// What a block-table entry outside the pool reads on an fp8 cache, which has no tensor map to fall outside of.
+__device__ __align__(16) const uint8_t g_zero_block[kBlk8Bytes] = {};
+
 // ------------------------------------------------------------------ the kernel
 // MT: several query tokens per sequence (paged, bf16 or fp8, T <= kMaxNewMT): the query rows of a
 // KV head are (token t, head h) pairs r = t G + h, one column of the products each; row t
@@ -1231,11 +1234,12 @@ __global__ void __launch_bounds__(kThreads, CPS)
                     bulk_load(q_tile(stg) + GP * kD * 2 + 4 * kD, p.rope_cos + row, kD * 2, bar);
                     bulk_load(q_tile(stg) + GP * kD * 2 + 6 * kD, p.rope_sin + row, kD * 2, bar);
                 }
-                if constexpr (KV8) {  // the whole block in one copy (a bad page reads block 0)
+                if constexpr (KV8) {  // the whole block in one copy (a bad page reads zeros)
                     const size_t blk = RING ? (static_cast<size_t>(tb) * Hkv + tg) * (p.window / kPage) + tt
-                                            : static_cast<size_t>(tp < 0 ? 0 : tp) * Hkv + tg;
-                    bulk_load_hint(k_tile(stg), reinterpret_cast<const uint8_t *>(p.k_cache) + blk * kBlk8Bytes,
-                                   kBlk8Bytes, bar, policy);
+                                            : static_cast<size_t>(tp) * Hkv + tg;
+                    const uint8_t *src = reinterpret_cast<const uint8_t *>(p.k_cache) + blk * kBlk8Bytes;
+                    if (!RING && tp < 0) src = g_zero_block;
+                    bulk_load_hint(k_tile(stg), src, kBlk8Bytes, bar, policy);
                 } else {
                     int c1, c2;
                     if (RING) { c1 = tt * kPage; c2 = tb * Hkv + tg; }
