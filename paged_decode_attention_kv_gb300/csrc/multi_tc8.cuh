@@ -577,7 +577,9 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             // the block-table entry of the next copy is read one copy early; -2: past the segment's tiles
             auto page_of = [&]() {
                 const int k = wu * kT8Tiles + lane;
-                return lane < kT8Tiles && k < w.keys.ntiles ? __ldg(p.block_table + static_cast<size_t>(w.b) * p.max_pages + w.keys.pt_lo + k) : -2;
+                // (a bad entry must not pass for "past": -1 stands for all negative ones)
+                return lane < kT8Tiles && k < w.keys.ntiles
+                           ? max(-1, __ldg(p.block_table + static_cast<size_t>(w.b) * p.max_pages + w.keys.pt_lo + k)) : -2;
             };
             int page = page_of(), rs = 0;
             uint32_t rs_ph = 1;  // (the first round is free)

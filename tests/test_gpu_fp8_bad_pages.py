@@ -60,3 +60,17 @@ def test_one_token(Hq, Hkv, entry):
                              c.scale, out)
     ref = oracle.decode_paged_fp8(c.q, c.k_new, c.v_new, full, want, c.lens, c.sinks, 0, c.scale)
     check(out.double().cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("T", [4, 16])
+@pytest.mark.parametrize("entry", [-2, -2 ** 31, 2 ** 31 - 1])
+def test_every_entry_outside_the_pool_is_reported(T, entry):
+    m = Multi(3020 + T, 16, 2, [100, 75], [T, T], T)
+    cache, bt, _ = fp8_paged(m, 1)
+    table = bt.copy()
+    table[1, 2] = entry
+    out = torch.empty((2, T, 16, 64), dtype=torch.bfloat16, device=DEV)
+    da.decode_attn_paged_fp8_multi(dev_bits(m.q), dev_bits(m.k_new), dev_bits(m.v_new), to_dev(cache), dev(table), dev(m.lens), None, 0,
+                                   m.c.scale, out, q_lens=dev(m.n))
+    assert da.decode_attn_device_status() == da.DA_STATUS_BAD_PAGE
+    assert out.isfinite().all()
