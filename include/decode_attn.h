@@ -452,6 +452,7 @@ DA_API int qk_norm_rope(const da_rows *q, const da_rows *k, const da_rows *v, in
  *                 decode_attn_paged (window ignored). NULL: ring kv_cache [B, Hkv, window / 16, 2176],
  *                 which keeps the last `window` of them; window % 16 == 0
  *   scale_rule    DA_FP8_SCALE_DIVIDE (the bytes of decode_attn_paged_fp8) or _RECIPROCAL
+ *   q_tokens      T, at least 1
  *   s             batch, num_kv_heads and head_dim count
  * Only the new tokens' bytes are written. q_lens[b] outside 0 .. min(T, L), a length outside
  * 0 .. max_seq_len: DA_STATUS_BAD_SEQ_LEN, nothing written for that sequence; a page outside the
@@ -490,7 +491,7 @@ DA_API int kv_read_fp8(const void *kv_cache, const int32_t *block_table, const i
  * outside a sequence's [window start, length) may hold anything; the cached and the new tokens of
  * a sequence must be finite (a NaN may reach rows of its sequence that do not attend it).
  * One launch for up to four tokens with T * G <= 32, else two, and one more where a few blocks of
- * query rows share the whole GPU. q_tokens up to 4096. Multi-token workspace
+ * query rows share the whole GPU. q_tokens 1 to 4096. Multi-token workspace
  * (decode_attn_paged_fp8_multi_workspace_bytes, decode_attn_multi_reserve). The ring form is not
  * there: a call's early tokens attend cells that its later ones overwrite.
  */

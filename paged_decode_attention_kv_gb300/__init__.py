@@ -630,6 +630,8 @@ def _token_rows(name, x, heads, dev):
         if len(shape) == 3 and shape[2] == 64 and shape[1] == heads and step[2] == 1 and (step[1] == 64 or heads == 1):
             return shape[0], step[0]
         if len(shape) > 3 and shape[-1] == 64 and shape[-2] == heads and step[-1] == 1 and (step[-2] == 64 or heads == 1):
+            if 0 in shape:  # (of no row there are no steps to compare)
+                return 0, heads * 64
             tokens, token = 1, None
             for n, st in zip(reversed(shape[:-2]), reversed(step[:-2])):
                 if n == 1:
@@ -640,7 +642,7 @@ def _token_rows(name, x, heads, dev):
                     break
                 tokens *= n
             else:
-                return tokens if 0 not in shape else 0, heads * 64 if token is None else token
+                return tokens, heads * 64 if token is None else token
     if x.is_cuda and x.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
     raise ValueError(f"{name} must be CUDA bf16 rows [..., {heads}, 64], contiguous within a token and evenly spaced, "
@@ -731,14 +733,14 @@ def kv_append_fp8(k_new, v_new, kv_cache, seq_lens, block_table=None, q_lens=Non
                   scale_rule=DA_FP8_SCALE_DIVIDE, stream=None):
     """New tokens quantised into fp8 blocks: k_new, v_new bf16 [B, T, Hkv, 64] (or [B, Hkv, 64]: one each), of which the
     first q_lens[b] (or T) of sequence b go to the positions before seq_lens[b]. Paged with a block table
-    (kv_cache as in decode_attn_paged_fp8), else a ring (as in decode_attn_ring_fp8)."""
+    (kv_cache as in decode_attn_paged_fp8), else a ring (as in decode_attn_ring_fp8). T may be 0: nothing is done."""
     dev = torch.cuda.current_device()
     kp, bp, lp, B, Hkv, window, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
     T = k_new.shape[1] if k_new.dim() == 4 else 1
     rows = (B, T, Hkv, 64) if k_new.dim() == 4 else (B, Hkv, 64)
     knp, vnp = _tensor("k_new", k_new, torch.bfloat16, rows, dev), _tensor("v_new", v_new, torch.bfloat16, rows, dev)
     qlp = None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev)
-    if B == 0:  # (an empty tensor has no address)
+    if B == 0 or T == 0:  # (an empty tensor has no address)
         return
     _check(load_library().kv_append_fp8(
         knp, vnp, kp, bp, lp, qlp, window, int(scale_rule),
@@ -766,7 +768,7 @@ def decode_attn_paged_fp8_multi(q, k_new, v_new, kv_cache, block_table, seq_lens
                                 max_seq_len=None, scale_rule=DA_FP8_SCALE_DIVIDE, stream=None):
     """decode_attn_paged_multi over an fp8 cache (kv_cache as in decode_attn_paged_fp8): the new tokens are quantised
     into their pages, and attended as they are cached. max_seq_len (default: what the block table can hold) sizes
-    the workspace and the split of long sequences."""
+    the workspace and the split of long sequences. T may be 0 (an empty chunk): nothing is done."""
     dev = torch.cuda.current_device()
     if q.dim() != 4 or block_table is None or k_new is None:
         raise ValueError("q is [B, T, Hq, 64]; k_new, v_new and the block table are required")
@@ -774,7 +776,7 @@ def decode_attn_paged_fp8_multi(q, k_new, v_new, kv_cache, block_table, seq_lens
     T = q.shape[1]
     qp, knp, vnp, sp, op, Hq = _new_tensors(q, k_new, v_new, sinks, out, (B, T), Hkv, dev)
     qlp = None if q_lens is None else _tensor("q_lens", q_lens, torch.int32, (B,), dev)
-    if B == 0:
+    if B == 0 or T == 0:
         return out
     _check(load_library().decode_attn_paged_fp8_multi(
         qp, knp, vnp, kp, bp, lp, qlp, sp, int(window),
