@@ -658,7 +658,7 @@ def _pair_axes(axes, sections, interleaved):
             raise ValueError("positions of several axes need sections")
         return None
     left = [int(n) for n in sections]
-    if len(left) != axes or min(left) < 0 or sum(left) != 32:
+    if not left or len(left) != axes or min(left) < 0 or sum(left) != 32:
         raise ValueError(f"sections {sections} must be {axes} counts of pairs that add up to 32")
     if not interleaved:
         return bytes(a for a, n in enumerate(left) for _ in range(n))
@@ -676,8 +676,8 @@ def qk_norm_rope(q, k, positions, rope_cos, rope_sin, q_out, k_out, q_weight=Non
     """The RMS norm of every query and key head (q_weight, k_weight fp32 [64]; None: no norm) and the rotary embedding
     at the given positions, in one pass; value rows (v, v_out) are copied along. q, k, v: bf16 [..., heads, 64], any
     views whose tokens are evenly spaced (slices of one packed projection); the outputs likewise, or the inputs
-    themselves. positions int32, one per token, or [axes, tokens] with sections (pairs per axis, 32 in all, in blocks
-    or interleaved: the axes taking turns); rope_cos / rope_sin fp32 [max_position, 32]. Returns q_out, k_out."""
+    themselves. positions int32, one per token, or [axes, tokens] (tokens also in the rows' leading dimensions) with
+    sections (pairs per axis, 32 in all, in blocks or interleaved: the axes taking turns); rope_cos / rope_sin fp32 [max_position, 32]. Returns q_out, k_out."""
     dev = torch.cuda.current_device()
     lead = q.shape[:-2]
     if len(lead) == 0 or len(k.shape) < 3:
@@ -699,9 +699,12 @@ def qk_norm_rope(q, k, positions, rope_cos, rope_sin, q_out, k_out, q_weight=Non
         axes = 1
         pp = _tensor("positions", positions, torch.int32, lead if len(lead) == positions.dim() else (tokens,), dev)
     else:
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        pp = _tensor("positions", positions, torch.int32, (axes, tokens) if positions.dim() == 2 else (tokens,), dev)
         sections = tuple(sections)
+        axes = len(sections)
+        want = (axes, *lead) if positions.dim() == 1 + len(lead) else (axes, tokens)
+        if axes == 1 and positions.shape in (lead, (tokens,)):
+            want = positions.shape
+        pp = _tensor("positions", positions, torch.int32, want, dev)
     most = rope_cos.shape[0] if rope_cos.dim() else 0
     _check((_lib or load_library()).qk_norm_rope(
         q_rows, k_rows, v_rows, tokens, Hq, Hkv, 64, pp, axes, _pair_axes(axes, sections, bool(interleaved)),
