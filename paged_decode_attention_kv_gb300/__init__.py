@@ -628,7 +628,7 @@ def _token_rows(name, x, heads, dev):
     if x.dtype is torch.bfloat16 and x.get_device() == dev:  # (-1: not on a GPU)
         shape, step = x.shape, x.stride()
         if len(shape) == 3 and shape[2] == 64 and shape[1] == heads and step[2] == 1 and (step[1] == 64 or heads == 1):
-            return shape[0], step[0]
+            return shape[0], step[0] if shape[0] > 1 else heads * 64  # (one row's step leads nowhere: it may be anything)
         if len(shape) > 3 and shape[-1] == 64 and shape[-2] == heads and step[-1] == 1 and (step[-2] == 64 or heads == 1):
             if 0 in shape:  # (of no row there are no steps to compare)
                 return 0, heads * 64
