@@ -582,13 +582,19 @@ DA_API int decode_attn_stream_release(void *stream);
 /*
  * decode_attn_test_expire_wait -- a testing aid for the bounded-wait failure path. It arms a
  * one-shot: in the next one-token attention call (decode_attn_paged / _ring and their
- * _rope / _fp8 forms), the first worker gives up at its first tile wait from its tile
- * `tile` on (0-based, counted over that worker's share of the tiles), after that tile has
- * landed, exactly as if the bounded wait had expired (a worker takes its tiles two at a
- * time, one wait per pass; if its share has no wait at or after `tile`, nothing happens).
+ * _rope / _fp8 forms) or decode_attn_paged_fp8_multi call, the first worker gives up at its
+ * first tile wait from its tile `tile` on (0-based, counted over that worker's share of the
+ * tiles), after that tile has landed, exactly as if the bounded wait had expired (a worker takes
+ * its tiles two at a time, one wait per pass; if its share has no wait at or after `tile`, nothing
+ * happens).
  * The call then records DA_STATUS_TIMEOUT, its output is garbage, no copy is left in
- * flight, and the library's arrival counters are back at zero for the next call. tile < 0
- * disarms. No GPU fault, trap or hang is involved. Returns DA_OK.
+ * flight, and the library's arrival counters are back at zero for the next call. Where
+ * decode_attn_paged_fp8_multi runs on tcgen05 (beyond four tokens or T * G = 32), `tile` is
+ * 8 i + role: of the first CTA, a warp with query rows (role 0), one that makes operands (1), the
+ * one that copies (2), that issues products (3) or that loads query rows (4) gives up at its unit
+ * of 64 keys i (1, 2) or its block of query rows i, and the warps that wait for it run into their
+ * limit of about two seconds. tile < 0 disarms. No GPU fault, trap or hang is involved. Returns
+ * DA_OK.
  */
 DA_API int decode_attn_test_expire_wait(int tile);
 

@@ -470,8 +470,9 @@ def decode_attn_set_early_inputs(level: int) -> int:
 
 
 def decode_attn_test_expire_wait(tile: int):
-    """Testing aid: the next one-token attention call gives up at its first worker's tile
-    wait number `tile` (after the tile landed) as if the wait had expired; < 0 disarms."""
+    """Testing aid: the next one-token attention call (or several-token call on an fp8 cache; the header
+    has its numbers) gives up at its first worker's tile wait number `tile` (after the tile landed) as if
+    the wait had expired; < 0 disarms."""
     _check(load_library().decode_attn_test_expire_wait(int(tile)))
 
 

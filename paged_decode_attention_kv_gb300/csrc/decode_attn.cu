@@ -2519,8 +2519,8 @@ int prepare_workspace(int dev, int G, cudaStream_t stream, float **part, int **c
     return DA_OK;
 }
 
-// Testing aid (decode_attn_test_expire_wait): the tile wait at which the next one-token
-// call's first worker gives up; -1 = none. Taken (and cleared) by that call.
+// Testing aid (decode_attn_test_expire_wait): the tile wait at which the first worker of the next one-token
+// call (or several-token call on an fp8 cache) gives up; -1 = none. Taken (and cleared) by that call.
 std::atomic<int> g_expire_next{-1};
 // decode_attn_set_early_inputs: what is read before the wait for the previous kernel
 std::atomic<int> g_early_inputs{0};
@@ -3210,6 +3210,7 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
     if (rc != DA_OK) return rc;
     if (kT8CtasPerSm * sm_count(dev) * 4 > kT8Counters) return DA_ERR_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    const int expire = g_expire_next.exchange(-1);
     const MultiPlan m = multi_fp8_plan(s, T, window, max_seq_len, sm_count(dev));
     if (static_cast<long long>(s.batch) * m.row_blocks > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
     void *ws = nullptr;
@@ -3222,6 +3223,7 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
         Params dp = multi_decode_params(q, k_new, v_new, kv_cache, nullptr, block_table, seq_lens, q_lens, sinks, window,
                                         scale, out, s, T, max_pages, num_pages, max_seq_len, m, ws, dev, nullptr);
         dp.fp8_rule = scale_rule;
+        dp.expire_at = expire;
         CUtensorMap none;
         memset(&none, 0, sizeof none);
         return m.rows == 8    ? launch_attn<1, false, false, true, 1, true>(none, none, dp, dev, stream)
@@ -3263,7 +3265,7 @@ int run_multi_fp8(const void *q, const void *k_new, const void *v_new, void *kv_
     prm.part = reinterpret_cast<float *>(static_cast<char *>(ws) + m.counter_bytes);
     prm.defer = m.defer ? 1 : 0;
     const unsigned grid = static_cast<unsigned>(kT8CtasPerSm * sm_count(dev));
-    rc = launch_pdl(multi_tc8_kernel, dim3(grid), kT8Threads, kT8Smem, stream, prm, static_cast<const uint8_t *>(kv_cache));
+    rc = launch_pdl(multi_tc8_kernel, dim3(grid), kT8Threads, kT8Smem, stream, prm, static_cast<const uint8_t *>(kv_cache), expire);
     if (rc != DA_OK || !m.defer) return rc;
     return launch_pdl(t8_combine_kernel,
                       dim3(static_cast<unsigned>(m.row_blocks * 4), static_cast<unsigned>(s.num_kv_heads),

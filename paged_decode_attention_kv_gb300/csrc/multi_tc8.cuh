@@ -342,8 +342,11 @@ __device__ __noinline__ void t8_fold(const MultiParams &p, int c0, int k0, int c
     }
 }
 
+// expire: -1, or 8 i + role: the first CTA's warp of that role (0: row warp 0, 1: tile 0 of the team that has unit i, 2:
+// copies, 3: MMAs, 4: query rows, first half) gives up at unit i (1, 2) or at segment i, as if its wait there had expired
+// (decode_attn_test_expire_wait). Looked at outside the loops over units: looks in them took 7 to 10% of a call.
 __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
-    multi_tc8_kernel(const MultiParams p, const uint8_t *__restrict__ kv) {
+    multi_tc8_kernel(const MultiParams p, const uint8_t *__restrict__ kv, const int expire) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem;                        // [2][128 rows][128 B], 128-byte swizzle
@@ -437,6 +440,10 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
     const uint32_t tm = s_tmem;
     const int units = static_cast<int>(s_before[1] - s_before[0]);
 
+    auto gives_up = [&](int role, int i) { return expire == 8 * i + role && blockIdx.x == 0; };
+    auto units_of = [&](int role) {  // the units that a role goes through: all, or up to where it gives up
+        return expire >= 0 && blockIdx.x == 0 && (expire & 7) == role ? min(units, expire >> 3) : units;
+    };
     bool failed = false;
     if (warp >= 4 && warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -445,7 +452,9 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
         unsigned short *const vfac = reinterpret_cast<unsigned short *>(s_vfac[warp - 4]);
         int st = team % kT8Stages, rs = team % kT8Raw;
         uint32_t st_ph = 1, rs_ph = 0;  // (the first round of stages is free)
-        for (int i = team; i < units; i += 2) {
+        const int all = u == 0 ? units_of(1) : units;
+        failed = all < units && (all & 1) == team;
+        for (int i = team; i < all; i += 2) {
             if (__any_sync(0xffffffffu, !mbar_wait_bounded(raw_full + 8 * rs, rs_ph))) {
                 failed = true;
                 break;
@@ -583,8 +592,10 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             };
             int page = page_of(), rs = 0;
             uint32_t rs_ph = 1;  // (the first round is free)
+            const int all = units_of(2);
+            failed = all < units;
             int i = 0;
-            for (; i < units; ++i) {
+            for (; i < all; ++i) {
                 if (__any_sync(0xffffffffu, !mbar_wait_idle(raw_empty + 8 * rs, rs_ph))) {
                     failed = true;
                     break;
@@ -629,7 +640,8 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             bool more = true;
             for (int k = 0; more; ++k) {
                 const int buf = k & 1;
-                if (k >= 2 && __any_sync(0xffffffffu, !mbar_wait_idle(q_free + 8 * buf, ((k >> 1) - 1) & 1))) {
+                if ((k >= 2 && __any_sync(0xffffffffu, !mbar_wait_idle(q_free + 8 * buf, ((k >> 1) - 1) & 1))) ||
+                    (gives_up(4, k) && warp == 14)) {
                     failed = true;
                     break;
                 }
@@ -682,7 +694,7 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
                     if (leader && seg >= 0) umma_commit(q_free + 8 * (seg & 1));  // the last segment's products are all issued
                     __syncwarp();
                     ++seg;
-                    if (!wait_all(q_full + 8 * (seg & 1), (seg >> 1) & 1)) {
+                    if (!wait_all(q_full + 8 * (seg & 1), (seg >> 1) & 1) || gives_up(3, seg)) {
                         failed = true;
                         break;
                     }
@@ -735,6 +747,10 @@ __global__ void __launch_bounds__(kT8Threads, kT8CtasPerSm)
             bool valid, warp_active;
             int place;  // the row's among its sequence's output rows, or -1
             float sink = -INFINITY;
+            if (warp == 0 && gives_up(0, seg)) {
+                failed = true;
+                break;
+            }
             if (__any_sync(0xffffffffu, !mbar_wait_bounded(q_full + 8 * (seg & 1), (seg >> 1) & 1))) {
                 failed = true;
                 break;
