@@ -3162,9 +3162,7 @@ int run_read_fp8(const void *kv_cache, const int32_t *block_table, const int32_t
                       static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out));
 }
 
-#ifndef DA_T8_DEFER
-#define DA_T8_DEFER 4
-#endif
+constexpr int kT8DeferCtas = 4;  // CTAs per segment from which the fold is a kernel of its own (multi_fp8_plan)
 // How a several-token call over fp8 pages is cut: the decode kernel's several-token form as
 // multi_plan has it (up to four tokens, at most 32 rows per KV head), else multi_tc8_kernel. Of shapes only, like
 // multi_plan. Both sides, us back to back, decode kernel and tcgen05: 32 sequences of 1024 to 8192 tokens, 8 heads per KV
@@ -3184,7 +3182,7 @@ MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, 
     m.chunk = 0;
     // Segments so few that each is spread over four CTAs or more, if they are about equally long: the fold is a kernel of
     // its own. 16 tokens behind 8192, with it / without: 8 segments 30 / 72 us, 32 35 / 46, 72 52 / 56, 152 89 / 82.
-    m.defer = m.groups * DA_T8_DEFER <= static_cast<long long>(kT8CtasPerSm) * sms;
+    m.defer = m.groups * kT8DeferCtas <= static_cast<long long>(kT8CtasPerSm) * sms;
     m.counter_bytes = static_cast<size_t>(kMMaxGroups) * sizeof(int);
     // two slots per CTA, then its counters (not among those that are zero at rest: every call clears them itself)
     m.part_bytes = static_cast<size_t>(kT8CtasPerSm) * sms * 2 * kT8SlotFloats * sizeof(float) + kT8Counters * sizeof(int);

@@ -43,16 +43,10 @@ struct RotateParams {
     unsigned char quads;                     // bit i: the pairs 4 i .. 4 i + 3 are of one axis
 };
 constexpr int kRotThreads = 128;
-#ifndef DA_ROT_AHEAD
-#define DA_ROT_AHEAD 4
-#endif
-constexpr int kRotAhead = DA_ROT_AHEAD;  // eights of rows on their way
-#ifndef DA_ROT_WARPS
-#define DA_ROT_WARPS 16
-#endif
+constexpr int kRotAhead = 4;  // eights of rows on their way
 // Warps per SM that a token's rows are spread over where there are few tokens: with 8 / 16 / 32, 64 tokens of 80 rows took
 // 6.2 / 6.2 / 8.1 us (events around one call), 1024 12.3 each, 2432 16.4 / 16.4 / 18.4.
-constexpr int kRotWarps = DA_ROT_WARPS;
+constexpr int kRotWarps = 16;
 
 // Rows h0 + lane / 4, + 8, .. below h1 of one token's query or key heads (in and out at head 0, this lane's first
 // element). c, s: the lane's pairs' angles, two pairs each; w: the heads' norm weights from this lane's first element on.

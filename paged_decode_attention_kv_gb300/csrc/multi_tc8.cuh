@@ -60,14 +60,8 @@
 // (the query buffer is then held to the segment's end: 297 us instead of 268 for the prompts), registers 96 / 56 / 48,
 // 88 / 48 / 72, 80 / 56 / 64, 104 / 48 / 56, all 64 scores in registers (they spill).
 constexpr int kT8Rows = 128, kT8Keys = 64, kT8Tiles = kT8Keys / kPage;
-#ifndef DA_T8_STAGES
-#define DA_T8_STAGES 3
-#endif
-#ifndef DA_T8_RAW
-#define DA_T8_RAW 2
-#endif
-constexpr int kT8Stages = DA_T8_STAGES;  // blocks of K' and V'
-constexpr int kT8Raw = DA_T8_RAW;        // units of fp8 blocks in flight
+constexpr int kT8Stages = 3;  // blocks of K' and V'
+constexpr int kT8Raw = 2;     // units of fp8 blocks in flight
 // An even number: every raw block is always the same team's. With three, a team could wait for its unit's
 // parity on a barrier whose last unit, the other team's, had not landed yet, and take the phase before for its own.
 // (The stages are safe with any number: a team's unit i - 2 has seen PV_{i-5} done, so that the phase before the one
@@ -93,16 +87,10 @@ constexpr int kT8Counters = 4 * kT8CtasPerSm * kMaxSms;  // arrivals at a shared
 // units as the others had several times their segments. With 3 / 4 / 5 / 6, four prompts took 237 / 230 / 232 / 235 us,
 // 64 sequences x 16 tokens 150 / 148 / 150 / 149, slots behind a window 75 each, a 512-token chunk 123 each; with 0
 // instead of 6, when a start cost more than now, 333 instead of 268, 165 instead of 156 and 82 instead of 78.
-#ifndef DA_T8_SEG
-#define DA_T8_SEG 4
-#endif
-constexpr int kT8SegCost = DA_T8_SEG;
+constexpr int kT8SegCost = 4;
 // A CTA's share at least, where there is so little: with 4 / 8 / 10, 36 short slots (9 to 300 tokens) took 35 / 30 / 32 us,
 // 16 tokens behind 1024 30 / 31 / 28, behind 4096 28 / 27 / 28, four prompts of 100 to 300 42 each.
-#ifndef DA_T8_MIN
-#define DA_T8_MIN 8
-#endif
-constexpr int kT8MinCost = DA_T8_MIN;
+constexpr int kT8MinCost = 8;
 constexpr size_t kT8SlotFloats = static_cast<size_t>(kT8Rows) * (2 + kD);
 
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
