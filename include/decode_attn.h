@@ -171,8 +171,11 @@ DA_API int decode_attn_ring_rope(const void *q, const void *k_new, const void *v
  * The new token is quantised when it is appended: scale = max_d |x_d| / 448 in fp32 (1 when
  * the row is all zero), code_d = the e4m3 value nearest to x_d / scale (fp32 division),
  * ties to even, saturating at +-448; its K row, V column and both scales are written.
- * Scores and the PV product run in fp16 on tensor cores: |q| must stay below 65504.
- * Other arguments, the status and the error behaviour as in decode_attn_paged / _ring.
+ * Scores and the PV product run in fp16 on tensor cores: |q| must stay below 65504, and
+ * probabilities enter the product times their tokens' V scales: scales above 2^8 (V of 1e5) may
+ * give infinities, below 2^-18 (V of 2e-3) bits are lost. decode_attn_paged_fp8_multi takes V of
+ * any size, also for one token. Other arguments, the status and the error behaviour as in
+ * decode_attn_paged / _ring.
  */
 DA_API int decode_attn_paged_fp8(const void *q, const void *k_new, const void *v_new,
                                  void *kv_cache, const int32_t *block_table,
@@ -455,8 +458,9 @@ DA_API int qk_norm_rope(const da_rows *q, const da_rows *k, const da_rows *v, in
  *   q_tokens      T, at least 1
  *   s             batch, num_kv_heads and head_dim count
  * Only the new tokens' bytes are written. q_lens[b] outside 0 .. min(T, L), a length outside
- * 0 .. max_seq_len: DA_STATUS_BAD_SEQ_LEN, nothing written for that sequence; a page outside the
- * pool: DA_STATUS_BAD_PAGE, its tokens skipped. One launch, no workspace.
+ * 0 .. max_seq_len: DA_STATUS_BAD_SEQ_LEN, nothing written for that sequence (L = 0 is an inactive
+ * slot, whatever the count up to T); a page outside the pool: DA_STATUS_BAD_PAGE, its tokens
+ * skipped. One launch, no workspace.
  */
 DA_API int kv_append_fp8(const void *k_new, const void *v_new, void *kv_cache,
                          const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
@@ -486,10 +490,11 @@ DA_API int kv_read_fp8(const void *kv_cache, const int32_t *block_table, const i
  * probabilities, times powers of two: V scales of 2^-60 .. 2^60 and K scales of 2^-100 .. 2^100
  * give the same digits whatever their size (smaller ones lose bits, larger ones may give
  * infinities). Up to four tokens with T * G <= 32, each token has its own powers. Beyond, the 16
- * tokens of a page share them: one whose K or V scale is below 2^-20 of the largest in its page,
- * attended by the row or not, loses bits (rows of zeros have scale 1, but do not count). Cells
- * outside a sequence's [window start, length) may hold anything; the cached and the new tokens of
- * a sequence must be finite (a NaN may reach rows of its sequence that do not attend it).
+ * tokens of a page share them: a token whose K scale is below 2^-20 of the largest in its page, or
+ * its V scale of the largest in any page that the row attends, loses bits, also where the larger
+ * one is not attended (rows of zeros have scale 1, but do not count). Cells outside a sequence's
+ * [window start, length) may hold anything; the cached and the new tokens of a sequence must be
+ * finite (a NaN may reach rows of its sequence that do not attend it).
  * One launch for up to four tokens with T * G <= 32, else two, and one more where a few blocks of
  * query rows share the whole GPU. q_tokens 1 to 4096. Multi-token workspace
  * (decode_attn_paged_fp8_multi_workspace_bytes, decode_attn_multi_reserve). The ring form is not

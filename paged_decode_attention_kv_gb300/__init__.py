@@ -754,7 +754,8 @@ def kv_append_fp8(k_new, v_new, kv_cache, seq_lens, block_table=None, q_lens=Non
 def kv_read_fp8(kv_cache, seq_lens, k_out, v_out, block_table=None, starts=None, max_seq_len=None, stream=None):
     """Cached positions as bf16: position starts[b] + i (starts None: i) of sequence b to row i of k_out and v_out
     [B, rows, Hkv, 64], as far as seq_lens[b] and the rows go; the other rows stay as they are. Paged with a block
-    table, else a ring (which holds the last window positions)."""
+    table, else a ring, which holds the last window positions: of a longer sequence give starts, for one that reaches
+    further back (None does) is DA_STATUS_BAD_SEQ_LEN, and none of its rows is written."""
     dev = torch.cuda.current_device()
     kp, bp, lp, B, Hkv, window, sizes = _blocks(kv_cache, block_table, seq_lens, max_seq_len, dev)
     rows = k_out.shape[1] if k_out.dim() > 1 else 0

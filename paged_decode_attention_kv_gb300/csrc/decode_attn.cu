@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
     // probability, so that V of any size (scales of 2^-60 .. 2^60) gives the same digits:
     //     P_j = fp16(2^(s_j + F_j - m) mant_j),  O = sum P_j code_j,  l = sum 2^(s_j + F_j - m) 2^-F_j,
     // with m the running maximum of s_j + F_j, the largest contribution instead of the largest probability.
-    // (With the scales as they are in fp16, as the one-token calls have them, V of 1e-3 lost bits and V of 1e5 overflowed.)
+    // (Scales as they are, as in the one-token calls: V of 1e-3 lost bits, 1e5 overflowed; 4 tokens x 32 91 us, now 94.)
     constexpr bool kVExp = KV8 && MT;
     constexpr int kVMaxExp = 60;  // (also of a token that has no scale: fp32 holds probabilities that far apart)
     // fp8: the power of two the V scales carry (taken out when a segment closes)
@@ -3166,8 +3166,8 @@ constexpr int kT8DeferCtas = 4;  // CTAs per segment from which the fold is a ke
 // How a several-token call over fp8 pages is cut: the decode kernel's several-token form as
 // multi_plan has it (up to four tokens, at most 32 rows per KV head), else multi_tc8_kernel. Of shapes only, like
 // multi_plan. Both sides, us back to back, decode kernel and tcgen05: 32 sequences of 1024 to 8192 tokens, 8 heads per KV
-// head, 4 tokens 91 and 106, 3 tokens 88 and 105, 2 tokens 66 and 105; 2 tokens of 16 heads 87 and 106; 64 sequences, 4
-// tokens 139 and 166; 4 sequences 30 and 41; 4 tokens behind 131072 69 and 77.
+// head, 4 tokens 95 and 106, 3 tokens 91 and 105, 2 tokens 71 and 105; 2 tokens of 16 heads of 4 KV heads 53 and 67; 64
+// sequences, 4 tokens 146 and 166; 4 sequences of 300 to 1024 23 and 32; 4 tokens behind 131072 72 and 78.
 MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, int sms) {
     MultiPlan m = multi_plan(s, T, false, window, max_seq_len, sms);
     if (m.dec) return m;
@@ -3180,8 +3180,8 @@ MultiPlan multi_fp8_plan(const da_shape &s, int T, int window, int max_seq_len, 
     m.groups = static_cast<long long>(s.batch) * s.num_kv_heads * m.row_blocks;
     m.splits = 1;
     m.chunk = 0;
-    // Segments so few that each is spread over four CTAs or more, if they are about equally long: the fold is a kernel of
-    // its own. 16 tokens behind 8192, with it / without: 8 segments 30 / 72 us, 32 35 / 46, 72 52 / 56, 152 89 / 82.
+    // Segments so few that each is spread over four CTAs or more, if all live and about equally long: the fold is a
+    // kernel of its own. 16 tokens behind 8192, with it / without: 8 segments 30 / 72 us, 32 35 / 46, 72 52 / 56, 152 89 / 82.
     m.defer = m.groups * kT8DeferCtas <= static_cast<long long>(kT8CtasPerSm) * sms;
     m.counter_bytes = static_cast<size_t>(kMMaxGroups) * sizeof(int);
     // two slots per CTA, then its counters (not among those that are zero at rest: every call clears them itself)

@@ -51,14 +51,14 @@
 //
 // What bounds it: the ring S issued -> scores -> probabilities -> P stored -> PV issued, and behind it the stage that PV
 // frees and the teams' next operands: about 2000 cycles a unit with two CTAs on an SM, 1400 of them the rows' work. The SM
-// issues 54% of the time (2500 instructions a unit: rows 1090, teams 690, waits, copies and MMAs the rest); the tensor
+// issues 52% of the time (2470 instructions a unit: rows 1090, teams 700, waits, copies and MMAs the rest); the tensor
 // cores work 21% of it, the exponentials' unit 256 cycles a unit. A segment's start and end are worth about 4 units.
-// 64 sequences of 1024 to 8192 tokens, 16 tokens each: 147 us (2.2 TB/s, 508 TFLOP/s); 512 tokens behind 7680: 123 us
-// (542 TFLOP/s); four prompts of 1201 to 2048: 231 us; 16 tokens behind 65536 of 19 sequences: 643 TFLOP/s; G = 8, 64
-// query heads throughout. Tried, without a gain or slower: four stages, more raw units, S and PV issued by two warps, S_i
-// issued before PV_{i-2} (the stage comes free later: 171 us instead of 156), outputs through shared memory in whole lines
-// (the query buffer is then held to the segment's end: 297 us instead of 268 for the prompts), registers 96 / 56 / 48,
-// 88 / 48 / 72, 80 / 56 / 64, 104 / 48 / 56, all 64 scores in registers (they spill).
+// 64 sequences of 1024 to 8192 tokens, 16 tokens each: 148 us (2.2 TB/s, 503 TFLOP/s); 512 tokens behind 7680: 124 us
+// (537 TFLOP/s); four prompts of 1201 to 2048: 236 us; 16 tokens behind 65536 of 19 sequences: 635 TFLOP/s; G = 8, 64
+// query heads throughout (the look for rows of zeros: 1 to 2% of it). Tried, without a gain or slower: four stages, more raw
+// units, S and PV by two warps, S_i before PV_{i-2} (the stage comes free later: 171 us instead of 156), outputs in whole
+// lines through shared memory (the query buffer is then held to the segment's end: 297 us instead of 268 for the prompts),
+// registers 96 / 56 / 48, 88 / 48 / 72, 80 / 56 / 64, 104 / 48 / 56, all 64 scores in registers (they spill).
 constexpr int kT8Rows = 128, kT8Keys = 64, kT8Tiles = kT8Keys / kPage;
 constexpr int kT8Stages = 3;  // blocks of K' and V'
 constexpr int kT8Raw = 2;     // units of fp8 blocks in flight
