@@ -89,3 +89,18 @@ def test_split_sequences_of_very_small_and_large_values():
     check(m)
     check(m, sinks=False)
     check(m, window=3000)
+
+
+@pytest.mark.parametrize("T", [1, 4, 16, 150])
+@pytest.mark.parametrize("power", [-50, 66])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_the_ends_of_the_range_on_both_routes(T, power, zeros):
+    """Scales of about 2^-59 to 2^-57, and up to 2^60."""
+    m = Multi(5000 + T, 16, 2, [T, T + 40, T + 700], [T] * 3, T)
+    m.c.hist_v[...] = scaled(m.c.hist_v, power)
+    m.v_new[...] = scaled(m.v_new, power)
+    if zeros:
+        set_rows(m, "v", lambda b: range(3, 900, 5), 0)
+        set_rows(m, "v", lambda b: range(32, 96), 0)
+    check(m)
+    check(m, window=50, sinks=False)
